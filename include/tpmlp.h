@@ -306,6 +306,114 @@ tpmlp_status tpmlp_sp_backward(const tpmlp_dims* dims, const tpmlp_sp_params* sp
                                void* const* dA_shards, void* db1,
                                void* const* dB_shards, void* db2, void* stream);
 
+/* ---- 8-bit linear layers ------------------------------------------------------
+ * The tensor-parallel linear layers on 8-bit floating-point operands with one
+ * fp32 scale for each group of 128 values ("blocks of 128"), sums in fp32:
+ *
+ *   Y[m, n] = b[n] + sum_kb sx[kb, m] sw[kb, n / 128] sum_{k in kb} xq[m, k] wq[k, n]
+ *
+ * over K blocks kb of 128 input features.  Half the weight bytes of bf16 when
+ * few tokens are decoded, twice its tensor rate when there are many.
+ *
+ * Quantisation of a group G of bf16 values x:
+ *   s = the smallest power of two with max |x| <= s * top, at least 2^-119
+ *   q = x / s (exact) rounded to nearest even
+ * top = 448 for e4m3, 57344 for e5m2.  A group that holds an infinity or a NaN
+ * gets s = NaN and q = 0, so what is computed from it is NaN.  The products
+ * take any finite scales (a scale of a matrix quantised elsewhere need not be
+ * a power of two), as long as the product of the two scales of a block is
+ * finite and, to count, at least 2^-149 in fp32.
+ *
+ * Layouts, for a matrix [R, C] row-major (R tokens or input features):
+ *   q         8-bit [R, C], C a multiple of 16
+ *   rows      groups of 128 along a row:    s fp32 [ceil(C/128), ld], ld >= R
+ *   columns   groups of 128 along a column: s fp32 [ceil(R/128), C]
+ *   weight    blocks of 128 x 128:          s fp32 [ceil(R/128), ceil(C/128)]
+ * Conventions, chunking, errors and workspace rules as for the bf16 linear
+ * layers, with features and shards multiples of 16 (else
+ * TPMLP_ERR_UNSUPPORTED). */
+typedef enum {
+    TPMLP_FP8_E4M3 = 0, /* 4 exponent bits, 3 mantissa bits, no infinities */
+    TPMLP_FP8_E5M2 = 1  /* 5 exponent bits, 2 mantissa bits */
+} tpmlp_fp8_format;
+
+/* `parts` matrices [rows, cols] of the same shape, quantised in one launch. */
+typedef struct {
+    int64_t rows, cols;   /* of each part */
+    int64_t scale_ld;     /* leading dimension (floats) of the row scales, >= rows */
+    int32_t parts;        /* 1..8 */
+    int32_t rows_format;  /* tpmlp_fp8_format of q_rows */
+    int32_t cols_format;  /* and of q_cols */
+} tpmlp_fp8_quant;
+
+/* Formats of a linear layer's operands. */
+typedef struct {
+    int32_t x, w, dy;
+} tpmlp_fp8_formats;
+
+/* Quantise activations by rows, by columns, or both in one read of src (bf16).
+ * src, q_rows, s_rows, q_cols, s_cols: host arrays of `parts` device pointers;
+ * the row pair or the column pair may be NULL, not both.  Parts may be the
+ * shards of a tensor (each with outputs of its own) or the token chunks of one
+ * [T, cols] matrix: then part j of Tc = T / parts rows writes
+ *   q + j Tc cols,  s_rows + j Tc (scale_ld = T),  s_cols + j (Tc / 128) cols,
+ * which gathers the chunks; Tc must then be a multiple of 128. */
+tpmlp_status tpmlp_fp8_quantize(const tpmlp_fp8_quant* quant, const void* const* src,
+                                void* const* q_rows, void* const* s_rows, void* const* q_cols,
+                                void* const* s_cols, void* stream);
+
+/* Quantise one weight shard W [in, out] bf16 in 128 x 128 blocks. */
+tpmlp_status tpmlp_fp8_quantize_weight(const void* W, int64_t in, int64_t out, int format, void* q,
+                                       void* s, void* stream);
+
+/* Bytes of scratch workspace any 8-bit linear call with these dims needs. */
+size_t tpmlp_fp8_linear_workspace_bytes(const tpmlp_linear_dims* dims);
+
+/* Column parallel.  Forward:  Y_i = X.W_i + b[i*oi:(i+1)*oi]
+ *   Xq, Xs     X [T, in] by rows (one matrix; quantising gathered the chunks)
+ *   Wq, Ws     [t] shards [in, oi] in blocks
+ *   b          [out] bf16;  Y_shards [t] of [T, oi] bf16 (output)
+ * Backward for upstream dY_i (bf16, quantised here by rows and by columns in
+ * the format formats->dy):
+ *   dX = sum_i dY_i.W_i^T (bf16, seq_chunks chunks), dW_i = X^T.dY_i (fp32),
+ *   db = column sums of the bf16 dY (fp32)
+ *   Xq, Xs     X [T, in] by columns, kept from the forward pass
+ * With T = 0 the forward does nothing and the backward zeroes dW and db. */
+tpmlp_status tpmlp_fp8_column_linear_forward(const tpmlp_linear_dims* dims,
+                                             const tpmlp_fp8_formats* formats, const void* Xq,
+                                             const void* Xs, const void* const* Wq_shards,
+                                             const void* const* Ws_shards, const void* b,
+                                             void* const* Y_shards, void* workspace, void* stream);
+tpmlp_status tpmlp_fp8_column_linear_backward(const tpmlp_linear_dims* dims,
+                                              const tpmlp_fp8_formats* formats,
+                                              const void* const* dY_shards, const void* Xq,
+                                              const void* Xs, const void* const* Wq_shards,
+                                              const void* const* Ws_shards, void* const* dX,
+                                              void* const* dW_shards, void* db, void* workspace,
+                                              void* stream);
+
+/* Row parallel.  Forward:  Z = (sum_i X_i.W_i) + b
+ *   Xq, Xs     [t] shards X_i [T, ii] by rows;  Wq, Ws [t] shards [ii, out]
+ *   b          [out] bf16;  Z seq_chunks chunks of [Tc, out] bf16 (output)
+ * Backward for upstream dZ (seq_chunks chunks, bf16):
+ *   dX_i = dZ.W_i^T (bf16 [T, ii]), dW_i = X_i^T.dZ (fp32 [ii, out]), db (fp32)
+ *   Xq, Xs     [t] shards X_i [T, ii] by columns, kept from the forward pass */
+tpmlp_status tpmlp_fp8_row_linear_forward(const tpmlp_linear_dims* dims,
+                                          const tpmlp_fp8_formats* formats,
+                                          const void* const* Xq_shards,
+                                          const void* const* Xs_shards,
+                                          const void* const* Wq_shards,
+                                          const void* const* Ws_shards, const void* b,
+                                          void* const* Z, void* workspace, void* stream);
+tpmlp_status tpmlp_fp8_row_linear_backward(const tpmlp_linear_dims* dims,
+                                           const tpmlp_fp8_formats* formats,
+                                           const void* const* dZ, const void* const* Xq_shards,
+                                           const void* const* Xs_shards,
+                                           const void* const* Wq_shards,
+                                           const void* const* Ws_shards, void* const* dX_shards,
+                                           void* const* dW_shards, void* db, void* workspace,
+                                           void* stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* tpmlp_status_string(tpmlp_status s);
 
@@ -442,13 +550,13 @@ enum {
     TPMLP_KERNEL_WGRAD_B = 4,     /* dB_i = H_i^T.dZ */
     TPMLP_KERNEL_WGRAD_A = 5,     /* dA_i = X^T.dY_i */
     TPMLP_KERNEL_BIAS_GRAD = 6,   /* db1, db2, linear db column sums (all launches) */
-    TPMLP_KERNEL_LINEAR_FWD = 7,  /* linear layers: Y_i = X.W_i + b, Z = sum_i X_i.W_i + b */
-    TPMLP_KERNEL_LINEAR_DGRAD = 8,  /* linear layers: dX = sum_i dY_i.W_i^T, dX_i = dZ.W_i^T */
-    TPMLP_KERNEL_LINEAR_WGRAD = 9,  /* linear layers: dW_i */
+    TPMLP_KERNEL_LINEAR_FWD = 7,  /* linear layers (bf16, 8-bit): Y_i = X.W_i + b, Z = sum_i X_i.W_i + b */
+    TPMLP_KERNEL_LINEAR_DGRAD = 8,  /* linear layers (bf16, 8-bit): dX = sum_i dY_i.W_i^T, dX_i = dZ.W_i^T */
+    TPMLP_KERNEL_LINEAR_WGRAD = 9,  /* linear layers (bf16, 8-bit): dW_i */
     TPMLP_KERNEL_LAYERNORM_FWD = 10,  /* sequence-parallel sublayer: LN(X) and row statistics */
     TPMLP_KERNEL_LAYERNORM_BWD = 11,  /* sequence-parallel sublayer: dX, dgamma, dbeta (2 launches; 3 for h > 4096) */
     TPMLP_KERNEL_DROPOUT_BWD = 12,    /* sequence-parallel sublayer: dZ from dOut and the mask, db2 (2 launches) */
-    TPMLP_KERNEL_SP_COPY = 13,        /* tpmlp_sp_gather / tpmlp_sp_scatter */
+    TPMLP_KERNEL_SP_COPY = 13,        /* tpmlp_sp_gather / tpmlp_sp_scatter, 8-bit quantisation */
     TPMLP_KERNEL_KINDS = 14
 };
 tpmlp_status tpmlp_profile_begin(int capacity);

@@ -42,6 +42,9 @@ EXPORTED = (
     "tpmlp_sp_workspace_bytes", "tpmlp_sp_workspace_layout", "tpmlp_sp_forward", "tpmlp_sp_backward",
     "tpmlp_set_head_prefetch", "tpmlp_map_cache_stats", "tpmlp_selftest_map_cache",
     "tpmlp_set_wide_tiles", "tpmlp_sp_gather", "tpmlp_sp_scatter",
+    "tpmlp_fp8_quantize", "tpmlp_fp8_quantize_weight", "tpmlp_fp8_linear_workspace_bytes",
+    "tpmlp_fp8_column_linear_forward", "tpmlp_fp8_column_linear_backward",
+    "tpmlp_fp8_row_linear_forward", "tpmlp_fp8_row_linear_backward",
 )
 
 
@@ -59,6 +62,16 @@ class tpmlp_linear_dims(ctypes.Structure):
 class tpmlp_sp_params(ctypes.Structure):
     _fields_ = [("eps", ctypes.c_float), ("dropout_p", ctypes.c_double),
                 ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
+
+
+class tpmlp_fp8_quant(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("scale_ld", ctypes.c_int64),
+                ("parts", ctypes.c_int32), ("rows_format", ctypes.c_int32),
+                ("cols_format", ctypes.c_int32)]
+
+
+class tpmlp_fp8_formats(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_int32), ("w", ctypes.c_int32), ("dy", ctypes.c_int32)]
 
 
 class TpmlpError(RuntimeError):
@@ -141,6 +154,28 @@ for _name in ("tpmlp_column_linear_backward", "tpmlp_row_linear_backward"):
     getattr(_lib, _name).restype = ctypes.c_int
     getattr(_lib, _name).argtypes = [_ldims_p, _vpp, _vpp, _vpp, _vpp, _vpp, _vp, _vp, _vp]
 
+_quant_p = ctypes.POINTER(tpmlp_fp8_quant)
+_fmt_p = ctypes.POINTER(tpmlp_fp8_formats)
+_lib.tpmlp_fp8_quantize.restype = ctypes.c_int
+_lib.tpmlp_fp8_quantize.argtypes = [_quant_p, _vpp, _vpp, _vpp, _vpp, _vpp, _vp]
+_lib.tpmlp_fp8_quantize_weight.restype = ctypes.c_int
+_lib.tpmlp_fp8_quantize_weight.argtypes = [_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, _vp,
+                                           _vp, _vp]
+_lib.tpmlp_fp8_linear_workspace_bytes.restype = ctypes.c_size_t
+_lib.tpmlp_fp8_linear_workspace_bytes.argtypes = [_ldims_p]
+_lib.tpmlp_fp8_column_linear_forward.restype = ctypes.c_int
+_lib.tpmlp_fp8_column_linear_forward.argtypes = [_ldims_p, _fmt_p, _vp, _vp, _vpp, _vpp, _vp, _vpp,
+                                                 _vp, _vp]
+_lib.tpmlp_fp8_row_linear_forward.restype = ctypes.c_int
+_lib.tpmlp_fp8_row_linear_forward.argtypes = [_ldims_p, _fmt_p, _vpp, _vpp, _vpp, _vpp, _vp, _vpp,
+                                              _vp, _vp]
+_lib.tpmlp_fp8_column_linear_backward.restype = ctypes.c_int
+_lib.tpmlp_fp8_column_linear_backward.argtypes = [_ldims_p, _fmt_p, _vpp, _vp, _vp, _vpp, _vpp,
+                                                  _vpp, _vpp, _vp, _vp, _vp]
+_lib.tpmlp_fp8_row_linear_backward.restype = ctypes.c_int
+_lib.tpmlp_fp8_row_linear_backward.argtypes = [_ldims_p, _fmt_p, _vpp, _vpp, _vpp, _vpp, _vpp,
+                                               _vpp, _vpp, _vp, _vp, _vp]
+
 
 def library_path() -> str:
     return _LIB_PATH
@@ -169,6 +204,8 @@ def _ptr(x) -> int | None:
 
 
 def _arr(xs):
+    if isinstance(xs, ctypes.Array):  # already marshalled (a layer's own buffers)
+        return xs
     return (ctypes.c_void_p * len(xs))(*[_ptr(x) for x in xs])
 
 
@@ -368,6 +405,74 @@ def tpmlp_row_linear_backward(dims, dZ, X_shards, W_shards, dX_shards, dW_shards
                                           _arr(W_shards), _arr(dX_shards), _arr(dW_shards),
                                           _ptr(db), _ptr(workspace), _stream(stream)),
            "tpmlp_row_linear_backward")
+
+
+TPMLP_FP8_E4M3 = 0
+TPMLP_FP8_E5M2 = 1
+FP8_FORMATS = {"e4m3": TPMLP_FP8_E4M3, "e5m2": TPMLP_FP8_E5M2}
+
+
+def make_fp8_quant(rows: int, cols: int, scale_ld: int, parts: int = 1, rows_format: int = 0,
+                   cols_format: int = 0) -> tpmlp_fp8_quant:
+    return tpmlp_fp8_quant(int(rows), int(cols), int(scale_ld), int(parts), int(rows_format),
+                           int(cols_format))
+
+
+def make_fp8_formats(x: int = 0, w: int = 0, dy: int = 0) -> tpmlp_fp8_formats:
+    return tpmlp_fp8_formats(int(x), int(w), int(dy))
+
+
+def tpmlp_fp8_quantize(quant, src, q_rows, s_rows, q_cols, s_cols, stream=None) -> None:
+    """src and the outputs: lists of quant.parts tensors; the row pair or the
+    column pair may be None."""
+    opt = lambda xs: None if xs is None else _arr(xs)  # noqa: E731
+    _check(_lib.tpmlp_fp8_quantize(ctypes.byref(quant), _arr(src), opt(q_rows), opt(s_rows),
+                                   opt(q_cols), opt(s_cols), _stream(stream)),
+           "tpmlp_fp8_quantize")
+
+
+def tpmlp_fp8_quantize_weight(W, in_features: int, out_features: int, fmt: int, q, s,
+                              stream=None) -> None:
+    _check(_lib.tpmlp_fp8_quantize_weight(_ptr(W), int(in_features), int(out_features), int(fmt),
+                                          _ptr(q), _ptr(s), _stream(stream)),
+           "tpmlp_fp8_quantize_weight")
+
+
+def tpmlp_fp8_linear_workspace_bytes(dims: tpmlp_linear_dims) -> int:
+    """Scratch bytes of any 8-bit linear call with these dims (0 if invalid)."""
+    return int(_lib.tpmlp_fp8_linear_workspace_bytes(ctypes.byref(dims)))
+
+
+def tpmlp_fp8_column_linear_forward(dims, formats, Xq, Xs, Wq_shards, Ws_shards, b, Y_shards,
+                                    workspace, stream=None) -> None:
+    _check(_lib.tpmlp_fp8_column_linear_forward(
+        ctypes.byref(dims), ctypes.byref(formats), _ptr(Xq), _ptr(Xs), _arr(Wq_shards),
+        _arr(Ws_shards), _ptr(b), _arr(Y_shards), _ptr(workspace), _stream(stream)),
+        "tpmlp_fp8_column_linear_forward")
+
+
+def tpmlp_fp8_row_linear_forward(dims, formats, Xq_shards, Xs_shards, Wq_shards, Ws_shards, b, Z,
+                                 workspace, stream=None) -> None:
+    _check(_lib.tpmlp_fp8_row_linear_forward(
+        ctypes.byref(dims), ctypes.byref(formats), _arr(Xq_shards), _arr(Xs_shards),
+        _arr(Wq_shards), _arr(Ws_shards), _ptr(b), _arr(Z), _ptr(workspace), _stream(stream)),
+        "tpmlp_fp8_row_linear_forward")
+
+
+def tpmlp_fp8_column_linear_backward(dims, formats, dY_shards, Xq, Xs, Wq_shards, Ws_shards, dX,
+                                     dW_shards, db, workspace, stream=None) -> None:
+    _check(_lib.tpmlp_fp8_column_linear_backward(
+        ctypes.byref(dims), ctypes.byref(formats), _arr(dY_shards), _ptr(Xq), _ptr(Xs),
+        _arr(Wq_shards), _arr(Ws_shards), _arr(dX), _arr(dW_shards), _ptr(db), _ptr(workspace),
+        _stream(stream)), "tpmlp_fp8_column_linear_backward")
+
+
+def tpmlp_fp8_row_linear_backward(dims, formats, dZ, Xq_shards, Xs_shards, Wq_shards, Ws_shards,
+                                  dX_shards, dW_shards, db, workspace, stream=None) -> None:
+    _check(_lib.tpmlp_fp8_row_linear_backward(
+        ctypes.byref(dims), ctypes.byref(formats), _arr(dZ), _arr(Xq_shards), _arr(Xs_shards),
+        _arr(Wq_shards), _arr(Ws_shards), _arr(dX_shards), _arr(dW_shards), _ptr(db),
+        _ptr(workspace), _stream(stream)), "tpmlp_fp8_row_linear_backward")
 
 
 def make_sp_params(eps: float = 1e-5, dropout_p: float = 0.1, seed: int = 0,

@@ -1,0 +1,46 @@
+// fp8_internal.h -- host-side helpers of the 8-bit calls: tensor maps of 8-bit
+// operands through the library's map cache.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "abi_internal.h"
+#include "map_cache.h"
+
+namespace tpmlp {
+namespace abi {
+
+// defined beside the tensor maps of the bf16 GEMM
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+extern EncodeTiledFn g_encode;
+extern MapCache g_maps;
+extern unsigned long long g_timeout_ns;
+
+// Row-major 8-bit matrix [outer, inner] (inner a multiple of 16), fetched as
+// boxes of 128 bytes x `box_outer` rows with the 128-byte swizzle; what lies
+// outside the matrix reads as zeros.
+inline bool encode_bytes(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
+                         uint32_t box_outer) {
+    const cuuint64_t dims[2] = {inner, outer};
+    const cuuint64_t strides[1] = {inner};
+    const cuuint32_t box[2] = {128, box_outer};
+    const MapKey key =
+        make_map_key(CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ptr, dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    return g_maps.get(key, m, [&](CUtensorMap* out) {
+        const cuuint32_t estr[2] = {1, 1};
+        return g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    });
+}
+
+}  // namespace abi
+}  // namespace tpmlp

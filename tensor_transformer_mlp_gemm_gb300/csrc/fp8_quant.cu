@@ -1,0 +1,267 @@
+// fp8_quant.cu -- quantisation to 8-bit floating point (see fp8_quant.cuh for
+// the definition).
+//
+// What bounds it: HBM traffic, 2 bytes read and 1 byte written per element and
+// grouping.  So both groupings of an activation, and the column sums of a
+// gradient (the bias gradient), come from one read.
+//
+// A CTA takes a 128 x 128 tile, which is 128 whole row groups, 128 whole
+// column groups and one whole block, so no group crosses CTAs and nothing is
+// read twice.  A thread holds 8 rows x 8 columns as eight 16-byte loads, all
+// in flight before the first use.  Magnitudes are compared as integers: the 15
+// low bits of a bf16 grow with |x|, with infinities and NaN on top, so one
+// packed 16-bit maximum instruction compares two values and a group that is not
+// finite shows as a maximum of at least 0x7F80.
+#include "fp8_quant.cuh"
+
+#include "ptx.cuh"
+
+namespace tpmlp {
+namespace {
+
+constexpr int QT = 256;          // threads
+constexpr int QV = 8;            // rows (and columns) per thread
+constexpr int QWARPS = QT / 32;
+
+// Magnitude bits of a group's largest value -> the scale and its reciprocal.
+struct Scale {
+    float s, inv;
+    bool fine;
+};
+
+__device__ __forceinline__ Scale scale_of(uint32_t amax, int fmt) {
+    // |x| = 2^(e - 127) (1 + m / 128); top = 1.75 * 2^8 or 1.75 * 2^15
+    const int e = static_cast<int>(amax >> 7), m = static_cast<int>(amax & 0x7Fu);
+    int k = e - 127 - (fmt == FP8_E4M3 ? 8 : 15) + (m > 96 ? 1 : 0);
+    if (e == 0 || k < -119) k = -119;
+    Scale r;
+    r.fine = amax < 0x7F80u;
+    r.s = r.fine ? __uint_as_float(static_cast<uint32_t>(k + 127) << 23)
+                 : __uint_as_float(0x7FC00000u);
+    r.inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+    return r;
+}
+
+// hi and lo rounded to 8 bits, hi in the upper byte
+__device__ __forceinline__ uint32_t cvt8(float lo, float hi, int fmt) {
+    uint16_t r;
+    if (fmt == FP8_E4M3)
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// the largest of the two 16-bit halves
+__device__ __forceinline__ uint32_t fold(uint32_t w) { return max(w & 0xFFFFu, w >> 16); }
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(QT) fp8_quant_kernel(const __grid_constant__ Fp8QuantParams p,
+                                                       int col_tiles) {
+    constexpr bool ROWS = MODE & FP8_Q_ROWS, COLS = MODE & FP8_Q_COLS, SUMS = MODE & FP8_Q_SUMS,
+                   BLOCK = MODE & FP8_Q_BLOCK;
+    __shared__ uint4 s_max[QWARPS][16];       // column magnitudes of each warp's rows
+    __shared__ float s_inv[FP8_GROUP];        // reciprocal column scales (0: not finite)
+    __shared__ float s_row[FP8_GROUP];        // row scales
+    __shared__ float s_sum[SUMS ? QWARPS : 1][FP8_GROUP];
+    __shared__ uint32_t s_blk[QWARPS];
+
+    const int part = blockIdx.y;
+    const long long rt = blockIdx.x / col_tiles, ct = blockIdx.x % col_tiles;
+    const long long r0 = rt * FP8_GROUP, c0 = ct * FP8_GROUP;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cv = lane & 15;                 // this thread's 8 columns
+    const int slot = warp * 2 + (lane >> 4);  // its rows: slot + 16 i
+    const long long c = c0 + cv * QV;
+    const bool col_in = c < p.cols;
+
+    // the dependent launch may be scheduled as soon as there is room for it; it
+    // waits for this grid's results itself
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.src[part]) + c);
+    const long long vstep = p.cols / 8;
+    uint4 v[QV];
+#pragma unroll
+    for (int i = 0; i < QV; ++i) {
+        const long long r = r0 + slot + 16 * i;
+        v[i] = (col_in && r < p.rows) ? __ldg(src + r * vstep) : make_uint4(0, 0, 0, 0);
+    }
+
+    constexpr uint32_t MAG = 0x7FFF7FFFu;
+    uint32_t row_max[QV];
+    uint32_t cm[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < QV; ++i) {
+        const uint32_t a = v[i].x & MAG, b = v[i].y & MAG, d = v[i].z & MAG, e = v[i].w & MAG;
+        if (ROWS) row_max[i] = fold(__vmaxu2(__vmaxu2(a, b), __vmaxu2(d, e)));
+        if (COLS || BLOCK) {
+            cm[0] = __vmaxu2(cm[0], a);
+            cm[1] = __vmaxu2(cm[1], b);
+            cm[2] = __vmaxu2(cm[2], d);
+            cm[3] = __vmaxu2(cm[3], e);
+        }
+    }
+
+    if constexpr (BLOCK) {
+        uint32_t m = fold(__vmaxu2(__vmaxu2(cm[0], cm[1]), __vmaxu2(cm[2], cm[3])));
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) s_blk[warp] = m;
+        __syncthreads();
+        m = s_blk[0];
+#pragma unroll
+        for (int w = 1; w < QWARPS; ++w) m = max(m, s_blk[w]);
+        const Scale sc = scale_of(m, p.fmt_cols);
+        if (threadIdx.x == 0) p.s_cols[part][rt * col_tiles + ct] = sc.s;
+        if (col_in) {
+            uint8_t* q = static_cast<uint8_t*>(p.q_cols[part]);
+#pragma unroll
+            for (int i = 0; i < QV; ++i) {
+                const long long r = r0 + slot + 16 * i;
+                if (r >= p.rows) break;
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t w = word(v[i], j);
+                    o[j] = sc.fine ? cvt8(lo_f(w) * sc.inv, hi_f(w) * sc.inv, p.fmt_cols) : 0u;
+                }
+                *reinterpret_cast<uint2*>(q + r * p.cols + c) =
+                    make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+            }
+        }
+        return;
+    }
+
+    if constexpr (COLS) {
+        // both row slots of the warp, then the warps
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cm[j] = __vmaxu2(cm[j], __shfl_xor_sync(0xffffffffu, cm[j], 16));
+        if (lane < 16) s_max[warp][cv] = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+    }
+    if constexpr (SUMS) {
+        // this thread's 8 rows in order, then the other row slot, then the warps
+        float cs[QV] = {};
+#pragma unroll
+        for (int i = 0; i < QV; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                cs[2 * j] += lo_f(word(v[i], j));
+                cs[2 * j + 1] += hi_f(word(v[i], j));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < QV; ++j) {
+            cs[j] += __shfl_xor_sync(0xffffffffu, cs[j], 16);
+            if (lane < 16) s_sum[warp][cv * QV + j] = cs[j];
+        }
+    }
+
+    if constexpr (ROWS) {
+        uint8_t* q = static_cast<uint8_t*>(p.q_rows[part]);
+#pragma unroll
+        for (int i = 0; i < QV; ++i) {
+            uint32_t m = row_max[i];
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const Scale sc = scale_of(m, p.fmt_rows);
+            const long long r = r0 + slot + 16 * i;
+            if (cv == 0) s_row[slot + 16 * i] = sc.s;
+            if (col_in && r < p.rows) {
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t w = word(v[i], j);
+                    o[j] = sc.fine ? cvt8(lo_f(w) * sc.inv, hi_f(w) * sc.inv, p.fmt_rows) : 0u;
+                }
+                *reinterpret_cast<uint2*>(q + r * p.cols + c) =
+                    make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+            }
+        }
+    }
+    __syncthreads();
+
+    if (threadIdx.x < FP8_GROUP) {
+        const int k = threadIdx.x;
+        if (ROWS && r0 + k < p.rows) p.s_rows[part][ct * p.ld + r0 + k] = s_row[k];
+        if constexpr (COLS) {
+            const uint16_t* mags = reinterpret_cast<const uint16_t*>(&s_max[0][0]);
+            uint32_t m = 0;
+#pragma unroll
+            for (int w = 0; w < QWARPS; ++w) m = max(m, static_cast<uint32_t>(mags[w * 128 + k]));
+            const Scale sc = scale_of(m, p.fmt_cols);
+            s_inv[k] = sc.fine ? sc.inv : 0.0f;
+            if (c0 + k < p.cols) p.s_cols[part][rt * p.cols + c0 + k] = sc.s;
+        }
+        if constexpr (SUMS) {
+            float t = s_sum[0][k];
+#pragma unroll
+            for (int w = 1; w < QWARPS; ++w) t += s_sum[w][k];
+            if (c0 + k < p.cols) p.sums[part][rt * p.sums_ld + c0 + k] = t;
+        }
+    }
+    if constexpr (COLS) {
+        __syncthreads();
+        if (!col_in) return;
+        float inv[QV];
+#pragma unroll
+        for (int j = 0; j < QV; ++j) inv[j] = s_inv[cv * QV + j];
+        uint8_t* q = static_cast<uint8_t*>(p.q_cols[part]);
+#pragma unroll
+        for (int i = 0; i < QV; ++i) {
+            const long long r = r0 + slot + 16 * i;
+            if (r >= p.rows) break;
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w = word(v[i], j);
+                // a column that is not finite: 0 * inf would be NaN
+                const float lo = inv[2 * j] > 0.0f ? lo_f(w) * inv[2 * j] : 0.0f;
+                const float hi = inv[2 * j + 1] > 0.0f ? hi_f(w) * inv[2 * j + 1] : 0.0f;
+                o[j] = cvt8(lo, hi, p.fmt_cols);
+            }
+            *reinterpret_cast<uint2*>(q + r * p.cols + c) =
+                make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+        }
+    }
+}
+
+template <int MODE>
+cudaError_t launch(const Fp8QuantParams& p, cudaStream_t st) {
+    const long long rt = (p.rows + FP8_GROUP - 1) / FP8_GROUP;
+    const long long ct = (p.cols + FP8_GROUP - 1) / FP8_GROUP;
+    if (ct > 0x7FFFFFFFLL || rt > 0x7FFFFFFFLL / ct) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rt * ct), static_cast<unsigned>(p.parts), 1);
+    cfg.blockDim = dim3(QT, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fp8_quant_kernel<MODE>, p, static_cast<int>(ct));
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quant(const Fp8QuantParams& p, int mode, cudaStream_t st) {
+    switch (mode) {
+        case FP8_Q_ROWS: return launch<FP8_Q_ROWS>(p, st);
+        case FP8_Q_COLS: return launch<FP8_Q_COLS>(p, st);
+        case FP8_Q_ROWS | FP8_Q_COLS: return launch<FP8_Q_ROWS | FP8_Q_COLS>(p, st);
+        case FP8_Q_ROWS | FP8_Q_COLS | FP8_Q_SUMS:
+            return launch<FP8_Q_ROWS | FP8_Q_COLS | FP8_Q_SUMS>(p, st);
+        case FP8_Q_BLOCK: return launch<FP8_Q_BLOCK>(p, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace tpmlp

@@ -1,0 +1,259 @@
+"""8-bit quantisation with a scale for each group of 128, and device buffers for
+one tensor-parallel linear layer on 8-bit operands.
+
+PyTorch is used for device memory and streams only; every step runs in libtpmlp
+through :mod:`binding`.  Layouts follow the C ABI (include/tpmlp.h):
+  activations  q [T, C] float8; row_scale fp32 [ceil(C/128), T] (groups along
+               features, for a product over features); col_scale fp32
+               [ceil(T/128), C] (groups along tokens, for the weight gradient)
+  weights      q [in, out] float8, scale fp32 [ceil(in/128), ceil(out/128)]
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import binding
+from .inputs import LinearWorkload
+
+DTYPES = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+
+
+def _up128(n: int) -> int:
+    return -(-n // 128)
+
+
+@dataclass
+class Fp8Tokens:
+    """One matrix of activations in 8 bits: by rows, by columns, or both."""
+    rows: torch.Tensor | None = None
+    row_scale: torch.Tensor | None = None
+    cols: torch.Tensor | None = None
+    col_scale: torch.Tensor | None = None
+
+
+def _format(name: str) -> int:
+    if name not in binding.FP8_FORMATS:
+        raise ValueError(f"format must be one of {sorted(binding.FP8_FORMATS)}, got {name!r}")
+    return binding.FP8_FORMATS[name]
+
+
+def _check_bf16(x: torch.Tensor, what: str) -> None:
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_contiguous() or not x.is_cuda:
+        raise ValueError(f"{what} must be a contiguous 2-d bf16 CUDA tensor, got "
+                         f"{x.dtype} {tuple(x.shape)} on {x.device}")
+
+
+def _check_like(x: torch.Tensor, shape: tuple, dtype, device, what: str) -> None:
+    if x.shape != shape or x.dtype != dtype or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
+
+
+def _empty_tokens(T: int, C: int, fmt: str, rows: bool, cols: bool, dev) -> Fp8Tokens:
+    x = Fp8Tokens()
+    if rows:
+        x.rows = torch.empty(T, C, dtype=DTYPES[fmt], device=dev)
+        x.row_scale = torch.empty(_up128(C), T, dtype=torch.float32, device=dev)
+    if cols:
+        x.cols = torch.empty(T, C, dtype=DTYPES[fmt], device=dev)
+        x.col_scale = torch.empty(_up128(T), C, dtype=torch.float32, device=dev)
+    return x
+
+
+def quantize_tokens(X, fmt: str = "e4m3", rows: bool = True, cols: bool = False,
+                    out: Fp8Tokens | None = None, stream=None) -> Fp8Tokens:
+    """X: a bf16 tensor [T, C], or the list of its token chunks, which are
+    gathered on the way.  rows and cols choose the groupings (one read makes
+    both); out: buffers to reuse, as returned by an earlier call."""
+    chunks = [X] if isinstance(X, torch.Tensor) else list(X)
+    code = _format(fmt)
+    for c in chunks:
+        _check_bf16(c, "X")
+    first, n = chunks[0], len(chunks)
+    tc, C = first.shape
+    if any(c.shape != first.shape for c in chunks):
+        raise ValueError("token chunks must have one shape")
+    if n > 1 and tc % 128:
+        raise ValueError("token chunks must be a multiple of 128 tokens")
+    if not (rows or cols):
+        raise ValueError("choose rows, cols or both")
+    T, dev = tc * n, first.device
+    if out is None:
+        out = _empty_tokens(T, C, fmt, rows, cols, dev)
+    if rows:
+        _check_like(out.rows, (T, C), DTYPES[fmt], dev, "out.rows")
+        _check_like(out.row_scale, (_up128(C), T), torch.float32, dev, "out.row_scale")
+    if cols:
+        _check_like(out.cols, (T, C), DTYPES[fmt], dev, "out.cols")
+        _check_like(out.col_scale, (_up128(T), C), torch.float32, dev, "out.col_scale")
+
+    def part(x, step):
+        return [x.data_ptr() + j * step for j in range(n)]
+    quant = binding.make_fp8_quant(tc, C, max(T, 1), n, code, code)
+    with torch.cuda.device(dev):
+        binding.tpmlp_fp8_quantize(
+            quant, chunks, part(out.rows, tc * C) if rows else None,
+            part(out.row_scale, tc * 4) if rows else None, part(out.cols, tc * C) if cols else None,
+            part(out.col_scale, tc // 128 * C * 4) if cols else None, stream)
+    return out
+
+
+def quantize_shards(shards, fmt: str = "e4m3", rows: bool = True, cols: bool = False,
+                    stream=None) -> list:
+    """Each of up to eight bf16 tensors [T, C] of one shape, in one launch."""
+    shards = list(shards)
+    code = _format(fmt)
+    for x in shards:
+        _check_bf16(x, "shard")
+    if any(x.shape != shards[0].shape for x in shards):
+        raise ValueError("shards must have one shape")
+    if not (rows or cols):
+        raise ValueError("choose rows, cols or both")
+    T, C = shards[0].shape
+    dev = shards[0].device
+    outs = [_empty_tokens(T, C, fmt, rows, cols, dev) for _ in shards]
+    quant = binding.make_fp8_quant(T, C, max(T, 1), len(shards), code, code)
+    with torch.cuda.device(dev):
+        binding.tpmlp_fp8_quantize(
+            quant, shards, [o.rows for o in outs] if rows else None,
+            [o.row_scale for o in outs] if rows else None, [o.cols for o in outs] if cols else None,
+            [o.col_scale for o in outs] if cols else None, stream)
+    return outs
+
+
+def quantize_weight(W: torch.Tensor, fmt: str = "e4m3", stream=None) -> tuple:
+    """(q, scale) of one bf16 weight shard [in, out] in 128 x 128 blocks."""
+    code = _format(fmt)
+    _check_bf16(W, "W")
+    r, c = W.shape
+    q = torch.empty(r, c, dtype=DTYPES[fmt], device=W.device)
+    s = torch.empty(_up128(r), _up128(c), dtype=torch.float32, device=W.device)
+    with torch.cuda.device(W.device):
+        binding.tpmlp_fp8_quantize_weight(W, r, c, code, q, s, stream)
+    return q, s
+
+
+class DeviceFp8Linear:
+    """One linear layer on quantised weight shards (``quantize_weight``): the
+    8-bit counterpart of ``linear.DeviceLinear`` for the same workloads.
+
+    forward takes activations by rows, backward the same activations by
+    columns; ``quantize(X, cols=True)`` makes both in one pass."""
+
+    def __init__(self, w: LinearWorkload, Wq, Ws, b: torch.Tensor, x_format: str = "e4m3",
+                 w_format: str = "e4m3", dy_format: str = "e4m3",
+                 workspace: torch.Tensor | None = None):
+        if w.split not in ("column", "row"):
+            raise ValueError("split must be 'column' or 'row'")
+        self.w = w
+        self.column = w.split == "column"
+        self.x_format = x_format
+        self.formats = binding.make_fp8_formats(_format(x_format), _format(w_format),
+                                                _format(dy_format))
+        T, din, dout, t, n = w.tokens, w.in_features, w.out_features, w.t, w.seq_chunks
+        self.dims = binding.make_linear_dims(T, din, dout, t, n)
+        need = binding.tpmlp_fp8_linear_workspace_bytes(self.dims)
+        if need == 0:
+            raise ValueError(f"unsupported dims for an 8-bit linear layer: {w}")
+        self.Wq, self.Ws, self.b = list(Wq), list(Ws), b
+        self.device = dev = b.device
+        s = w.shard
+        wshape = (din, s) if self.column else (s, dout)
+        if len(self.Wq) != t or len(self.Ws) != t:
+            raise ValueError(f"{t} weight shards and scales are needed")
+        for q, sc in zip(self.Wq, self.Ws):
+            _check_like(q, wshape, DTYPES[w_format], dev, "a weight shard")
+            _check_like(sc, (_up128(wshape[0]), _up128(wshape[1])), torch.float32, dev,
+                        "a weight shard's scale")
+        _check_like(b, (dout,), torch.bfloat16, dev, "b")
+        bf, f32 = torch.bfloat16, torch.float32
+        # the shapes of X_i, Y_i (or Z) and their gradients, and how many of each
+        self._x = ((T, din), 1) if self.column else ((T, s), t)
+        self._y = ((T, s), t) if self.column else ((T // n, dout), n)
+        self._dx = ((T // n, din), n) if self.column else ((T, s), t)
+        self.Y = [torch.empty(self._y[0], dtype=bf, device=dev) for _ in range(self._y[1])]
+        self.dX = [torch.empty(self._dx[0], dtype=bf, device=dev) for _ in range(self._dx[1])]
+        self._grads = None
+        if workspace is not None and workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"the workspace needs {need} bytes")
+        self.ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8,
+                                                                      device=dev)
+        self._args = tuple(binding._arr(x) for x in (self.Wq, self.Ws))
+
+    def _weight_grads(self):
+        # fp32 gradients, four times the weights' bytes: made by the first backward call
+        if self._grads is None:
+            shape = self.Wq[0].shape
+            self._grads = ([torch.empty(shape, dtype=torch.float32, device=self.device)
+                            for _ in range(self.w.t)],
+                           torch.empty(self.w.out_features, dtype=torch.float32,
+                                       device=self.device))
+        return self._grads
+
+    @property
+    def dW(self):
+        return self._weight_grads()[0]
+
+    @property
+    def db(self):
+        return self._weight_grads()[1]
+
+    def quantize(self, X, cols: bool = False, stream=None):
+        """The layer's bf16 input (column: [T, in] or its token chunks; row: the
+        t shards) as forward and backward take it."""
+        if self.column:
+            return quantize_tokens(X, self.x_format, True, cols, stream=stream)
+        return quantize_shards(X, self.x_format, True, cols, stream=stream)
+
+    def _tokens(self, x, cols: bool):
+        x = [x] if isinstance(x, Fp8Tokens) else list(x)
+        shape, n = self._x
+        if len(x) != n:
+            raise ValueError(f"{n} quantised inputs are needed, got {len(x)}")
+        T, C = shape
+        sshape = (_up128(T), C) if cols else (_up128(C), T)
+        q = [v.cols if cols else v.rows for v in x]
+        s = [v.col_scale if cols else v.row_scale for v in x]
+        for a, b in zip(q, s):
+            if a is None or b is None:
+                raise ValueError("the input is not quantised by " + ("columns" if cols else "rows"))
+            _check_like(a, shape, DTYPES[self.x_format], self.device, "a quantised input")
+            _check_like(b, sshape, torch.float32, self.device, "its scale")
+        return q, s
+
+    def _list(self, xs, spec, what):
+        xs = [xs] if isinstance(xs, torch.Tensor) else list(xs)
+        if len(xs) != spec[1]:
+            raise ValueError(f"{what}: {spec[1]} tensors are needed, got {len(xs)}")
+        for x in xs:
+            _check_like(x, spec[0], torch.bfloat16, self.device, what)
+        return xs
+
+    def forward(self, x, Y=None, stream=None) -> None:
+        """x: Fp8Tokens by rows (column: one, row: t of them)."""
+        q, s = self._tokens(x, cols=False)
+        Y = self.Y if Y is None else self._list(Y, self._y, "Y")
+        with torch.cuda.device(self.device):
+            if self.column:
+                binding.tpmlp_fp8_column_linear_forward(self.dims, self.formats, q[0], s[0],
+                                                        *self._args, self.b, Y, self.ws, stream)
+            else:
+                binding.tpmlp_fp8_row_linear_forward(self.dims, self.formats, q, s, *self._args,
+                                                     self.b, Y, self.ws, stream)
+
+    def backward(self, dY, x, dX=None, stream=None) -> None:
+        """dY: bf16 (column: t shards, row: token chunks); x: Fp8Tokens by columns."""
+        q, s = self._tokens(x, cols=True)
+        dY = self._list(dY, self._y, "dY")
+        dX = self.dX if dX is None else self._list(dX, self._dx, "dX")
+        with torch.cuda.device(self.device):
+            if self.column:
+                binding.tpmlp_fp8_column_linear_backward(
+                    self.dims, self.formats, dY, q[0], s[0], *self._args, dX, self.dW, self.db,
+                    self.ws, stream)
+            else:
+                binding.tpmlp_fp8_row_linear_backward(
+                    self.dims, self.formats, dY, q, s, *self._args, dX, self.dW, self.db, self.ws,
+                    stream)
