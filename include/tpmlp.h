@@ -319,10 +319,9 @@ tpmlp_status tpmlp_sp_backward(const tpmlp_dims* dims, const tpmlp_sp_params* sp
  *   s = the smallest power of two with max |x| <= s * top, at least 2^-119
  *   q = x / s (exact) rounded to nearest even
  * top = 448 for e4m3, 57344 for e5m2.  A group that holds an infinity or a NaN
- * gets s = NaN and q = 0, so what is computed from it is NaN.  The products
- * take any finite scales (a scale of a matrix quantised elsewhere need not be
- * a power of two), as long as the product of the two scales of a block is
- * finite and, to count, at least 2^-149 in fp32.
+ * gets s = NaN and q = 0, so what is computed from it is NaN.  The tensor cores
+ * apply the scales as 8-bit exponents: a matrix quantised elsewhere may be used
+ * if its scales are powers of two, 2^-126 .. 2^127; any other scale reads as NaN.
  *
  * Layouts, for a matrix [R, C] row-major (R tokens or input features):
  *   q         8-bit [R, C], C a multiple of 16

@@ -1,27 +1,28 @@
 // fp8_gemm.cu -- the 8-bit product with scales per block of 128 on tcgen05 CTA
 // pairs (see fp8_gemm.cuh for the mathematics).
 //
-// A scale changes every 128 of K, so the sum over K cannot stay in tensor
-// memory: each K block's 256 x 256 partial sums go to one of two accumulators
-// there, and the epilogue warps read them back, multiply by the block's scales
-// and add them up in fp32 registers while the tensor cores fill the other
-// accumulator.
+// The tensor cores apply the scales (fp8_mma.cuh), so the sum over all of K stays
+// in tensor memory.  An earlier form kept each K block's sums apart and scaled
+// and added them in registers: reading 128 x 256 sums back for every K block
+// and the way from there to the next MMAs took 880 clocks a block where the MMAs
+// take 512, and that form spent 1050 on scales per column of B.
 //
-// CTA layout (384 threads, persistent over tiles; both CTAs of a pair):
+// CTA layout (512 threads, persistent over tiles; both CTAs of a pair compute one
+// 256 x 256 tile, 128 rows each):
 //   warp 0       TMA producer: this CTA's 128 rows of A and of B for each K block
 //   warp 1       owns the tensor memory; in the even CTA issues the pair's MMAs,
 //                four K slices of 32 for each K block
-//   warps 2, 3   idle (registers move between whole warpgroups)
-//   warps 4..11  promotion and output: warp w reads lanes 32 (w % 4) .. of the
-//                accumulator, columns 128 ((w - 4) / 4) .., so a thread keeps 128
-//                sums of one row in registers, and the 128 columns share one
-//                weight block
-// 128 sums, the 32 values read and the addresses do not fit the 168 registers a
-// thread of 384 can launch with (measured: 450 bytes of spills): the first
-// warpgroup gives most of its registers to the other two.
-// What bounds it: the tensor cores at 512 clocks for a K block of a pair's tile
-// if the promotion of 128 x 256 sums per CTA (half the fp32 rate with single
-// multiply-adds, a quarter with the packed ones used here) stays below that.
+//   warps 4..7   scales: the exponents of this CTA's 128 rows of A and of all 256
+//                rows of B for each K block, into tensor memory, a slot per stage.
+//                Each warp fetches a quarter of them, they are exchanged in shared
+//                memory, and each writes all of them to its quarter of the lanes
+//   warps 8..15  output: warp w reads lanes 32 (w % 4) .. of the accumulator and
+//                columns 128 ((w - 8) / 4) .. into registers, frees the accumulator
+//                for the next tile's MMAs, and writes from there
+// Tensor memory: 256 columns of sums, then 6 x 16 columns of scales.  Two
+// accumulators of 256 columns leave none for the scales; with one, the MMAs wait
+// about 1000 clocks a tile for it to be read.
+// What bounds it: the tensor cores, 512 clocks for each K block of a tile.
 //
 // Every wait is bounded as in the bf16 GEMM: a wait that expires sets a flag
 // that ends the CTA's roles, copies and MMAs in flight are drained (bounded),
@@ -38,24 +39,23 @@ namespace {
 
 using namespace f8;
 
-constexpr int F_THREADS = 384;
-// 128 x 56 + 256 x 216 = 62464 of the 384 x 168 = 64512 registers at launch
-constexpr int F_FEW_REGS = 56, F_MANY_REGS = 216;
-constexpr int F_EPI_WARPS = 8;
+constexpr int F_THREADS = 512;
+// registers per thread: 128 x 56 + 128 x 72 + 256 x 192 = 65536, as at launch (512 x 128)
+constexpr int F_FEW_REGS = 56, F_SCALE_REGS = 72, F_MANY_REGS = 192;
+constexpr int F_AHEAD = 6;         // K blocks whose scales are under way: one load takes
+                                   // about 1000 clocks, two K blocks of MMAs
+constexpr int F_SCALE_WARPS = 4, F_OUT_WARPS = 8;
 constexpr int F_TILE = 256;        // pair tile rows and columns
+constexpr int F_STAGES = 6;
 constexpr int F_STAGE_BYTES = 2 * F8_BOX_BYTES;
-constexpr int F_STORE_BYTES = F_EPI_WARPS * 4096;  // per warp: 2 bf16 boxes or 1 fp32 box
 constexpr int F_TMEM_COLS = 512;
-
-template <int OUT>
-struct Cfg {
-    static constexpr bool kVec = OUT == F8_F32_VECTOR;
-    static constexpr int kStages = kVec ? 5 : 6;
-    // column factors: two K blocks of 128 floats per warp
-    static constexpr int kColBytes = kVec ? F_EPI_WARPS * 2 * 512 : 0;
-    static constexpr int kSmem = 1024 + kStages * F_STAGE_BYTES + F_STORE_BYTES + kColBytes + 256;
-};
-static_assert(Cfg<F8_BF16_BLOCK>::kSmem <= 232448 && Cfg<F8_F32_VECTOR>::kSmem <= 232448, "fits a CTA");
+constexpr int F_SCALE_COL = 256;   // first column of the scale slots, 16 columns each:
+constexpr int F_SCALE_B = 4;       // A's 4, then B's 8
+constexpr int F_BIAS = F_OUT_WARPS * 512;   // each output warp's 128 columns, fp32
+constexpr int F_TURN = F_OUT_WARPS * 2048;  // and 32 rows of 64 output bytes
+constexpr int F_SWAP = 2 * 32 * 12 * 4;     // scale words of two K blocks: [c / 4][lane][c % 4]
+constexpr int F_SMEM = 1024 + F_STAGES * F_STAGE_BYTES + F_BIAS + F_TURN + F_SWAP + 256;
+static_assert(F_SMEM <= 232448, "fits a CTA");
 
 __device__ __forceinline__ void decode(const Fp8GemmParams& p, int tile, int& g, int& m0, int& n0) {
     // bands of `band` M-tiles, M fastest: the pairs running together share B
@@ -73,12 +73,6 @@ __device__ __forceinline__ int pick(int part, int g, int s) {
     return part == F8_GROUP ? g : part == F8_KSEG ? s : 0;
 }
 
-// 128 x 128-byte box of an operand: rows from `row`, K from k0
-__device__ __forceinline__ void load_box(const CUtensorMap* m, int mn, int row, int k0, uint32_t dst,
-                                         uint32_t bar) {
-    ptx::tma_load_2d_pair(dst, m, mn ? row : k0, mn ? k0 : row, bar);
-}
-
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
@@ -87,23 +81,21 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 template <int OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
-    using C = Cfg<OUT>;
-    constexpr int NST = C::kStages;
+    constexpr bool F32 = OUT == F8_F32_VECTOR;
+    constexpr int NST = F_STAGES;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t* gbase = smem_raw + (base - raw);
-    const uint32_t store0 = base + NST * F_STAGE_BYTES;
-    uint8_t* col_area = gbase + NST * F_STAGE_BYTES + F_STORE_BYTES;
-    const uint32_t bar0 = store0 + F_STORE_BYTES + C::kColBytes;
-    uint8_t* bar_area = col_area + C::kColBytes;
-    const uint32_t bar_full = bar0;              // [NST] used in the even CTA
+    uint8_t* after = smem_raw + (base - raw) + NST * F_STAGE_BYTES;
+    const uint32_t bar0 = base + NST * F_STAGE_BYTES + F_BIAS + F_TURN + F_SWAP;
+    uint8_t* bar_area = after + F_BIAS + F_TURN + F_SWAP;
+    const uint32_t bar_full = bar0;              // [NST] even CTA: both CTAs' operands and scales
     const uint32_t bar_empty = bar0 + 8 * NST;   // [NST] both CTAs
-    const uint32_t bar_tfull = bar0 + 16 * NST;  // [2] both CTAs
-    const uint32_t bar_tempty = bar_tfull + 16;  // [2] used in the even CTA
-    const uint32_t bar_drain = bar_tempty + 16;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 16 * NST + 40);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_area + 16 * NST + 44);
+    const uint32_t bar_done = bar0 + 16 * NST;   // both CTAs: the tile is in the accumulator
+    const uint32_t bar_free = bar_done + 8;      // even CTA: both CTAs have read it
+    const uint32_t bar_drain = bar_free + 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 16 * NST + 24);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_area + 16 * NST + 28);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(ptx::cluster_ctarank());
@@ -111,13 +103,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_full + 8 * s, 1 + 2 * F_SCALE_WARPS);
             ptx::mbar_init(bar_empty + 8 * s, 1);
         }
-        for (int a = 0; a < 2; ++a) {
-            ptx::mbar_init(bar_tfull + 8 * a, 1);
-            ptx::mbar_init(bar_tempty + 8 * a, 2 * F_EPI_WARPS);
-        }
+        ptx::mbar_init(bar_done, 1);
+        ptx::mbar_init(bar_free, 2 * F_OUT_WARPS);
         ptx::mbar_init(bar_drain, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -140,6 +130,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     if (warp < 4) {
         reg_dec<F_FEW_REGS>();
         if (warp == 0 && lane == 0) {
+            // ---------------- TMA producer ----------------
             const uint32_t even_full = ptx::mapa_shared(bar_full, 0);
             int stage = 0;
             uint32_t phase = 0;
@@ -154,17 +145,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     const CUtensorMap* am = p.a_map + pick(p.a_part, g, s);
                     const CUtensorMap* bm = p.b_map + pick(p.b_part, g, s);
                     for (int kb = 0; kb < kblocks; ++kb) {
-                        if (!wait<false>(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.timeout_ns,
-                                         p.err, ERR_PRODUCER)) {
+                        if (!wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.timeout_ns, p.err,
+                                  ERR_PRODUCER)) {
                             ok = false;
                             break;
                         }
-                        const uint32_t sa = base + stage * F_STAGE_BYTES;
-                        if (rank == 0)
+                        const uint32_t sa = base + stage * F_STAGE_BYTES, full = even_full + 8 * stage;
+                        const int k0 = kb * F8_BK;
+                        if (rank == 0)  // counts both CTAs' bytes
                             ptx::mbar_arrive_expect_tx(bar_full + 8 * stage, 2 * F_STAGE_BYTES);
-                        load_box(am, p.a_mn, arow, kb * F8_BK, sa, even_full + 8 * stage);
-                        load_box(bm, p.b_mn, brow, kb * F8_BK, sa + F8_BOX_BYTES,
-                                 even_full + 8 * stage);
+                        ptx::tma_load_2d_pair(sa, am, p.a_mn ? arow : k0, p.a_mn ? k0 : arow, full);
+                        ptx::tma_load_2d_pair(sa + F8_BOX_BYTES, bm, p.b_mn ? brow : k0,
+                                              p.b_mn ? k0 : brow, full);
                         ++fills;
                         if (++stage == NST) {
                             stage = 0;
@@ -191,170 +183,218 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 }
             }
         } else if (warp == 1 && lane == 0 && rank == 0) {
+            // ---------------- MMA issuer ----------------
             const uint32_t id = idesc(F_TILE, F_TILE, p.a_mn, p.b_mn) | p.ab_format;
             int stage = 0;
-            uint32_t phase = 0;
-            long long blk = 0;  // K blocks issued
+            uint32_t phase = 0, tiles = 0;
             bool ok = true;
-            for (int tile = cluster; ok && tile < p.total_tiles; tile += nclusters) {
-                for (int kk = 0; kk < nk; ++kk, ++blk) {
-                    const int acc = static_cast<int>(blk & 1);
-                    if (!wait<true>(bar_tempty + 8 * acc, static_cast<uint32_t>((blk >> 1) & 1) ^ 1u,
-                                    abort_flag, p.timeout_ns, p.err, ERR_MMA) ||
-                        !wait<false>(bar_full + 8 * stage, phase, abort_flag, p.timeout_ns, p.err,
-                                     ERR_MMA)) {
+            for (int tile = cluster; ok && tile < p.total_tiles; tile += nclusters, ++tiles) {
+                if (!wait(bar_free, (tiles & 1) ^ 1u, abort_flag, p.timeout_ns, p.err, ERR_MMA)) {
+                    ok = false;
+                    break;
+                }
+                for (int kk = 0; kk < nk; ++kk) {
+                    if (!wait(bar_full + 8 * stage, phase, abort_flag, p.timeout_ns, p.err, ERR_MMA)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
                     const uint32_t sa = base + stage * F_STAGE_BYTES;
+                    const uint32_t sf = tmem + F_SCALE_COL + stage * 16;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_pair(tmem + acc * 256, operand_desc(sa, k, p.a_mn),
-                                 operand_desc(sa + F8_BOX_BYTES, k, p.b_mn), id, k > 0 ? 1u : 0u);
+                        mma_pair(tmem, operand_desc(sa, k, p.a_mn),
+                                 operand_desc(sa + F8_BOX_BYTES, k, p.b_mn), id, sf, sf + F_SCALE_B,
+                                 (kk > 0 || k > 0) ? 1u : 0u);
                     ptx::mma_commit_pair_multicast(bar_empty + 8 * stage, 0x3);
-                    ptx::mma_commit_pair_multicast(bar_tfull + 8 * acc, 0x3);
+                    if (++stage == NST) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) ptx::mma_commit_pair_multicast(bar_done, 0x3);
+            }
+            ptx::mma_commit_pair(bar_drain);
+            drain(bar_drain, 0, p.timeout_ns, p.err);
+            // the last release of the accumulator arrives on this CTA
+            if (ok && tiles > 0) drain(bar_free, (tiles - 1) & 1, p.timeout_ns, p.err);
+        }
+    } else if (warp < 8) {
+        // ---------------- scales ----------------
+        reg_dec<F_SCALE_REGS>();
+        const int q = warp & 3;  // its quarter of the lanes
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + F_SCALE_COL;
+        const uint32_t even_full = ptx::mapa_shared(bar_full, 0);
+        uint32_t* swap = reinterpret_cast<uint32_t*>(after + F_BIAS + F_TURN) + lane * 4;
+        int stage = 0, buf = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = cluster; ok && tile < p.total_tiles; tile += nclusters) {
+            int g, m0, n0;
+            decode(p, tile, g, m0, n0);
+            // words 0..3 of a lane: A's rows lane + 32 c; words 4..11: B's.  This warp
+            // fetches words q (A), and 4 + 2q, 5 + 2q (B; a weight's two blocks are
+            // fetched by every warp)
+            const int m = m0 + rank * 128 + lane + 32 * q;
+            const int n = F32 ? n0 + lane + 64 * q : n0;
+            constexpr int NSTEP = F32 ? 32 : 128;
+            int s = 0, kb = 0;
+            float v[F_AHEAD][3];
+            auto fetch = [&](float (&d)[3]) {
+                const float* sa = p.sa[pick(p.a_part, g, s)] + kb * p.sa_kb;
+                const float* sb = p.sb[pick(p.b_part, g, s)] + kb * p.sb_kb;
+                d[0] = m < p.M ? __ldg(sa + m) : 1.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int nn = n + NSTEP * c;
+                    d[1 + c] = nn < p.N ? __ldg(sb + (F32 ? nn : (nn >> 7) * p.sb_n)) : 1.0f;
+                }
+                if (++kb == kblocks) {
+                    kb = 0;
+                    ++s;
+                }
+            };
+#pragma unroll
+            for (int u = 0; u < F_AHEAD; ++u)
+                if (u < nk) fetch(v[u]);
+            for (int k0 = 0; ok && k0 < nk; k0 += F_AHEAD) {
+#pragma unroll
+                for (int u = 0; u < F_AHEAD; ++u) {
+                    if (!ok || k0 + u >= nk) break;
+                    uint32_t* sw = swap + buf * (32 * 12);
+                    buf ^= 1;
+                    uint32_t w[12];
+                    sw[q] = scale_word(v[u][0]);
+                    w[4] = scale_word(v[u][1]);
+                    w[5] = scale_word(v[u][2]);
+                    if (F32) {
+                        const int c = 4 + 2 * q;
+                        *reinterpret_cast<uint2*>(sw + (c >> 2) * 128 + (c & 3)) = make_uint2(w[4], w[5]);
+                    }
+                    if (k0 + u + F_AHEAD < nk) fetch(v[u]);
+                    // the stage's last MMAs have read its scales
+                    ok = wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.timeout_ns, p.err,
+                              ERR_PRODUCER);
+                    ok = !barrier_any<F_SCALE_WARPS * 32>(!ok);  // the four give up together
+                    if (!ok) break;
+#pragma unroll
+                    for (int c = 0; c < 12; c += 4) {
+                        if (c == 0 || F32) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(sw + (c >> 2) * 128);
+                            w[c] = x.x;
+                            w[c + 1] = x.y;
+                            w[c + 2] = x.z;
+                            w[c + 3] = x.w;
+                        }
+                    }
+                    if (!F32) {
+                        w[8] = w[9] = w[10] = w[11] = w[5];
+                        w[5] = w[6] = w[7] = w[4];
+                    }
+                    ptx::tc_fence_after();
+                    store_cols4(lanes + stage * 16, w);
+                    store_cols8(lanes + stage * 16 + F_SCALE_B, w + 4);
+                    store_wait();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_relaxed_cluster(even_full + 8 * stage);
                     if (++stage == NST) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            ptx::mma_commit_pair(bar_drain);
-            drain(bar_drain, 0, p.timeout_ns, p.err);
-            if (ok) {
-                // the last releases of both accumulators arrive on this CTA
-                for (long long j = (blk > 2 ? blk - 2 : 0); j < blk; ++j)
-                    if (!drain(bar_tempty + 8 * (j & 1), static_cast<uint32_t>((j >> 1) & 1),
-                               p.timeout_ns, p.err))
-                        break;
-            }
         }
     } else {
+        // ---------------- output ----------------
         reg_inc<F_MANY_REGS>();
         const int quarter = warp & 3;         // the accumulator lanes this warp may read
-        const int half = (warp - 4) >> 2;     // its 128 columns
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
-        const uint32_t even_tempty = ptx::mapa_shared(bar_tempty, 0);
-        uint8_t* store = gbase + NST * F_STAGE_BYTES + (warp - 4) * 4096;
-        const uint32_t store_u32 = store0 + (warp - 4) * 4096;
-        float* colbuf = reinterpret_cast<float*>(col_area + (warp - 4) * 1024);
-        long long blk = 0;
-        bool ok = true;
-        for (int tile = cluster; ok && tile < p.total_tiles; tile += nclusters) {
+        const int side = (warp - 8) >> 2;     // its 128 columns
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + side * 128;
+        const uint32_t even_free = ptx::mapa_shared(bar_free, 0);
+        float* bias_buf = reinterpret_cast<float*>(after) + (warp - 8) * 128;
+        uint8_t* turn = after + F_BIAS + (warp - 8) * 2048;
+        uint32_t tiles = 0;
+        for (int tile = cluster; tile < p.total_tiles; tile += nclusters, ++tiles) {
             int g, m0, n0;
             decode(p, tile, g, m0, n0);
             const int row0 = m0 + rank * 128 + quarter * 32;
-            const int m = row0 + lane, n = n0 + half * 128;
-            const bool row_in = m < p.M, col_in = n < p.N;
-            uint64_t acc[64];
-#pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0;
-            // scales of K block (s, kb), fetched one block ahead
-            auto scales = [&](int s, int kb, float& a, float& b, float4& bv) {
-                a = row_in ? __ldg(p.sa[pick(p.a_part, g, s)] + kb * p.sa_kb + m) : 0.0f;
-                const float* sb = p.sb[pick(p.b_part, g, s)] + kb * p.sb_kb;
-                if constexpr (C::kVec) {
-                    const int nn = n + lane * 4;
-                    bv = nn < p.N ? __ldg(reinterpret_cast<const float4*>(sb + nn))
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-                } else {
-                    b = col_in ? __ldg(sb + (n >> 7) * p.sb_n) : 0.0f;
-                }
-            };
-            float a = 0.0f, b = 1.0f;
-            float4 bv = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (nk > 0) scales(0, 0, a, b, bv);
-            int s = 0, kb = 0;
-            for (int kk = 0; kk < nk; ++kk, ++blk) {
-                const float scale = a * b;
-                float* cb = colbuf + (blk & 1) * 128;
-                if constexpr (C::kVec) {
-                    // two buffers: the lanes that still read the other one are at most a block behind
-                    *reinterpret_cast<float4*>(cb + lane * 4) = bv;
-                    __syncwarp();
-                }
-                if (++kb == kblocks) {
-                    kb = 0;
-                    ++s;
-                }
-                if (kk + 1 < nk) scales(s, kb, a, b, bv);
-                const int ab = static_cast<int>(blk & 1);
-                ok = wait<false>(bar_tfull + 8 * ab, static_cast<uint32_t>((blk >> 1) & 1),
-                                 abort_flag, p.timeout_ns, p.err, ERR_EPILOGUE);
-                ok = __all_sync(0xffffffffu, ok);  // the warp gives up together
-                if (!ok) break;
-                ptx::tc_fence_after();
-                promote<128, C::kVec>(lanes + ab * 256, scale,
-                                      reinterpret_cast<const uint64_t*>(cb), acc);
-                ptx::tc_fence_before();
+            const int n = n0 + side * 128;
+            if constexpr (!F32) {
+                // four columns of the bias per lane, under the MMAs
+                uint2 u = make_uint2(0, 0);
+                if (p.bias && n + lane * 4 < p.N)
+                    u = __ldg(reinterpret_cast<const uint2*>(
+                        static_cast<const __nv_bfloat16*>(p.bias) + static_cast<long long>(g) * p.N +
+                        n + lane * 4));
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(even_tempty + 8 * ab);
+                *reinterpret_cast<float4*>(bias_buf + lane * 4) =
+                    make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                                __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+                __syncwarp();
             }
+            bool ok = wait(bar_done, tiles & 1, abort_flag, p.timeout_ns, p.err, ERR_EPILOGUE);
+            ok = __all_sync(0xffffffffu, ok);  // the warp gives up together
             if (!ok) break;
-            // output: 32 columns at a time through this warp's staging box
-            if (!col_in || row0 >= p.M) continue;
+            ptx::tc_fence_after();
+            float acc[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) load_cols(lanes + c * 32, acc + c * 32);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 128; ++i) asm volatile("" : "+f"(acc[i]));  // used after the wait
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_relaxed_cluster(even_free);
+
+            // 64 bytes of each of the warp's 32 rows at a time are turned round in
+            // shared memory and leave as whole sectors, 8 rows to a store
+            // instruction.  (Bulk stores waited for each other's staging, 8600
+            // clocks a tile; each thread storing along its own row, 32 rows to an
+            // instruction, took 9800; this takes 4100; measured.)
+            if (n >= p.N || row0 >= p.M) continue;
             int part = g, y0 = row0;
             if (p.chunk_rows > 0) {
                 part = row0 / p.chunk_rows;
                 y0 -= part * p.chunk_rows;
             }
-            const __nv_bfloat16* bias =
-                p.bias ? static_cast<const __nv_bfloat16*>(p.bias) + static_cast<long long>(g) * p.N
-                       : nullptr;
+            constexpr int ELEM = F32 ? 4 : 2;
+            constexpr int W = 64 / ELEM, V = 16 / ELEM;  // columns a step, columns a vector
+            uint8_t* out = static_cast<uint8_t*>(p.out[part]) +
+                           (static_cast<long long>(y0) * p.N + n) * ELEM;
+            const int sw = (lane >> 1) & 3, rr = lane >> 2, rv = lane & 3;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int nn = n + c * 32;
-                if (nn < p.N) {
-                    float x[32];
+            for (int c = 0; c < 128 / W; ++c) {
+                if (n + c * W < p.N) {  // (the same for the whole warp)
+                    __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) unpack2(acc[c * 16 + i], x[2 * i], x[2 * i + 1]);
-                    uint8_t* box = C::kVec ? store : store + (c & 1) * 2048;
-                    const uint32_t box_u32 = C::kVec ? store_u32 : store_u32 + (c & 1) * 2048;
-                    if (lane == 0) {
-                        if (C::kVec) ptx::bulk_wait_group_read<0>();
-                        else ptx::bulk_wait_group_read<1>();
+                    for (int q = 0; q < 4; ++q) {
+                        const float* x = acc + c * W + q * V;
+                        uint4 u;
+                        if constexpr (F32) {
+                            u = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                           __float_as_uint(x[2]), __float_as_uint(x[3]));
+                        } else {
+                            const float4* b = reinterpret_cast<const float4*>(bias_buf + c * W + q * V);
+                            const float4 b0 = b[0], b1 = b[1];
+                            u = make_uint4(bf16x2(x[0] + b0.x, x[1] + b0.y), bf16x2(x[2] + b0.z, x[3] + b0.w),
+                                           bf16x2(x[4] + b1.x, x[5] + b1.y), bf16x2(x[6] + b1.z, x[7] + b1.w));
+                        }
+                        *reinterpret_cast<uint4*>(turn + lane * 64 + ((q ^ sw) << 4)) = u;
                     }
                     __syncwarp();
-                    if constexpr (C::kVec) {
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            *reinterpret_cast<float4*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-                                make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-                    } else {
-                        if (bias) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                if (nn + 8 * q < p.N) {
-                                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(bias + nn + 8 * q));
-                                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) {
-                                        x[8 * q + 2 * j] += __uint_as_float(w[j] << 16);
-                                        x[8 * q + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
-                                    }
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const float* f = x + 8 * q;
-                            *reinterpret_cast<uint4*>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-                                make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]),
-                                           bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
-                        }
-                    }
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        ptx::tma_store_2d(&p.out_map[part], box_u32, nn, y0);
-                        ptx::bulk_commit_group();
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = rr + 8 * i;
+                        const uint4 u = *reinterpret_cast<const uint4*>(
+                            turn + r * 64 + ((rv ^ ((r >> 1) & 3)) << 4));
+                        if (row0 + r < p.M && n + c * W + rv * V < p.N)
+                            *reinterpret_cast<uint4*>(out + static_cast<long long>(r) * p.N * ELEM +
+                                                      c * 64 + rv * 16) = u;
                     }
                 }
             }
         }
-        if (lane == 0) ptx::bulk_wait_group<0>();
-        __syncwarp();
     }
 
     ptx::tc_fence_before();
@@ -379,12 +419,12 @@ cudaError_t max_clusters(int& out) {
     int n = __atomic_load_n(&known[dev], __ATOMIC_ACQUIRE);
     if (n == 0) {
         auto kern = fp8_gemm_kernel<OUT>;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<OUT>::kSmem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F_SMEM);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2, 1, 1);
         cfg.blockDim = dim3(F_THREADS, 1, 1);
-        cfg.dynamicSmemBytes = Cfg<OUT>::kSmem;
+        cfg.dynamicSmemBytes = F_SMEM;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = 2;
@@ -410,7 +450,7 @@ cudaError_t launch(const Fp8GemmParams& p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters, 1, 1);
     cfg.blockDim = dim3(F_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = Cfg<OUT>::kSmem;
+    cfg.dynamicSmemBytes = F_SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -4,7 +4,8 @@
 //     C_g[m, n] = sum_s sum_kb sa[kb, m] * sb[kb, n] * sum_{k in kb} A[m, k] B[n, k]   (+ bias[n])
 //
 // over K blocks of 128, with A's scale per row and K block and B's either per
-// 128 columns and K block (weights) or per column and K block (activations).
+// 128 columns and K block (weights) or per column and K block (activations);
+// the scales are powers of two (any other reads as NaN).
 // Groups g share a launch (column-parallel shards), segments s are summed into
 // the same output (row-parallel shards), as in the bf16 GEMM.  Operands are
 // 8-bit matrices, K-major (row-major [rows, K]) or MN-major (row-major
@@ -32,7 +33,7 @@ enum Fp8Out : int {
 struct Fp8GemmParams {
     CUtensorMap a_map[F8_MAX_MAPS];
     CUtensorMap b_map[F8_MAX_MAPS];
-    CUtensorMap out_map[F8_MAX_MAPS];  // 32 x 32 store boxes: per group, or per token chunk
+    void* out[F8_MAX_MAPS];            // [M, N] per group, or [chunk_rows, N] per token chunk
     const float* sa[F8_MAX_MAPS];      // A's scales: [kb * sa_kb + m]
     const float* sb[F8_MAX_MAPS];      // B's: [kb * sb_kb + (n / 128) * sb_n] or [kb * sb_kb + n]
     long long sa_kb, sb_kb, sb_n;

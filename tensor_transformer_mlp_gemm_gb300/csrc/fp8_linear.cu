@@ -139,10 +139,7 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int kind, cuda
         if (!encode_operand(&p.b_map[i], d.b, i, d.K, d.N)) return TPMLP_ERR_UNSUPPORTED;
         p.sb[i] = static_cast<const float*>(d.b.s[i]);
     }
-    const bool f32 = d.out_kind == F8_F32_VECTOR;
-    for (int i = 0; i < d.nout; ++i)
-        if (!encode_out(&p.out_map[i], d.out[i], d.N, d.chunk_rows > 0 ? d.chunk_rows : d.M, f32))
-            return TPMLP_ERR_UNSUPPORTED;
+    for (int i = 0; i < d.nout; ++i) p.out[i] = d.out[i];
     p.sa_kb = d.sa_kb;
     p.sb_kb = d.sb_kb;
     p.sb_n = d.sb_n;

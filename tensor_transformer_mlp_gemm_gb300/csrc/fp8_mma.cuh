@@ -1,6 +1,16 @@
 // fp8_mma.cuh -- device pieces of the 8-bit products: the tcgen05 instructions
-// for 8-bit operands, bounded waits, and the promotion of a K block's partial
-// sums from tensor memory into scaled fp32 sums.
+// for 8-bit operands with block scales, the scales' way into tensor memory, and
+// bounded waits.
+//
+// tcgen05.mma.kind::mxf8f6f4.block_scale multiplies every 32 elements of K of a
+// row of A and of B by a power of two each, given as 8-bit exponents (biased by
+// 127, 255 = NaN) in tensor memory, and accumulates in fp32.  A scale of 128
+// elements is that of its four slices of 32.
+//
+// Scales of 128 rows take 4 columns of tensor memory: row r in lane r % 32,
+// column r / 32, and the 32 lanes' words again in each of the other three
+// quarters of the lanes.  A word holds four exponents, of which the instruction
+// picks one; here all four are the same.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -14,24 +24,28 @@
 namespace tpmlp {
 namespace f8 {
 
-// D[tmem] (+)= A[smem] x B[smem], 8-bit floating-point operands, fp32 sums; the
-// pair form is issued by the even CTA.
+// D[tmem] (+)= (A x scale_A) x (B x scale_B); the pair form is issued by the even
+// CTA and takes each CTA's own rows of A with their scales, and from each CTA half
+// the rows of B, whose scales both CTAs hold in full.
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                         uint32_t idesc, uint32_t accumulate) {
+                                         uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
+                                         uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
         : "memory");
 }
 
-// Instruction descriptor of kind::f8f6f4 with an fp32 accumulator.
-//   bits 4-5 D format (1 = f32); 7-9 A format, 10-12 B format (0 = e4m3, 1 = e5m2);
-//   bit 15 A is MN-major; bit 16 B is MN-major; 17-22 N >> 3; 24-28 M >> 4.
+// Instruction descriptor of kind::mxf8f6f4 with an fp32 accumulator.
+//   bits 4-5, 29-30 which exponent of a scale word is B's, A's (the first);
+//   7-9 A format, 10-12 B format (0 = e4m3, 1 = e5m2); bit 15 A is MN-major, 16 B;
+//   17-22 N >> 3; bit 23 the scales are 8-bit exponents; 27-28 M >> 7.
 __host__ __device__ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
-    return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
-           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+    return (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 7) << 27);
 }
 
 // Descriptor of the 32-wide K slice kk (0..3) of a 128 x 128-byte operand box.
@@ -43,18 +57,39 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t tile, int kk, int mn) 
     return ptx::smem_desc_sw128(tile + (mn ? kk * 4096 : kk * 32), mn ? F8_BOX_BYTES : 16, 1024);
 }
 
+// A scale's word: its exponent four times; NaN (255) for anything but a positive
+// power of two.
+__device__ __forceinline__ uint32_t scale_word(float s) {
+    const uint32_t u = __float_as_uint(s), e = u >> 23;
+    const bool ok = (u & 0x007FFFFFu) == 0 && e >= 1 && e <= 254;
+    return (ok ? e : 255u) * 0x01010101u;
+}
+constexpr uint32_t kScaleOne = 127u * 0x01010101u;
+
+// This thread's lane of its warp's quarter: 4 and 8 consecutive columns.
+__device__ __forceinline__ void store_cols4(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+__device__ __forceinline__ void store_cols8(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        : "memory");
+}
+__device__ __forceinline__ void store_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // Waits for phase `parity` of `bar`; gives up (false) when another role has, or
 // after the limit (then this one aborts the CTA and sets `code` in the error word).
-template <bool CLUSTER>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                      unsigned long long timeout_ns, unsigned* err, unsigned code) {
-    auto done = [&] {
-        return CLUSTER ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
-    };
-    if (done()) return true;
+    if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer_ns();
     while (true) {
-        if (done()) return true;
+        if (ptx::mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (ptx::globaltimer_ns() - t0 > timeout_ns) {
             *abort_flag = 1;
@@ -77,6 +112,30 @@ __device__ __forceinline__ bool drain(uint32_t bar, uint32_t parity, unsigned lo
     return true;
 }
 
+// Arrive on an mbarrier of either CTA of the pair without ordering this thread's
+// memory accesses: it only says that tensor memory has been read or written,
+// which the waits and the fence before it order.  (A release at cluster scope
+// waits for the thread's outstanding global loads too: 2000 clocks, measured.)
+__device__ __forceinline__ void arrive_relaxed_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+
+// Barrier 1 of `threads` threads of the CTA; whether any of them came with `fail`.
+template <int THREADS>
+__device__ __forceinline__ bool barrier_any(bool fail) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred q, r;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "barrier.cta.red.or.pred r, 1, %2, q;\n\t"
+        "selp.u32 %0, 1, 0, r;\n\t}"
+        : "=r"(r)
+        : "r"(fail ? 1u : 0u), "n"(THREADS)
+        : "memory");
+    return r != 0;
+}
+
 // Registers per thread of the calling warpgroup (all of its warps call it).
 template <int N>
 __device__ __forceinline__ void reg_dec() {
@@ -87,48 +146,18 @@ __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// ---- packed fp32 pairs -----------------------------------------------------------
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-// acc[0..C) += scale * (C columns of this thread's tensor-memory lane), C a
-// multiple of 32 (acc holds pairs).  VEC: times column factors too, read from
-// shared memory as pairs (every lane reads the same ones).
-template <int C, bool VEC>
-__device__ __forceinline__ void promote(uint32_t taddr, float scale, const uint64_t* col,
-                                        uint64_t (&acc)[C / 2]) {
-    const uint64_t s2 = pack2(scale, scale);
-#pragma unroll
-    for (int c = 0; c < C / 32; ++c) {
-        uint32_t v[32];
-        ptx::tmem_ld_32x32b_x32(taddr + c * 32, v);
-        ptx::tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint64_t x = pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            if constexpr (VEC) {
-                acc[c * 16 + i] = fma2(x, mul2(col[c * 16 + i], s2), acc[c * 16 + i]);
-            } else {
-                acc[c * 16 + i] = fma2(x, s2, acc[c * 16 + i]);
-            }
-        }
-    }
+// 32 columns of this thread's tensor-memory lane into v (usable after load_wait).
+__device__ __forceinline__ void load_cols(uint32_t taddr, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+          "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+          "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+          "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
 }
 
 }  // namespace f8

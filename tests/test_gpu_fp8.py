@@ -235,6 +235,75 @@ def test_linear(split, T, din, dout, t, chunks):
     _check_backward(lay, x, dY, "e4m3")
 
 
+@pytest.mark.parametrize("split,T,din,dout,t", [
+    ("column", 3, 400, 784, 1), ("row", 40, 784, 400, 1), ("column", 130, 528, 1056, 2),
+    ("row", 700, 1552, 656, 1), ("column", 515, 656, 1040, 1)])
+def test_linear_scales_of_every_row(split, T, din, dout, t):
+    """Every token, feature and weight block at a magnitude of its own, so that a
+    scale taken from a wrong row, column or block shows."""
+    from tensor_transformer_mlp_gemm_gb300 import fp8
+    w = custom_linear(T, din, dout, t, split)
+    lay, X, dY = _layer(w, 77)
+    g = _gen(78)
+
+    def spread(x, rows, cols):
+        def f(n, step):
+            e = torch.randint(-12, 13, (-(-n // step),), generator=g, device="cuda")
+            return torch.ldexp(torch.ones_like(e, dtype=torch.float32), e).repeat_interleave(step)[:n]
+        return (x.float() * f(x.shape[0], rows)[:, None] * f(x.shape[1], cols)).to(torch.bfloat16)
+
+    X = [spread(x, 1, 1) for x in X]
+    dY = [spread(x, 1, 1) for x in dY]
+    for i in range(t):
+        W = spread(_randn(g, *lay.Wq[i].shape), 128, 128)
+        q, s = fp8.quantize_weight(W)
+        lay.Wq[i].copy_(q)
+        lay.Ws[i].copy_(s)
+    x = lay.quantize(X, cols=True)
+    lay.forward(x)
+    lay.backward(dY, x)
+    _sync()
+    _check_forward(lay, x)
+    _check_backward(lay, x, dY, "e4m3")
+
+
+@pytest.mark.parametrize("T", [9, 300])
+def test_linear_not_finite(T):
+    """NaN where, and only where, a group that is not finite takes part."""
+    w = custom_linear(T, 400, 528, 1, "column")
+    lay, X, dY = _layer(w, 21)
+    X[0][3, 200] = float("inf")
+    dY[0][5, 7] = float("nan")
+    x = lay.quantize(X, cols=True)
+    lay.forward(x)
+    lay.backward(dY, x)
+    _sync()
+    nan = torch.isnan(lay.Y[0])
+    assert nan[3].all() and int(nan.sum()) == w.out_features
+    nan = torch.isnan(lay.dX[0])
+    assert nan[5].all() and int(nan.sum()) == w.in_features
+    nan = torch.isnan(lay.dW[0])
+    assert nan[200].all() and nan[:, 7].all()
+    assert int(nan.sum()) == w.in_features + w.out_features - 1
+    assert torch.isnan(lay.db[7]) and int(torch.isnan(lay.db).sum()) == 1
+
+
+@pytest.mark.parametrize("T", [4, 260])
+def test_linear_other_scales_read_as_nan(T):
+    """A scale that is not a positive power of two is never taken for another."""
+    w = custom_linear(T, 256, 384, 1, "column")
+    lay, X, _ = _layer(w, 31)
+    x = lay.quantize(X)
+    for j, bad in enumerate([0.75, -1.0, 0.0]):
+        keep = float(lay.Ws[0][1, 1])
+        lay.Ws[0][1, 1] = bad
+        lay.forward(x)
+        _sync()
+        nan = torch.isnan(lay.Y[0])
+        assert nan[:, 128:256].all() and int(nan.sum()) == T * 128, bad
+        lay.Ws[0][1, 1] = keep
+
+
 @pytest.mark.parametrize("T", [5, 300])
 @pytest.mark.parametrize("split", ["column", "row"])
 def test_linear_mixed_formats(split, T):
