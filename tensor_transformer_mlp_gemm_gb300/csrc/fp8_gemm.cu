@@ -14,8 +14,10 @@
 //                four K slices of 32 for each K block
 //   warps 4..7   scales: the exponents of this CTA's 128 rows of A and of all 256
 //                rows of B for each K block, into tensor memory, a slot per stage.
-//                Each warp fetches a quarter of them, they are exchanged in shared
-//                memory, and each writes all of them to its quarter of the lanes
+//                Each warp copies a quarter of them to a ring in shared memory, six
+//                to eight K blocks ahead, and writes all of them to its quarter of
+//                the lanes, two K blocks at a time (one at a time, loaded into
+//                registers, took 750 to 1100 clocks a block)
 //   warps 8..15  output: warp w reads lanes 32 (w % 4) .. of the accumulator and
 //                columns 128 ((w - 8) / 4) .. into registers, frees the accumulator
 //                for the next tile's MMAs, and writes from there
@@ -42,8 +44,6 @@ using namespace f8;
 constexpr int F_THREADS = 512;
 // registers per thread: 128 x 56 + 128 x 72 + 256 x 192 = 65536, as at launch (512 x 128)
 constexpr int F_FEW_REGS = 56, F_SCALE_REGS = 72, F_MANY_REGS = 192;
-constexpr int F_AHEAD = 6;         // K blocks whose scales are under way: one load takes
-                                   // about 1000 clocks, two K blocks of MMAs
 constexpr int F_SCALE_WARPS = 4, F_OUT_WARPS = 8;
 constexpr int F_TILE = 256;        // pair tile rows and columns
 constexpr int F_STAGES = 6;
@@ -53,7 +53,10 @@ constexpr int F_SCALE_COL = 256;   // first column of the scale slots, 16 column
 constexpr int F_SCALE_B = 4;       // A's 4, then B's 8
 constexpr int F_BIAS = F_OUT_WARPS * 512;   // each output warp's 128 columns, fp32
 constexpr int F_TURN = F_OUT_WARPS * 2048;  // and 32 rows of 64 output bytes
-constexpr int F_SWAP = 2 * 32 * 12 * 4;     // scale words of two K blocks: [c / 4][lane][c % 4]
+constexpr int F_BATCH = 2;       // K blocks the scale warps take at a time
+constexpr int F_RING = 4;        // batches in their ring
+constexpr int F_SLOT = 32 * 12 * 4;  // scales of a K block: [c / 4][lane][c % 4], c as below
+constexpr int F_SWAP = F_RING * F_BATCH * F_SLOT;
 constexpr int F_SMEM = 1024 + F_STAGES * F_STAGE_BYTES + F_BIAS + F_TURN + F_SWAP + 256;
 static_assert(F_SMEM <= 232448, "fits a CTA");
 
@@ -225,86 +228,129 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const int q = warp & 3;  // its quarter of the lanes
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + F_SCALE_COL;
         const uint32_t even_full = ptx::mapa_shared(bar_full, 0);
-        uint32_t* swap = reinterpret_cast<uint32_t*>(after + F_BIAS + F_TURN) + lane * 4;
-        int stage = 0, buf = 0;
+        const uint8_t* ring = after + F_BIAS + F_TURN;
+        const uint32_t ring_u32 = base + NST * F_STAGE_BYTES + F_BIAS + F_TURN;
+        // Scales 0..3 of a lane are A's rows lane + 32 c, 4..11 B's rows lane + 32 (c - 4).
+        // This warp fetches A's c = q and B's 4 + 2q, 5 + 2q; of a weight, whose 128 rows
+        // have one scale, two lanes of warp 0 fetch two.
+        struct {
+            int tile, seg, kb, m, n, g;
+            const float *a, *b;
+        } f;
+        f.tile = cluster;
+        auto start_segment = [&] {
+            f.a = p.sa[pick(p.a_part, f.g, f.seg)] + f.m;
+            f.b = p.sb[pick(p.b_part, f.g, f.seg)] + (F32 ? f.n : (f.n >> 7) * p.sb_n);
+        };
+        auto start_tile = [&] {
+            int m0, n0;
+            decode(p, f.tile, f.g, m0, n0);
+            f.m = m0 + rank * 128 + lane + 32 * q;
+            f.n = F32 ? n0 + lane + 64 * q : n0 + 128 * lane;
+            f.seg = f.kb = 0;
+            start_segment();
+        };
+        if (f.tile < p.total_tiles) start_tile();
+        auto fetch = [&](uint32_t slot) {
+            if (f.tile >= p.total_tiles) return;
+            const uint32_t dst = ring_u32 + slot * F_SLOT + lane * 16;
+            copy4(dst + q * 4, f.m < p.M ? f.a : p.sa[0], f.m < p.M);
+            if constexpr (F32) {
+                const int c = 2 * q;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool in = f.n + 32 * i < p.N;
+                    copy4(dst + 512 + (c >> 2) * 512 + ((c & 3) + i) * 4, in ? f.b + 32 * i : p.sb[0], in);
+                }
+            } else if (q == 0 && lane < 2) {
+                copy4(ring_u32 + slot * F_SLOT + 512 + lane * 4, f.n < p.N ? f.b : p.sb[0], f.n < p.N);
+            }
+            f.a += p.sa_kb;
+            f.b += p.sb_kb;
+            if (++f.kb == kblocks) {
+                f.kb = 0;
+                if (++f.seg == p.ksegs) {
+                    f.tile += nclusters;
+                    if (f.tile < p.total_tiles) start_tile();
+                } else {
+                    start_segment();
+                }
+            }
+        };
+        auto fetch_batch = [&](uint32_t batch) {
+#pragma unroll
+            for (int u = 0; u < F_BATCH; ++u) fetch((batch % F_RING) * F_BATCH + u);
+            copy_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < F_RING - 1; ++i) fetch_batch(i);
+        const int tiles = cluster < p.total_tiles ? (p.total_tiles - cluster - 1) / nclusters + 1 : 0;
+        const long long blocks = static_cast<long long>(tiles) * nk;
+        int stage = 0;
         uint32_t phase = 0;
-        bool ok = true;
-        for (int tile = cluster; ok && tile < p.total_tiles; tile += nclusters) {
-            int g, m0, n0;
-            decode(p, tile, g, m0, n0);
-            // words 0..3 of a lane: A's rows lane + 32 c; words 4..11: B's.  This warp
-            // fetches words q (A), and 4 + 2q, 5 + 2q (B; a weight's two blocks are
-            // fetched by every warp)
-            const int m = m0 + rank * 128 + lane + 32 * q;
-            const int n = F32 ? n0 + lane + 64 * q : n0;
-            constexpr int NSTEP = F32 ? 32 : 128;
-            int s = 0, kb = 0;
-            float v[F_AHEAD][3];
-            auto fetch = [&](float (&d)[3]) {
-                const float* sa = p.sa[pick(p.a_part, g, s)] + kb * p.sa_kb;
-                const float* sb = p.sb[pick(p.b_part, g, s)] + kb * p.sb_kb;
-                d[0] = m < p.M ? __ldg(sa + m) : 1.0f;
+        for (long long done = 0; done < blocks; done += F_BATCH) {
+            const uint32_t batch = static_cast<uint32_t>(done / F_BATCH);
+            const int here = blocks - done < F_BATCH ? 1 : F_BATCH;
+            // the stages' last MMAs have read their scales
+            bool ok = wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.timeout_ns, p.err,
+                           ERR_PRODUCER);
+            const int stage2 = stage + 1 == NST ? 0 : stage + 1;
+            const uint32_t phase2 = stage + 1 == NST ? phase ^ 1u : phase;
+            if (here > 1)
+                ok = ok && wait(bar_empty + 8 * stage2, phase2 ^ 1u, abort_flag, p.timeout_ns, p.err,
+                                ERR_PRODUCER);
+            copy_wait<F_RING - 2>();
+            // this batch has arrived and the one before it has been read by all four
+            // warps, which also give up together
+            if (barrier_any<F_SCALE_WARPS * 32>(!ok)) break;
+            fetch_batch(batch + F_RING - 1);
+            const uint8_t* src = ring + (batch % F_RING) * (F_BATCH * F_SLOT);
+            ptx::tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int nn = n + NSTEP * c;
-                    d[1 + c] = nn < p.N ? __ldg(sb + (F32 ? nn : (nn >> 7) * p.sb_n)) : 1.0f;
-                }
-                if (++kb == kblocks) {
-                    kb = 0;
-                    ++s;
-                }
-            };
-#pragma unroll
-            for (int u = 0; u < F_AHEAD; ++u)
-                if (u < nk) fetch(v[u]);
-            for (int k0 = 0; ok && k0 < nk; k0 += F_AHEAD) {
-#pragma unroll
-                for (int u = 0; u < F_AHEAD; ++u) {
-                    if (!ok || k0 + u >= nk) break;
-                    uint32_t* sw = swap + buf * (32 * 12);
-                    buf ^= 1;
+            for (int u = 0; u < F_BATCH; ++u) {
+                if (u < here) {
+                    const float4* x = reinterpret_cast<const float4*>(src + u * F_SLOT) + lane;
                     uint32_t w[12];
-                    sw[q] = scale_word(v[u][0]);
-                    w[4] = scale_word(v[u][1]);
-                    w[5] = scale_word(v[u][2]);
-                    if (F32) {
-                        const int c = 4 + 2 * q;
-                        *reinterpret_cast<uint2*>(sw + (c >> 2) * 128 + (c & 3)) = make_uint2(w[4], w[5]);
-                    }
-                    if (k0 + u + F_AHEAD < nk) fetch(v[u]);
-                    // the stage's last MMAs have read its scales
-                    ok = wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.timeout_ns, p.err,
-                              ERR_PRODUCER);
-                    ok = !barrier_any<F_SCALE_WARPS * 32>(!ok);  // the four give up together
-                    if (!ok) break;
+                    const float4 x0 = x[0];
+                    w[0] = scale_word(x0.x);
+                    w[1] = scale_word(x0.y);
+                    w[2] = scale_word(x0.z);
+                    w[3] = scale_word(x0.w);
+                    if constexpr (F32) {
 #pragma unroll
-                    for (int c = 0; c < 12; c += 4) {
-                        if (c == 0 || F32) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(sw + (c >> 2) * 128);
-                            w[c] = x.x;
-                            w[c + 1] = x.y;
-                            w[c + 2] = x.z;
-                            w[c + 3] = x.w;
+                        for (int c = 0; c < 2; ++c) {
+                            const float4 y = x[32 * (1 + c)];
+                            w[4 + 4 * c] = scale_word(y.x);
+                            w[5 + 4 * c] = scale_word(y.y);
+                            w[6 + 4 * c] = scale_word(y.z);
+                            w[7 + 4 * c] = scale_word(y.w);
                         }
+                    } else {
+                        const float2 y = *reinterpret_cast<const float2*>(src + u * F_SLOT + 512);
+                        w[4] = w[5] = w[6] = w[7] = scale_word(y.x);
+                        w[8] = w[9] = w[10] = w[11] = scale_word(y.y);
                     }
-                    if (!F32) {
-                        w[8] = w[9] = w[10] = w[11] = w[5];
-                        w[5] = w[6] = w[7] = w[4];
-                    }
-                    ptx::tc_fence_after();
-                    store_cols4(lanes + stage * 16, w);
-                    store_cols8(lanes + stage * 16 + F_SCALE_B, w + 4);
-                    store_wait();
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_relaxed_cluster(even_full + 8 * stage);
-                    if (++stage == NST) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    const uint32_t t = lanes + (u == 0 ? stage : stage2) * 16;
+                    store_cols4(t, w);
+                    store_cols8(t + F_SCALE_B, w + 4);
+                }
+            }
+            store_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                arrive_relaxed_cluster(even_full + 8 * stage);
+                if (here > 1) arrive_relaxed_cluster(even_full + 8 * stage2);
+            }
+#pragma unroll
+            for (int u = 0; u < F_BATCH; ++u) {
+                if (u < here && ++stage == NST) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
         }
+        copy_wait<0>();
     } else {
         // ---------------- output ----------------
         reg_inc<F_MANY_REGS>();

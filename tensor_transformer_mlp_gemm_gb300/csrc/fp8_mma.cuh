@@ -136,6 +136,18 @@ __device__ __forceinline__ bool barrier_any(bool fail) {
     return r != 0;
 }
 
+// ---- asynchronous 4-byte copies into shared memory (zero where !in) ------------------
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Registers per thread of the calling warpgroup (all of its warps call it).
 template <int N>
 __device__ __forceinline__ void reg_dec() {
