@@ -15,9 +15,10 @@
 //   warps 4..7   scales: the exponents of this CTA's 128 rows of A and of all 256
 //                rows of B for each K block, into tensor memory, a slot per stage.
 //                Each warp copies a quarter of them to a ring in shared memory, six
-//                to eight K blocks ahead, and writes all of them to its quarter of
-//                the lanes, two K blocks at a time (one at a time, loaded into
-//                registers, took 750 to 1100 clocks a block)
+//                to nine K blocks ahead, turns them into exponents there, and
+//                writes all of them to its quarter of the lanes, three K blocks at
+//                a time (one at a time, loaded into registers, took 750 to 1100
+//                clocks a block; each warp turning all of them, 840)
 //   warps 8..15  output: warp w reads lanes 32 (w % 4) .. of the accumulator and
 //                columns 128 ((w - 8) / 4) .. into registers, frees the accumulator
 //                for the next tile's MMAs, and writes from there
@@ -53,9 +54,10 @@ constexpr int F_SCALE_COL = 256;   // first column of the scale slots, 16 column
 constexpr int F_SCALE_B = 4;       // A's 4, then B's 8
 constexpr int F_BIAS = F_OUT_WARPS * 512;   // each output warp's 128 columns, fp32
 constexpr int F_TURN = F_OUT_WARPS * 2048;  // and 32 rows of 64 output bytes
-constexpr int F_BATCH = 2;       // K blocks the scale warps take at a time
-constexpr int F_RING = 4;        // batches in their ring
-constexpr int F_SLOT = 32 * 12 * 4;  // scales of a K block: [c / 4][lane][c % 4], c as below
+constexpr int F_BATCH = 3;       // K blocks the scale warps take at a time
+constexpr int F_RING = 3;        // batches in their ring
+static_assert(F_STAGES % F_BATCH == 0, "a batch's stages are consecutive");
+constexpr int F_SLOT = 32 * 12 * 4;  // scales of a K block: [c][lane], c as below
 constexpr int F_SWAP = F_RING * F_BATCH * F_SLOT;
 constexpr int F_SMEM = 1024 + F_STAGES * F_STAGE_BYTES + F_BIAS + F_TURN + F_SWAP + 256;
 static_assert(F_SMEM <= 232448, "fits a CTA");
@@ -228,7 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const int q = warp & 3;  // its quarter of the lanes
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + F_SCALE_COL;
         const uint32_t even_full = ptx::mapa_shared(bar_full, 0);
-        const uint8_t* ring = after + F_BIAS + F_TURN;
+        uint8_t* ring = after + F_BIAS + F_TURN;
         const uint32_t ring_u32 = base + NST * F_STAGE_BYTES + F_BIAS + F_TURN;
         // Scales 0..3 of a lane are A's rows lane + 32 c, 4..11 B's rows lane + 32 (c - 4).
         // This warp fetches A's c = q and B's 4 + 2q, 5 + 2q; of a weight, whose 128 rows
@@ -253,17 +255,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         if (f.tile < p.total_tiles) start_tile();
         auto fetch = [&](uint32_t slot) {
             if (f.tile >= p.total_tiles) return;
-            const uint32_t dst = ring_u32 + slot * F_SLOT + lane * 16;
-            copy4(dst + q * 4, f.m < p.M ? f.a : p.sa[0], f.m < p.M);
+            const uint32_t dst = ring_u32 + slot * F_SLOT + lane * 4;
+            copy4(dst + q * 128, f.m < p.M ? f.a : p.sa[0], f.m < p.M);
             if constexpr (F32) {
-                const int c = 2 * q;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const bool in = f.n + 32 * i < p.N;
-                    copy4(dst + 512 + (c >> 2) * 512 + ((c & 3) + i) * 4, in ? f.b + 32 * i : p.sb[0], in);
+                    copy4(dst + (4 + 2 * q + i) * 128, in ? f.b + 32 * i : p.sb[0], in);
                 }
             } else if (q == 0 && lane < 2) {
-                copy4(ring_u32 + slot * F_SLOT + 512 + lane * 4, f.n < p.N ? f.b : p.sb[0], f.n < p.N);
+                copy4(dst + 4 * 128, f.n < p.N ? f.b : p.sb[0], f.n < p.N);
             }
             f.a += p.sa_kb;
             f.b += p.sb_kb;
@@ -288,49 +289,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const long long blocks = static_cast<long long>(tiles) * nk;
         int stage = 0;
         uint32_t phase = 0;
-        for (long long done = 0; done < blocks; done += F_BATCH) {
-            const uint32_t batch = static_cast<uint32_t>(done / F_BATCH);
-            const int here = blocks - done < F_BATCH ? 1 : F_BATCH;
-            // the stages' last MMAs have read their scales
-            bool ok = wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.timeout_ns, p.err,
-                           ERR_PRODUCER);
-            const int stage2 = stage + 1 == NST ? 0 : stage + 1;
-            const uint32_t phase2 = stage + 1 == NST ? phase ^ 1u : phase;
-            if (here > 1)
-                ok = ok && wait(bar_empty + 8 * stage2, phase2 ^ 1u, abort_flag, p.timeout_ns, p.err,
-                                ERR_PRODUCER);
+        uint32_t slot = 0, batch = 0;
+        for (long long done = 0; done < blocks; done += F_BATCH, ++batch) {
+            const int here = blocks - done < F_BATCH ? static_cast<int>(blocks - done) : F_BATCH;
+            // the stages' last MMAs have read their scales (they end in order)
+            const bool ok = wait(bar_empty + 8 * (stage + here - 1), phase ^ 1u, abort_flag,
+                                 p.timeout_ns, p.err, ERR_PRODUCER);
             copy_wait<F_RING - 2>();
-            // this batch has arrived and the one before it has been read by all four
-            // warps, which also give up together
+            // what this thread copied, as exponents
+            uint32_t* words = reinterpret_cast<uint32_t*>(ring + slot * (F_BATCH * F_SLOT)) + lane;
+            if (++slot == F_RING) slot = 0;
+#pragma unroll
+            for (int u = 0; u < F_BATCH; ++u) {
+                uint32_t* x = words + u * (F_SLOT / 4);
+                x[32 * q] = scale_word(x[32 * q]);
+                if constexpr (F32) {
+                    uint32_t* y = x + 32 * (4 + 2 * q);
+                    y[0] = scale_word(y[0]);
+                    y[32] = scale_word(y[32]);
+                } else if (q == 0 && lane < 2) {
+                    x[32 * 4] = scale_word(x[32 * 4]);
+                }
+            }
+            // this batch is ready and the one before it has been read by all four warps,
+            // which also give up together
             if (barrier_any<F_SCALE_WARPS * 32>(!ok)) break;
-            fetch_batch(batch + F_RING - 1);
-            const uint8_t* src = ring + (batch % F_RING) * (F_BATCH * F_SLOT);
             ptx::tc_fence_after();
 #pragma unroll
             for (int u = 0; u < F_BATCH; ++u) {
                 if (u < here) {
-                    const float4* x = reinterpret_cast<const float4*>(src + u * F_SLOT) + lane;
+                    const uint32_t* x = words + u * (F_SLOT / 4);
                     uint32_t w[12];
-                    const float4 x0 = x[0];
-                    w[0] = scale_word(x0.x);
-                    w[1] = scale_word(x0.y);
-                    w[2] = scale_word(x0.z);
-                    w[3] = scale_word(x0.w);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) w[c] = x[32 * c];
                     if constexpr (F32) {
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float4 y = x[32 * (1 + c)];
-                            w[4 + 4 * c] = scale_word(y.x);
-                            w[5 + 4 * c] = scale_word(y.y);
-                            w[6 + 4 * c] = scale_word(y.z);
-                            w[7 + 4 * c] = scale_word(y.w);
-                        }
+                        for (int c = 4; c < 12; ++c) w[c] = x[32 * c];
                     } else {
-                        const float2 y = *reinterpret_cast<const float2*>(src + u * F_SLOT + 512);
-                        w[4] = w[5] = w[6] = w[7] = scale_word(y.x);
-                        w[8] = w[9] = w[10] = w[11] = scale_word(y.y);
+                        const uint2 y = *reinterpret_cast<const uint2*>(x - lane + 32 * 4);
+                        w[4] = w[5] = w[6] = w[7] = y.x;
+                        w[8] = w[9] = w[10] = w[11] = y.y;
                     }
-                    const uint32_t t = lanes + (u == 0 ? stage : stage2) * 16;
+                    const uint32_t t = lanes + (stage + u) * 16;
                     store_cols4(t, w);
                     store_cols8(t + F_SCALE_B, w + 4);
                 }
@@ -339,15 +339,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                arrive_relaxed_cluster(even_full + 8 * stage);
-                if (here > 1) arrive_relaxed_cluster(even_full + 8 * stage2);
-            }
 #pragma unroll
-            for (int u = 0; u < F_BATCH; ++u) {
-                if (u < here && ++stage == NST) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+                for (int u = 0; u < F_BATCH; ++u)
+                    if (u < here) arrive_relaxed_cluster(even_full + 8 * (stage + u));
+            }
+            // into the batch before this one, which all four have read
+            fetch_batch(batch + F_RING - 1);
+            stage += F_BATCH;
+            if (stage == NST) {
+                stage = 0;
+                phase ^= 1u;
             }
         }
         copy_wait<0>();

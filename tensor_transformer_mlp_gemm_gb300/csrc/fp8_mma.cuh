@@ -58,13 +58,11 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t tile, int kk, int mn) 
 }
 
 // A scale's word: its exponent four times; NaN (255) for anything but a positive
-// power of two.
-__device__ __forceinline__ uint32_t scale_word(float s) {
-    const uint32_t u = __float_as_uint(s), e = u >> 23;
-    const bool ok = (u & 0x007FFFFFu) == 0 && e >= 1 && e <= 254;
-    return (ok ? e : 255u) * 0x01010101u;
+// power of two of 2^-126 .. 2^127.
+__device__ __forceinline__ uint32_t scale_word(uint32_t bits) {
+    const uint32_t e = (bits & 0x807FFFFFu) == 0 && bits != 0 ? bits >> 23 : 255u;
+    return __byte_perm(e, 0, 0);
 }
-constexpr uint32_t kScaleOne = 127u * 0x01010101u;
 
 // This thread's lane of its warp's quarter: 4 and 8 consecutive columns.
 __device__ __forceinline__ void store_cols4(uint32_t taddr, const uint32_t* v) {
