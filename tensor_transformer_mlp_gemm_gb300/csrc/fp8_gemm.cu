@@ -187,42 +187,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                         break;
                 }
             }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             // ---------------- MMA issuer ----------------
+            // The whole warp walks the loop and one lane issues, so the descriptors
+            // stay in uniform registers.
             const uint32_t id = idesc(F_TILE, F_TILE, p.a_mn, p.b_mn) | p.ab_format;
+            const uint64_t da = operand_desc(base, 0, p.a_mn);
+            const uint64_t db = operand_desc(base + F8_BOX_BYTES, 0, p.b_mn);
+            const uint32_t ka = (p.a_mn ? 4096 : 32) >> 4, kb = (p.b_mn ? 4096 : 32) >> 4;
             int stage = 0;
             uint32_t phase = 0, tiles = 0;
             bool ok = true;
             for (int tile = cluster; ok && tile < p.total_tiles; tile += nclusters, ++tiles) {
-                if (!wait(bar_free, (tiles & 1) ^ 1u, abort_flag, p.timeout_ns, p.err, ERR_MMA)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, wait(bar_free, (tiles & 1) ^ 1u, abort_flag, p.timeout_ns,
+                                                  p.err, ERR_MMA));
+                if (!ok) break;
                 for (int kk = 0; kk < nk; ++kk) {
-                    if (!wait(bar_full + 8 * stage, phase, abort_flag, p.timeout_ns, p.err, ERR_MMA)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(0xffffffffu, wait(bar_full + 8 * stage, phase, abort_flag,
+                                                      p.timeout_ns, p.err, ERR_MMA));
+                    if (!ok) break;
                     ptx::tc_fence_after();
-                    const uint32_t sa = base + stage * F_STAGE_BYTES;
+                    const uint32_t step = stage * (F_STAGE_BYTES >> 4);
                     const uint32_t sf = tmem + F_SCALE_COL + stage * 16;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_pair(tmem, operand_desc(sa, k, p.a_mn),
-                                 operand_desc(sa + F8_BOX_BYTES, k, p.b_mn), id, sf, sf + F_SCALE_B,
-                                 (kk > 0 || k > 0) ? 1u : 0u);
-                    ptx::mma_commit_pair_multicast(bar_empty + 8 * stage, 0x3);
+                        for (uint32_t k = 0; k < 4; ++k)
+                            mma_pair(tmem, da + step + k * ka, db + step + k * kb, id, sf,
+                                     sf + F_SCALE_B, (kk > 0 || k > 0) ? 1u : 0u);
+                        ptx::mma_commit_pair_multicast(bar_empty + 8 * stage, 0x3);
+                        if (kk + 1 == nk) ptx::mma_commit_pair_multicast(bar_done, 0x3);
+                    }
+                    __syncwarp();
                     if (++stage == NST) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (ok) ptx::mma_commit_pair_multicast(bar_done, 0x3);
             }
-            ptx::mma_commit_pair(bar_drain);
-            drain(bar_drain, 0, p.timeout_ns, p.err);
-            // the last release of the accumulator arrives on this CTA
-            if (ok && tiles > 0) drain(bar_free, (tiles - 1) & 1, p.timeout_ns, p.err);
+            if (elect_one()) {
+                ptx::mma_commit_pair(bar_drain);
+                drain(bar_drain, 0, p.timeout_ns, p.err);
+                // the last release of the accumulator arrives on this CTA
+                if (ok && tiles > 0) drain(bar_free, (tiles - 1) & 1, p.timeout_ns, p.err);
+            }
+            __syncwarp();
         }
     } else if (warp < 8) {
         // ---------------- scales ----------------

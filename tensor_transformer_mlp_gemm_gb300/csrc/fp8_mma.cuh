@@ -80,6 +80,17 @@ __device__ __forceinline__ void store_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// One lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Waits for phase `parity` of `bar`; gives up (false) when another role has, or
 // after the limit (then this one aborts the CTA and sets `code` in the error word).
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
