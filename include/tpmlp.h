@@ -413,6 +413,73 @@ tpmlp_status tpmlp_fp8_row_linear_backward(const tpmlp_linear_dims* dims,
                                            void* const* dW_shards, void* db, void* workspace,
                                            void* stream);
 
+/* ---- Norms before and after a block, with its gate and residual scale ------------
+ * What surrounds a block f in a residual stream X with a norm on both sides of it:
+ *
+ *   u   = N_post(Z)                                  Z = f(...), per token row over h
+ *   Out = residual_scale * X + gate[row / gate_rows] * u      (bf16)
+ *   Xn  = N_pre(Out)                                 the next block's input
+ *
+ *   rms    N(v) = v rstd gamma,                rstd = 1 / sqrt(mean(v^2) + eps)
+ *   layer  N(v) = (v - mean) rstd gamma + beta, rstd = 1 / sqrt(var + eps), var biased
+ *   none   post: u = Z;  pre: no Xn
+ *
+ * in one pass over the rows.  Xn is written in bf16, in 8 bits by rows (as the
+ * 8-bit linear layers take it: the bf16 rounding of Xn, quantised), or both.
+ * With Z = NULL there is no block before: Xn = N_pre(X), Out is X and not written
+ * (post none, no gate, Out NULL; residual_scale is not used).
+ *
+ *   gate   bf16 [tokens / gate_rows, h]: one row for each run of gate_rows tokens (a
+ *          sequence, or all tokens: gate_rows = tokens).  gate_rows = 0: no gate.
+ *   stats  fp32 [4][tokens]: mean and rstd of Z's rows, mean and rstd of Out's (means
+ *          of rms norms are 0; rows of kind none are not written).  Kept for the
+ *          backward pass; NULL in the forward call: not wanted.
+ *
+ * Backward, for the gradients dOut of Out (NULL: none) and dXn of Xn:
+ *   g = dOut + N_pre'(dXn),  dX = residual_scale * g,  dgate = sum of g * u over the
+ *   gate's rows,  dZ = N_post'(gate * g),  and the weights' gradients.
+ *   With Z = NULL:  dX = dOut + N_pre'(dXn), Out being X.
+ * gamma, beta, gate bf16; their gradients fp32 (overwritten).  Pointers of what a
+ * kind does not have must be NULL.  Statistics and sums are fp32, in a fixed order.
+ * X, Z, Out, Xn and their gradients come in seq_chunks token chunks of tokens /
+ * seq_chunks rows; Xq and Xs are whole.  hidden: a multiple of 8 (16 with Xq), at most
+ * 16384; else TPMLP_ERR_UNSUPPORTED.  gate_rows divides tokens, eps >= 0, else
+ * TPMLP_ERR_INVALID_ARG.  With tokens = 0 the forward does nothing and the backward
+ * zeroes the gammas' and betas' gradients.  The workspace is scratch of one call. */
+typedef enum {
+    TPMLP_NORM_NONE = 0,
+    TPMLP_NORM_RMS = 1,
+    TPMLP_NORM_LAYER = 2
+} tpmlp_norm_kind;
+
+typedef struct {
+    int64_t tokens, hidden;
+    int64_t gate_rows;     /* tokens that share a row of the gate; 0 = no gate */
+    int32_t seq_chunks;
+    int32_t post, pre;     /* tpmlp_norm_kind */
+    int32_t q_format;      /* tpmlp_fp8_format of Xq */
+    float eps;
+    float residual_scale;
+} tpmlp_norm_params;
+
+/* Bytes of workspace the backward call needs (0 for invalid params). */
+size_t tpmlp_norm_workspace_bytes(const tpmlp_norm_params* params);
+
+tpmlp_status tpmlp_norm_forward(const tpmlp_norm_params* params, const void* const* X,
+                                const void* const* Z, const void* post_gamma,
+                                const void* post_beta, const void* gate, const void* pre_gamma,
+                                const void* pre_beta, void* const* Out, void* const* Xn, void* Xq,
+                                void* Xs, void* stats, void* stream);
+
+tpmlp_status tpmlp_norm_backward(const tpmlp_norm_params* params, const void* const* dOut,
+                                 const void* const* dXn, const void* const* Z,
+                                 const void* const* Out, const void* post_gamma,
+                                 const void* post_beta, const void* gate, const void* pre_gamma,
+                                 const void* stats, void* const* dX, void* const* dZ,
+                                 void* dpost_gamma, void* dpost_beta, void* dgate,
+                                 void* dpre_gamma, void* dpre_beta, void* workspace,
+                                 void* stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* tpmlp_status_string(tpmlp_status s);
 
@@ -552,8 +619,8 @@ enum {
     TPMLP_KERNEL_LINEAR_FWD = 7,  /* linear layers (bf16, 8-bit): Y_i = X.W_i + b, Z = sum_i X_i.W_i + b */
     TPMLP_KERNEL_LINEAR_DGRAD = 8,  /* linear layers (bf16, 8-bit): dX = sum_i dY_i.W_i^T, dX_i = dZ.W_i^T */
     TPMLP_KERNEL_LINEAR_WGRAD = 9,  /* linear layers (bf16, 8-bit): dW_i */
-    TPMLP_KERNEL_LAYERNORM_FWD = 10,  /* sequence-parallel sublayer: LN(X) and row statistics */
-    TPMLP_KERNEL_LAYERNORM_BWD = 11,  /* sequence-parallel sublayer: dX, dgamma, dbeta (2 launches; 3 for h > 4096) */
+    TPMLP_KERNEL_LAYERNORM_FWD = 10,  /* sequence-parallel sublayer: LN(X) and row statistics; tpmlp_norm_forward */
+    TPMLP_KERNEL_LAYERNORM_BWD = 11,  /* sequence-parallel sublayer: dX, dgamma, dbeta (2 launches; 3 for h > 4096); tpmlp_norm_backward (2) */
     TPMLP_KERNEL_DROPOUT_BWD = 12,    /* sequence-parallel sublayer: dZ from dOut and the mask, db2 (2 launches) */
     TPMLP_KERNEL_SP_COPY = 13,        /* tpmlp_sp_gather / tpmlp_sp_scatter, 8-bit quantisation */
     TPMLP_KERNEL_KINDS = 14

@@ -45,6 +45,7 @@ EXPORTED = (
     "tpmlp_fp8_quantize", "tpmlp_fp8_quantize_weight", "tpmlp_fp8_linear_workspace_bytes",
     "tpmlp_fp8_column_linear_forward", "tpmlp_fp8_column_linear_backward",
     "tpmlp_fp8_row_linear_forward", "tpmlp_fp8_row_linear_backward",
+    "tpmlp_norm_workspace_bytes", "tpmlp_norm_forward", "tpmlp_norm_backward",
 )
 
 
@@ -72,6 +73,13 @@ class tpmlp_fp8_quant(ctypes.Structure):
 
 class tpmlp_fp8_formats(ctypes.Structure):
     _fields_ = [("x", ctypes.c_int32), ("w", ctypes.c_int32), ("dy", ctypes.c_int32)]
+
+
+class tpmlp_norm_params(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("gate_rows", ctypes.c_int64), ("seq_chunks", ctypes.c_int32),
+                ("post", ctypes.c_int32), ("pre", ctypes.c_int32), ("q_format", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float)]
 
 
 class TpmlpError(RuntimeError):
@@ -176,6 +184,16 @@ _lib.tpmlp_fp8_row_linear_backward.restype = ctypes.c_int
 _lib.tpmlp_fp8_row_linear_backward.argtypes = [_ldims_p, _fmt_p, _vpp, _vpp, _vpp, _vpp, _vpp,
                                                _vpp, _vpp, _vp, _vp, _vp]
 
+_norm_p = ctypes.POINTER(tpmlp_norm_params)
+_lib.tpmlp_norm_workspace_bytes.restype = ctypes.c_size_t
+_lib.tpmlp_norm_workspace_bytes.argtypes = [_norm_p]
+_lib.tpmlp_norm_forward.restype = ctypes.c_int
+_lib.tpmlp_norm_forward.argtypes = [_norm_p, _vpp, _vpp, _vp, _vp, _vp, _vp, _vp, _vpp, _vpp, _vp, _vp,
+                                    _vp, _vp]
+_lib.tpmlp_norm_backward.restype = ctypes.c_int
+_lib.tpmlp_norm_backward.argtypes = [_norm_p, _vpp, _vpp, _vpp, _vpp, _vp, _vp, _vp, _vp, _vp, _vpp,
+                                     _vpp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+
 
 def library_path() -> str:
     return _LIB_PATH
@@ -201,6 +219,11 @@ def _ptr(x) -> int | None:
     if isinstance(x, int):
         return x
     return x.data_ptr()
+
+
+def _opt(xs):
+    """A pointer array, or NULL for None."""
+    return None if xs is None else _arr(xs)
 
 
 def _arr(xs):
@@ -425,9 +448,8 @@ def make_fp8_formats(x: int = 0, w: int = 0, dy: int = 0) -> tpmlp_fp8_formats:
 def tpmlp_fp8_quantize(quant, src, q_rows, s_rows, q_cols, s_cols, stream=None) -> None:
     """src and the outputs: lists of quant.parts tensors; the row pair or the
     column pair may be None."""
-    opt = lambda xs: None if xs is None else _arr(xs)  # noqa: E731
-    _check(_lib.tpmlp_fp8_quantize(ctypes.byref(quant), _arr(src), opt(q_rows), opt(s_rows),
-                                   opt(q_cols), opt(s_cols), _stream(stream)),
+    _check(_lib.tpmlp_fp8_quantize(ctypes.byref(quant), _arr(src), _opt(q_rows), _opt(s_rows),
+                                   _opt(q_cols), _opt(s_cols), _stream(stream)),
            "tpmlp_fp8_quantize")
 
 
@@ -473,6 +495,41 @@ def tpmlp_fp8_row_linear_backward(dims, formats, dZ, Xq_shards, Xs_shards, Wq_sh
         ctypes.byref(dims), ctypes.byref(formats), _arr(dZ), _arr(Xq_shards), _arr(Xs_shards),
         _arr(Wq_shards), _arr(Ws_shards), _arr(dX_shards), _arr(dW_shards), _ptr(db),
         _ptr(workspace), _stream(stream)), "tpmlp_fp8_row_linear_backward")
+
+
+NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def make_norm_params(tokens: int, hidden: int, post: int, pre: int, gate_rows: int = 0,
+                     seq_chunks: int = 1, q_format: int = 0, eps: float = 1e-5,
+                     residual_scale: float = 1.0) -> tpmlp_norm_params:
+    return tpmlp_norm_params(int(tokens), int(hidden), int(gate_rows), int(seq_chunks), int(post),
+                             int(pre), int(q_format), float(eps), float(residual_scale))
+
+
+def tpmlp_norm_workspace_bytes(params: tpmlp_norm_params) -> int:
+    """Workspace bytes of the backward call (0 if invalid)."""
+    return int(_lib.tpmlp_norm_workspace_bytes(ctypes.byref(params)))
+
+
+def tpmlp_norm_forward(params, X, Z, post_gamma, post_beta, gate, pre_gamma, pre_beta, Out, Xn, Xq,
+                       Xs, stats, stream=None) -> None:
+    """X, Z, Out, Xn: lists of seq_chunks tensors, or None where there is none."""
+    _check(_lib.tpmlp_norm_forward(ctypes.byref(params), _arr(X), _opt(Z), _ptr(post_gamma),
+                                   _ptr(post_beta), _ptr(gate), _ptr(pre_gamma), _ptr(pre_beta),
+                                   _opt(Out), _opt(Xn), _ptr(Xq), _ptr(Xs), _ptr(stats),
+                                   _stream(stream)), "tpmlp_norm_forward")
+
+
+def tpmlp_norm_backward(params, dOut, dXn, Z, Out, post_gamma, post_beta, gate, pre_gamma, stats, dX,
+                        dZ, dpost_gamma, dpost_beta, dgate, dpre_gamma, dpre_beta, workspace,
+                        stream=None) -> None:
+    _check(_lib.tpmlp_norm_backward(ctypes.byref(params), _opt(dOut), _opt(dXn), _opt(Z), _opt(Out),
+                                    _ptr(post_gamma), _ptr(post_beta), _ptr(gate),
+                                    _ptr(pre_gamma), _ptr(stats), _arr(dX), _opt(dZ),
+                                    _ptr(dpost_gamma), _ptr(dpost_beta), _ptr(dgate),
+                                    _ptr(dpre_gamma), _ptr(dpre_beta), _ptr(workspace),
+                                    _stream(stream)), "tpmlp_norm_backward")
 
 
 def make_sp_params(eps: float = 1e-5, dropout_p: float = 0.1, seed: int = 0,

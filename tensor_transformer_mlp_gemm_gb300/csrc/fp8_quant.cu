@@ -8,55 +8,20 @@
 // A CTA takes a 128 x 128 tile, which is 128 whole row groups, 128 whole
 // column groups and one whole block, so no group crosses CTAs and nothing is
 // read twice.  A thread holds 8 rows x 8 columns as eight 16-byte loads, all
-// in flight before the first use.  Magnitudes are compared as integers: the 15
-// low bits of a bf16 grow with |x|, with infinities and NaN on top, so one
-// packed 16-bit maximum instruction compares two values and a group that is not
-// finite shows as a maximum of at least 0x7F80.
+// in flight before the first use; the arithmetic is fp8_cvt.cuh's.
 #include "fp8_quant.cuh"
 
+#include "fp8_cvt.cuh"
 #include "ptx.cuh"
 
 namespace tpmlp {
 namespace {
 
+using namespace q8;
+
 constexpr int QT = 256;          // threads
 constexpr int QV = 8;            // rows (and columns) per thread
 constexpr int QWARPS = QT / 32;
-
-// Magnitude bits of a group's largest value -> the scale and its reciprocal.
-struct Scale {
-    float s, inv;
-    bool fine;
-};
-
-__device__ __forceinline__ Scale scale_of(uint32_t amax, int fmt) {
-    // |x| = 2^(e - 127) (1 + m / 128); top = 1.75 * 2^8 or 1.75 * 2^15
-    const int e = static_cast<int>(amax >> 7), m = static_cast<int>(amax & 0x7Fu);
-    int k = e - 127 - (fmt == FP8_E4M3 ? 8 : 15) + (m > 96 ? 1 : 0);
-    if (e == 0 || k < -119) k = -119;
-    Scale r;
-    r.fine = amax < 0x7F80u;
-    r.s = r.fine ? __uint_as_float(static_cast<uint32_t>(k + 127) << 23)
-                 : __uint_as_float(0x7FC00000u);
-    r.inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-    return r;
-}
-
-// hi and lo rounded to 8 bits, hi in the upper byte
-__device__ __forceinline__ uint32_t cvt8(float lo, float hi, int fmt) {
-    uint16_t r;
-    if (fmt == FP8_E4M3)
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    else
-        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-// the largest of the two 16-bit halves
-__device__ __forceinline__ uint32_t fold(uint32_t w) { return max(w & 0xFFFFu, w >> 16); }
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
@@ -96,18 +61,14 @@ __global__ void __launch_bounds__(QT) fp8_quant_kernel(const __grid_constant__ F
         v[i] = (col_in && r < p.rows) ? __ldg(src + r * vstep) : make_uint4(0, 0, 0, 0);
     }
 
-    constexpr uint32_t MAG = 0x7FFF7FFFu;
     uint32_t row_max[QV];
     uint32_t cm[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < QV; ++i) {
-        const uint32_t a = v[i].x & MAG, b = v[i].y & MAG, d = v[i].z & MAG, e = v[i].w & MAG;
-        if (ROWS) row_max[i] = fold(__vmaxu2(__vmaxu2(a, b), __vmaxu2(d, e)));
+        if (ROWS) row_max[i] = largest(v[i]);
         if (COLS || BLOCK) {
-            cm[0] = __vmaxu2(cm[0], a);
-            cm[1] = __vmaxu2(cm[1], b);
-            cm[2] = __vmaxu2(cm[2], d);
-            cm[3] = __vmaxu2(cm[3], e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cm[j] = __vmaxu2(cm[j], word(v[i], j) & kMagnitudes);
         }
     }
 
@@ -127,14 +88,7 @@ __global__ void __launch_bounds__(QT) fp8_quant_kernel(const __grid_constant__ F
             for (int i = 0; i < QV; ++i) {
                 const long long r = r0 + slot + 16 * i;
                 if (r >= p.rows) break;
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t w = word(v[i], j);
-                    o[j] = sc.fine ? cvt8(lo_f(w) * sc.inv, hi_f(w) * sc.inv, p.fmt_cols) : 0u;
-                }
-                *reinterpret_cast<uint2*>(q + r * p.cols + c) =
-                    make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+                *reinterpret_cast<uint2*>(q + r * p.cols + c) = cvt8(v[i], sc, p.fmt_cols);
             }
         }
         return;
@@ -175,14 +129,7 @@ __global__ void __launch_bounds__(QT) fp8_quant_kernel(const __grid_constant__ F
             const long long r = r0 + slot + 16 * i;
             if (cv == 0) s_row[slot + 16 * i] = sc.s;
             if (col_in && r < p.rows) {
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t w = word(v[i], j);
-                    o[j] = sc.fine ? cvt8(lo_f(w) * sc.inv, hi_f(w) * sc.inv, p.fmt_rows) : 0u;
-                }
-                *reinterpret_cast<uint2*>(q + r * p.cols + c) =
-                    make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+                *reinterpret_cast<uint2*>(q + r * p.cols + c) = cvt8(v[i], sc, p.fmt_rows);
             }
         }
     }
@@ -225,7 +172,7 @@ __global__ void __launch_bounds__(QT) fp8_quant_kernel(const __grid_constant__ F
                 // a column that is not finite: 0 * inf would be NaN
                 const float lo = inv[2 * j] > 0.0f ? lo_f(w) * inv[2 * j] : 0.0f;
                 const float hi = inv[2 * j + 1] > 0.0f ? hi_f(w) * inv[2 * j + 1] : 0.0f;
-                o[j] = cvt8(lo, hi, p.fmt_cols);
+                o[j] = cvt2(lo, hi, p.fmt_cols);
             }
             *reinterpret_cast<uint2*>(q + r * p.cols + c) =
                 make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
