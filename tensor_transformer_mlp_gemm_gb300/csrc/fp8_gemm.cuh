@@ -49,7 +49,14 @@ struct Fp8GemmParams {
     unsigned long long timeout_ns;
 };
 
-// The whole product on CTA pairs with 256 x 256 output tiles.
+// The whole product on CTA pairs with 256 x 256 output tiles; A's maps have boxes of
+// 128 rows.
 cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int out, cudaStream_t st);
+
+// The same (bf16 output, B scaled per block) for few rows of A: tiles of 128 columns
+// by fp8_small_rows() rows of A, K cut over up to 8 CTAs of a cluster.
+cudaError_t launch_fp8_small(const Fp8GemmParams& p, int sm_count, cudaStream_t st);
+// Rows of A of a tile, which is also the box of A's maps.
+inline int fp8_small_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
 }  // namespace tpmlp

@@ -124,19 +124,24 @@ struct Product {
     int chunk_rows;    // > 0: rows per token chunk
 };
 
-bool encode_operand(CUtensorMap* m, const Operand& o, int i, int K, int rows) {
-    return o.mn ? encode_bytes(m, o.q[i], rows, K, 128) : encode_bytes(m, o.q[i], K, rows, 128);
+bool encode_operand(CUtensorMap* m, const Operand& o, int i, int K, int rows, int box) {
+    return o.mn ? encode_bytes(m, o.q[i], rows, K, 128) : encode_bytes(m, o.q[i], K, rows, box);
 }
+
+// Rows of A up to which the few-rows kernel is taken.
+constexpr int kFewRows = 128;
 
 tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int kind, cudaStream_t st) {
     Fp8GemmParams p;
     std::memset(&p, 0, sizeof(p));
+    const bool few = d.out_kind == F8_BF16_BLOCK && d.M <= kFewRows;
     for (int i = 0; i < d.a.n; ++i) {
-        if (!encode_operand(&p.a_map[i], d.a, i, d.K, d.M)) return TPMLP_ERR_UNSUPPORTED;
+        if (!encode_operand(&p.a_map[i], d.a, i, d.K, d.M, few ? fp8_small_rows(d.M) : 128))
+            return TPMLP_ERR_UNSUPPORTED;
         p.sa[i] = static_cast<const float*>(d.a.s[i]);
     }
     for (int i = 0; i < d.b.n; ++i) {
-        if (!encode_operand(&p.b_map[i], d.b, i, d.K, d.N)) return TPMLP_ERR_UNSUPPORTED;
+        if (!encode_operand(&p.b_map[i], d.b, i, d.K, d.N, 128)) return TPMLP_ERR_UNSUPPORTED;
         p.sb[i] = static_cast<const float*>(d.b.s[i]);
     }
     for (int i = 0; i < d.nout; ++i) p.out[i] = d.out[i];
@@ -161,10 +166,14 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int kind, cuda
     p.band = p.mtiles < kBand ? p.mtiles : kBand;
     p.chunk_rows = d.chunk_rows;
     p.bias = d.bias;
-    p.ab_format = (static_cast<uint32_t>(d.a_format) << 7) | (static_cast<uint32_t>(d.b_format) << 10);
+    // the few-rows kernel has the weights for the instruction's A
+    const int fa = few ? d.b_format : d.a_format, fb = few ? d.a_format : d.b_format;
+    p.ab_format = (static_cast<uint32_t>(fa) << 7) | (static_cast<uint32_t>(fb) << 10);
     p.err = dev->err;
     p.timeout_ns = g_timeout_ns;
-    TPMLP_CUDA(timed(kind, 1, st, [&] { return launch_fp8_gemm(p, d.out_kind, st); }));
+    TPMLP_CUDA(timed(kind, 1, st, [&] {
+        return few ? launch_fp8_small(p, dev->sm_count, st) : launch_fp8_gemm(p, d.out_kind, st);
+    }));
     return TPMLP_OK;
 }
 

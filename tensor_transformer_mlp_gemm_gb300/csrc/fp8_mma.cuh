@@ -39,6 +39,19 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint6
         : "memory");
 }
 
+// The same on one CTA (its own 128 rows of A, all rows of B).
+__device__ __forceinline__ void mma_one(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+
 // Instruction descriptor of kind::mxf8f6f4 with an fp32 accumulator.
 //   bits 4-5, 29-30 which exponent of a scale word is B's, A's (the first);
 //   7-9 A format, 10-12 B format (0 = e4m3, 1 = e5m2); bit 15 A is MN-major, 16 B;
@@ -64,7 +77,10 @@ __device__ __forceinline__ uint32_t scale_word(uint32_t bits) {
     return __byte_perm(e, 0, 0);
 }
 
-// This thread's lane of its warp's quarter: 4 and 8 consecutive columns.
+// This thread's lane of its warp's quarter: 1, 4 and 8 consecutive columns.
+__device__ __forceinline__ void store_col(uint32_t taddr, uint32_t v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void store_cols4(uint32_t taddr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
                  "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
@@ -78,6 +94,11 @@ __device__ __forceinline__ void store_cols8(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void store_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// The same on this CTA's own mbarrier.
+__device__ __forceinline__ void arrive_relaxed(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // One lane of the (converged) warp, the same one every time.
@@ -178,6 +199,17 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, float* v) {
           "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
           "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
           "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+
+// 16 columns of this thread's tensor-memory lane into v (usable after load_wait).
+__device__ __forceinline__ void load_cols16(uint32_t taddr, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+          "=f"(v[14]), "=f"(v[15])
         : "r"(taddr));
 }
 
