@@ -221,6 +221,35 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+class _Here:
+    """Does nothing: the tensors' device is the current one."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def on_device(device: torch.device):
+    """Context with `device` current: a launch, its stream and the library's record
+    of the device go by the current device.  (Entering torch.cuda.device costs 3 us,
+    as much as the launch, so it is left out where there is nothing to change.)"""
+    if device.index == torch.cuda.current_device():
+        return _HERE
+    return torch.cuda.device(device)
+
+
+def stream_on(device: torch.device, stream) -> int:
+    """The raw handle of `stream`, or of the device's current stream for None."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream(stream)
+
+
 def _opt(xs):
     """A pointer array, or NULL for None."""
     return None if xs is None else _arr(xs)

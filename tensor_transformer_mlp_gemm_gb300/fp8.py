@@ -10,6 +10,7 @@ through :mod:`binding`.  Layouts follow the C ABI (include/tpmlp.h):
 """
 from __future__ import annotations
 
+import ctypes
 from dataclasses import dataclass
 
 import torch
@@ -31,6 +32,44 @@ class Fp8Tokens:
     row_scale: torch.Tensor | None = None
     cols: torch.Tensor | None = None
     col_scale: torch.Tensor | None = None
+
+
+class Fp8Shards:
+    """The shards of one tensor in 8 bits, side by side in one buffer for each kind
+    of output: a sequence of Fp8Tokens (views of the buffers)."""
+
+    def __init__(self, n: int, T: int, C: int, fmt: str, rows: bool, cols: bool, dev):
+        self.n, self.T, self.C = n, T, C
+        new = lambda d, *shape: torch.empty(shape, dtype=d, device=dev)  # noqa: E731
+        # every shard's scales start on 16 bytes
+        self._pad = -(-_up128(C) * T // 4) * 4
+        self.rows = new(DTYPES[fmt], n, T, C) if rows else None
+        self.row_scale = new(torch.float32, n, self._pad) if rows else None
+        self.cols = new(DTYPES[fmt], n, T, C) if cols else None
+        self.col_scale = new(torch.float32, n, _up128(T), C) if cols else None
+
+    def __len__(self) -> int:
+        return self.n
+
+    def __getitem__(self, i: int) -> Fp8Tokens:
+        if not 0 <= i < self.n:
+            raise IndexError(i)
+        x = Fp8Tokens()
+        if self.rows is not None:
+            k = _up128(self.C)
+            x.rows, x.row_scale = self.rows[i], self.row_scale[i, :k * self.T].view(k, self.T)
+        if self.cols is not None:
+            x.cols, x.col_scale = self.cols[i], self.col_scale[i]
+        return x
+
+    def pointers(self, cols: bool):
+        """(q, scale) pointer arrays, one entry for each shard."""
+        q, s = (self.cols, self.col_scale) if cols else (self.rows, self.row_scale)
+        size = self.T * self.C
+        step = 4 * (_up128(self.T) * self.C if cols else self._pad)
+        a, b = q.data_ptr(), s.data_ptr()
+        return (_array([a + i * size for i in range(self.n)]),
+                _array([b + i * step for i in range(self.n)]))
 
 
 def _format(name: str) -> int:
@@ -62,6 +101,39 @@ def _empty_tokens(T: int, C: int, fmt: str, rows: bool, cols: bool, dev) -> Fp8T
     return x
 
 
+def _array(ptrs):
+    return (ctypes.c_void_p * len(ptrs))(*ptrs)
+
+
+def _pointers(xs):
+    return _array([x.data_ptr() for x in xs])
+
+
+def _quantize(parts, code: int, scale_ld: int, rows, cols, stream) -> None:
+    """One launch over `parts` [T, C]; rows, cols: (q, scale) pointer arrays or None."""
+    T, C = parts[0].shape
+    dev = parts[0].device
+    quant = binding.make_fp8_quant(T, C, scale_ld, len(parts), code, code)
+    q_rows, s_rows = rows or (None, None)
+    q_cols, s_cols = cols or (None, None)
+    with binding.on_device(dev):
+        binding.tpmlp_fp8_quantize(quant, _pointers(parts), q_rows, s_rows, q_cols,
+                                   s_cols, binding.stream_on(dev, stream))
+
+
+def _check_parts(parts, what: str) -> None:
+    if not 1 <= len(parts) <= 8:
+        raise ValueError(f"1 to 8 {what}s are taken in a call, got {len(parts)}")
+    first = parts[0]
+    _check_bf16(first, what)
+    shape, dev = first.shape, first.device
+    for x in parts[1:]:
+        if (x.dtype is not torch.bfloat16 or x.shape != shape or x.device != dev
+                or not x.is_contiguous()):
+            _check_bf16(x, what)
+            raise ValueError(f"{what}s must have one shape and device")
+
+
 def quantize_tokens(X, fmt: str = "e4m3", rows: bool = True, cols: bool = False,
                     out: Fp8Tokens | None = None, stream=None) -> Fp8Tokens:
     """X: a bf16 tensor [T, C], or the list of its token chunks, which are
@@ -69,12 +141,9 @@ def quantize_tokens(X, fmt: str = "e4m3", rows: bool = True, cols: bool = False,
     both); out: buffers to reuse, as returned by an earlier call."""
     chunks = [X] if isinstance(X, torch.Tensor) else list(X)
     code = _format(fmt)
-    for c in chunks:
-        _check_bf16(c, "X")
+    _check_parts(chunks, "token chunk")
     first, n = chunks[0], len(chunks)
     tc, C = first.shape
-    if any(c.shape != first.shape for c in chunks):
-        raise ValueError("token chunks must have one shape")
     if n > 1 and tc % 128:
         raise ValueError("token chunks must be a multiple of 128 tokens")
     if not (rows or cols):
@@ -82,45 +151,36 @@ def quantize_tokens(X, fmt: str = "e4m3", rows: bool = True, cols: bool = False,
     T, dev = tc * n, first.device
     if out is None:
         out = _empty_tokens(T, C, fmt, rows, cols, dev)
-    if rows:
-        _check_like(out.rows, (T, C), DTYPES[fmt], dev, "out.rows")
-        _check_like(out.row_scale, (_up128(C), T), torch.float32, dev, "out.row_scale")
-    if cols:
-        _check_like(out.cols, (T, C), DTYPES[fmt], dev, "out.cols")
-        _check_like(out.col_scale, (_up128(T), C), torch.float32, dev, "out.col_scale")
+    else:
+        if rows:
+            _check_like(out.rows, (T, C), DTYPES[fmt], dev, "out.rows")
+            _check_like(out.row_scale, (_up128(C), T), torch.float32, dev, "out.row_scale")
+        if cols:
+            _check_like(out.cols, (T, C), DTYPES[fmt], dev, "out.cols")
+            _check_like(out.col_scale, (_up128(T), C), torch.float32, dev, "out.col_scale")
 
     def part(x, step):
-        return [x.data_ptr() + j * step for j in range(n)]
-    quant = binding.make_fp8_quant(tc, C, max(T, 1), n, code, code)
-    with torch.cuda.device(dev):
-        binding.tpmlp_fp8_quantize(
-            quant, chunks, part(out.rows, tc * C) if rows else None,
-            part(out.row_scale, tc * 4) if rows else None, part(out.cols, tc * C) if cols else None,
-            part(out.col_scale, tc // 128 * C * 4) if cols else None, stream)
+        at = x.data_ptr()
+        return _array([at + j * step for j in range(n)])
+    _quantize(chunks, code, max(T, 1),
+              (part(out.rows, tc * C), part(out.row_scale, tc * 4)) if rows else None,
+              (part(out.cols, tc * C), part(out.col_scale, tc // 128 * C * 4)) if cols else None, stream)
     return out
 
 
 def quantize_shards(shards, fmt: str = "e4m3", rows: bool = True, cols: bool = False,
-                    stream=None) -> list:
+                    stream=None) -> Fp8Shards:
     """Each of up to eight bf16 tensors [T, C] of one shape, in one launch."""
     shards = list(shards)
     code = _format(fmt)
-    for x in shards:
-        _check_bf16(x, "shard")
-    if any(x.shape != shards[0].shape for x in shards):
-        raise ValueError("shards must have one shape")
+    _check_parts(shards, "shard")
     if not (rows or cols):
         raise ValueError("choose rows, cols or both")
     T, C = shards[0].shape
-    dev = shards[0].device
-    outs = [_empty_tokens(T, C, fmt, rows, cols, dev) for _ in shards]
-    quant = binding.make_fp8_quant(T, C, max(T, 1), len(shards), code, code)
-    with torch.cuda.device(dev):
-        binding.tpmlp_fp8_quantize(
-            quant, shards, [o.rows for o in outs] if rows else None,
-            [o.row_scale for o in outs] if rows else None, [o.cols for o in outs] if cols else None,
-            [o.col_scale for o in outs] if cols else None, stream)
-    return outs
+    out = Fp8Shards(len(shards), T, C, fmt, rows, cols, shards[0].device)
+    _quantize(shards, code, max(T, 1), out.pointers(False) if rows else None,
+              out.pointers(True) if cols else None, stream)
+    return out
 
 
 def quantize_weight(W: torch.Tensor, fmt: str = "e4m3", stream=None) -> tuple:
@@ -130,8 +190,8 @@ def quantize_weight(W: torch.Tensor, fmt: str = "e4m3", stream=None) -> tuple:
     r, c = W.shape
     q = torch.empty(r, c, dtype=DTYPES[fmt], device=W.device)
     s = torch.empty(_up128(r), _up128(c), dtype=torch.float32, device=W.device)
-    with torch.cuda.device(W.device):
-        binding.tpmlp_fp8_quantize_weight(W, r, c, code, q, s, stream)
+    with binding.on_device(W.device):
+        binding.tpmlp_fp8_quantize_weight(W, r, c, code, q, s, binding.stream_on(W.device, stream))
     return q, s
 
 
@@ -150,6 +210,7 @@ class DeviceFp8Linear:
         self.w = w
         self.column = w.split == "column"
         self.x_format = x_format
+        self._x_dtype = DTYPES.get(x_format)
         self.formats = binding.make_fp8_formats(_format(x_format), _format(w_format),
                                                 _format(dy_format))
         T, din, dout, t, n = w.tokens, w.in_features, w.out_features, w.t, w.seq_chunks
@@ -158,6 +219,8 @@ class DeviceFp8Linear:
         if need == 0:
             raise ValueError(f"unsupported dims for an 8-bit linear layer: {w}")
         self.Wq, self.Ws, self.b = list(Wq), list(Ws), b
+        if not b.is_cuda:
+            raise ValueError(f"the layer's tensors must be CUDA tensors, got b on {b.device}")
         self.device = dev = b.device
         s = w.shard
         wshape = (din, s) if self.column else (s, dout)
@@ -180,7 +243,19 @@ class DeviceFp8Linear:
             raise ValueError(f"the workspace needs {need} bytes")
         self.ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8,
                                                                       device=dev)
-        self._args = tuple(binding._arr(x) for x in (self.Wq, self.Ws))
+        # pointer arrays of the layer's own buffers, marshalled once
+        self._weights = (_pointers(self.Wq), _pointers(self.Ws))
+        self._own = {"Y": (self.Y, _pointers(self.Y)), "dX": (self.dX, _pointers(self.dX))}
+
+    def _outputs(self, name: str):
+        """The pointer array of a list of the layer's buffers (which a caller may have
+        replaced)."""
+        xs = getattr(self, name)
+        kept, arr = self._own[name]
+        if xs is not kept:
+            arr = _pointers(self._list(xs, self._y if name == "Y" else self._dx, name))
+            self._own[name] = (xs, arr)
+        return arr
 
     def _weight_grads(self):
         # fp32 gradients, four times the weights' bytes: made by the first backward call
@@ -208,8 +283,14 @@ class DeviceFp8Linear:
         return quantize_shards(X, self.x_format, True, cols, stream=stream)
 
     def _tokens(self, x, cols: bool):
-        x = [x] if isinstance(x, Fp8Tokens) else list(x)
         shape, n = self._x
+        if isinstance(x, Fp8Shards) and (x.n, x.T, x.C) == (n, *shape):
+            q = x.cols if cols else x.rows
+            if q is None or q.dtype != self._x_dtype or q.device != self.device:
+                raise ValueError(f"the input is not quantised by {'columns' if cols else 'rows'} in "
+                                 f"{self.x_format} on {self.device}")
+            return x.pointers(cols)
+        x = [x] if isinstance(x, Fp8Tokens) else list(x)
         if len(x) != n:
             raise ValueError(f"{n} quantised inputs are needed, got {len(x)}")
         T, C = shape
@@ -219,9 +300,9 @@ class DeviceFp8Linear:
         for a, b in zip(q, s):
             if a is None or b is None:
                 raise ValueError("the input is not quantised by " + ("columns" if cols else "rows"))
-            _check_like(a, shape, DTYPES[self.x_format], self.device, "a quantised input")
+            _check_like(a, shape, self._x_dtype, self.device, "a quantised input")
             _check_like(b, sshape, torch.float32, self.device, "its scale")
-        return q, s
+        return _pointers(q), _pointers(s)
 
     def _list(self, xs, spec, what):
         xs = [xs] if isinstance(xs, torch.Tensor) else list(xs)
@@ -232,28 +313,30 @@ class DeviceFp8Linear:
         return xs
 
     def forward(self, x, Y=None, stream=None) -> None:
-        """x: Fp8Tokens by rows (column: one, row: t of them)."""
+        """x: by rows, as ``quantize`` makes it (column: Fp8Tokens, row: t of them)."""
         q, s = self._tokens(x, cols=False)
-        Y = self.Y if Y is None else self._list(Y, self._y, "Y")
-        with torch.cuda.device(self.device):
+        Y = self._outputs("Y") if Y is None else _pointers(self._list(Y, self._y, "Y"))
+        with binding.on_device(self.device):
+            stream = binding.stream_on(self.device, stream)
             if self.column:
                 binding.tpmlp_fp8_column_linear_forward(self.dims, self.formats, q[0], s[0],
-                                                        *self._args, self.b, Y, self.ws, stream)
+                                                        *self._weights, self.b, Y, self.ws, stream)
             else:
-                binding.tpmlp_fp8_row_linear_forward(self.dims, self.formats, q, s, *self._args,
+                binding.tpmlp_fp8_row_linear_forward(self.dims, self.formats, q, s, *self._weights,
                                                      self.b, Y, self.ws, stream)
 
     def backward(self, dY, x, dX=None, stream=None) -> None:
-        """dY: bf16 (column: t shards, row: token chunks); x: Fp8Tokens by columns."""
+        """dY: bf16 (column: t shards, row: token chunks); x: by columns, as
+        ``quantize`` makes it."""
         q, s = self._tokens(x, cols=True)
-        dY = self._list(dY, self._y, "dY")
-        dX = self.dX if dX is None else self._list(dX, self._dx, "dX")
-        with torch.cuda.device(self.device):
+        dY = _pointers(self._list(dY, self._y, "dY"))
+        dX = self._outputs("dX") if dX is None else _pointers(self._list(dX, self._dx, "dX"))
+        dW, db = self._weight_grads()
+        with binding.on_device(self.device):
+            stream = binding.stream_on(self.device, stream)
             if self.column:
                 binding.tpmlp_fp8_column_linear_backward(
-                    self.dims, self.formats, dY, q[0], s[0], *self._args, dX, self.dW, self.db,
-                    self.ws, stream)
+                    self.dims, self.formats, dY, q[0], s[0], *self._weights, dX, dW, db, self.ws, stream)
             else:
                 binding.tpmlp_fp8_row_linear_backward(
-                    self.dims, self.formats, dY, q, s, *self._args, dX, self.dW, self.db, self.ws,
-                    stream)
+                    self.dims, self.formats, dY, q, s, *self._weights, dX, dW, db, self.ws, stream)

@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import binding
-from .fp8 import DTYPES, Fp8Tokens, _check_like, _format, _up128
+from .fp8 import DTYPES, Fp8Tokens, _check_like, _format, _pointers, _up128
 
 
 class DeviceNormResidual:
@@ -52,6 +52,10 @@ class DeviceNormResidual:
         given = [w for w, used in wanted.values() if used and w is not None]
         self.device = torch.device(device) if device is not None else (
             given[0].device if given else torch.device("cuda:0"))
+        if self.device.type != "cuda":
+            raise ValueError(f"the norms run on a CUDA device, got {self.device}")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
         for name, (w, used) in wanted.items():
             if used:
                 if w is None:
@@ -119,11 +123,12 @@ class DeviceNormResidual:
         X = self._list(X, "X")
         Z = self._list(Z, "Z") if z else None
         self._check_gate(gate, z)
-        with torch.cuda.device(self.device):
+        with binding.on_device(self.device):
             binding.tpmlp_norm_forward(
-                self.params if z else self._before, X, Z, self.post_gamma if z else None,
-                self.post_beta if z else None, gate, self.pre_gamma, self.pre_beta,
-                self._Out if z else None, self._Xn, self.q, self.q_scale, self.stats, stream)
+                self.params if z else self._before, _pointers(X), Z and _pointers(Z),
+                self.post_gamma if z else None, self.post_beta if z else None, gate, self.pre_gamma,
+                self.pre_beta, _pointers(self._Out) if z else None, self._Xn and _pointers(self._Xn),
+                self.q, self.q_scale, self.stats, binding.stream_on(self.device, stream))
 
     def _gradients(self):
         if self._grads is None:
@@ -160,12 +165,13 @@ class DeviceNormResidual:
         _check_like(stats, (4, self.tokens), torch.float32, self.device, "stats")
         self._check_gate(gate, z)
         d = self._gradients()
-        opt = lambda x, what: None if x is None else self._list(x, what)  # noqa: E731
-        with torch.cuda.device(self.device):
+        opt = lambda x, what: None if x is None else _pointers(self._list(x, what))  # noqa: E731
+        with binding.on_device(self.device):
             binding.tpmlp_norm_backward(
                 self.params if z else self._before, opt(dOut, "dOut"), opt(dXn, "dXn"), opt(Z, "Z"),
-                self._list(Out, "Out") if self.pre != "none" else None,
+                opt(Out, "Out") if self.pre != "none" else None,
                 self.post_gamma if z else None, self.post_beta if z else None, gate, self.pre_gamma,
-                stats, d["dX"], d["dZ"] if z else None, d["dpost_gamma"] if z else None,
-                d["dpost_beta"] if z else None, d["dgate"] if z else None, d["dpre_gamma"],
-                d["dpre_beta"], d["ws"], stream)
+                stats, _pointers(d["dX"]), _pointers(d["dZ"]) if z else None,
+                d["dpost_gamma"] if z else None, d["dpost_beta"] if z else None,
+                d["dgate"] if z else None, d["dpre_gamma"], d["dpre_beta"], d["ws"],
+                binding.stream_on(self.device, stream))
