@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "abi_internal.h"
+#include "fp8_internal.h"
 #include "norm_residual.cuh"
 #include "tpmlp.h"
 
@@ -209,6 +210,8 @@ TPMLP_API tpmlp_status tpmlp_norm_backward(const tpmlp_norm_params* params, cons
     p.gate_rows = d.gate_rows > 0 ? d.gate_rows : d.tokens;
     p.h = static_cast<int>(d.hidden);
     p.alpha = d.residual_scale;
+    p.err = dev->err;
+    p.timeout_ns = g_timeout_ns;
     nr_plan(p, dev->sm_count);
     TPMLP_CUDA(timed(TPMLP_KERNEL_LAYERNORM_BWD, 2, st, [&] {
         return launch_nr_backward(p, post_of(d, z), pre_of(d), st);

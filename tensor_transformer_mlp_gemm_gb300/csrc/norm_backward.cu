@@ -8,13 +8,16 @@
 // are loaded while this one is worked on.
 //
 // 512 threads hold 4096 columns.  Wider rows take a cluster of 2 or 4 CTAs side by
-// side, whose row sums meet in each other's shared memory: each warp writes its part
-// into every CTA's copy, one cluster barrier, and every warp adds all parts in the
-// same order.  A row has two such sums, as dZ needs dOut_total's row sum first.
+// side, whose row sums meet in each other's shared memory: each warp sends its part
+// to every CTA, counted on that CTA's mbarrier, and every warp adds all parts in the
+// same order.  (A cluster barrier instead waits for the row's own loads and stores
+// too: 6600 clocks a row, measured at 917 x 9000.)  A row has two such sums, as dZ
+// needs dX's row sum first.
 // The column sums of a block go to a partial row, and a second kernel adds the blocks
 // in order; a gate whose rows lie in one block is finished there and then.  No atomics.
 #include <algorithm>
 
+#include "gemm_params.h"
 #include "norm_device.cuh"
 #include "norm_residual.cuh"
 #include "ptx.cuh"
@@ -32,46 +35,77 @@ static_assert(NB_COLS * NB_MAX_CLUSTER >= NR_MAX_H, "a cluster holds the widest 
 
 int cluster_of(long long h) { return h <= NB_COLS ? 1 : h <= 2 * NB_COLS ? 2 : 4; }
 
-__device__ __forceinline__ void store_cluster(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// A float into a CTA of the cluster, its four bytes counted on that CTA's mbarrier.
+__device__ __forceinline__ void send(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                     addr),
+                 "r"(__float_as_uint(v)), "r"(bar)
+                 : "memory");
 }
 
-// Sums of two values over the row (all CTAs of the cluster), in a fixed order.
-// smem[buf][value][CTA * 16 + warp]; buf alternates from call to call.
+// What the row sums of a CTA need: the parts [buf][value][CTA * 16 + warp], two
+// mbarriers, and the limit of a wait.
+struct Sums {
+    float part[2][2][NB_MAX_CLUSTER * NB_WARPS];
+    alignas(8) uint64_t bar[2];
+};
+struct SumState {
+    int buf;
+    uint32_t phase[2];
+    int rank;
+    unsigned long long timeout_ns;
+    unsigned* err;
+};
+
+// Sums of one or two values over the row (all CTAs of the cluster), in a fixed order.
+// The buffers alternate: a part of the next but one sum can only be sent once every
+// warp has sent its part of the next, and so has read this one.
 template <int CL, bool TWO>
-__device__ __forceinline__ void row_sum(float& a, float& b,
-                                        float (*smem)[2][NB_MAX_CLUSTER * NB_WARPS], int& buf,
-                                        int rank) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ void row_sum(float& a, float& b, Sums& sm, SumState& st) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, buf = st.buf;
     a = warp_sum(a);
     if (TWO) b = warp_sum(b);
     if constexpr (CL == 1) {
         if (lane == 0) {
-            smem[buf][0][warp] = a;
-            if (TWO) smem[buf][1][warp] = b;
+            sm.part[buf][0][warp] = a;
+            if (TWO) sm.part[buf][1][warp] = b;
         }
         __syncthreads();
     } else {
+        const uint32_t bar = ptx::smem_u32(&sm.bar[buf]);
+        if (threadIdx.x == 0)
+            ptx::mbar_arrive_expect_tx(bar, CL * NB_WARPS * (TWO ? 8 : 4));
         if (lane < CL) {
-            const uint32_t dst = ptx::mapa_shared(ptx::smem_u32(&smem[buf][0][rank * NB_WARPS + warp]),
-                                                  static_cast<uint32_t>(lane));
-            store_cluster(dst, a);
-            if (TWO) store_cluster(dst + NB_MAX_CLUSTER * NB_WARPS * 4, b);
+            const uint32_t to = static_cast<uint32_t>(lane);
+            const uint32_t rbar = ptx::mapa_shared(bar, to);
+            send(ptx::mapa_shared(ptx::smem_u32(&sm.part[buf][0][st.rank * NB_WARPS + warp]), to), a, rbar);
+            if (TWO)
+                send(ptx::mapa_shared(ptx::smem_u32(&sm.part[buf][1][st.rank * NB_WARPS + warp]), to), b,
+                     rbar);
         }
         __syncwarp();
-        ptx::cluster_sync();
+        if (!ptx::mbar_try_wait(bar, st.phase[buf])) {
+            const uint64_t t0 = ptx::globaltimer_ns();
+            while (!ptx::mbar_try_wait(bar, st.phase[buf])) {
+                if (ptx::globaltimer_ns() - t0 > st.timeout_ns) {
+                    atomicOr(st.err, ERR_EPILOGUE);
+                    break;
+                }
+            }
+        }
+        st.phase[buf] ^= 1u;
     }
     float s = 0.0f, t = 0.0f;
 #pragma unroll
     for (int i = 0; i < (CL * NB_WARPS + 31) / 32; ++i) {
         if (i * 32 + lane < CL * NB_WARPS) {
-            s += smem[buf][0][i * 32 + lane];
-            if (TWO) t += smem[buf][1][i * 32 + lane];
+            s += sm.part[buf][0][i * 32 + lane];
+            if (TWO) t += sm.part[buf][1][i * 32 + lane];
         }
     }
     a = warp_sum(s);
     if (TWO) b = warp_sum(t);
-    buf ^= 1;
+    st.buf ^= 1;
 }
 
 template <int POST, int PRE, int CL>
@@ -79,15 +113,23 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
     nr_backward_kernel(const __grid_constant__ NrBackwardParams p) {
     constexpr bool Z = POST != NR_ABSENT, POST_NORM = POST >= NR_POST_RMS;
     constexpr bool POST_LAYER = POST == NR_POST_LAYER, PRE_LAYER = PRE == NR_PRE_LAYER;
-    __shared__ float smem[2][2][NB_MAX_CLUSTER * NB_WARPS];
-    int buf = 0;
+    __shared__ Sums sm;
     const int rank = CL == 1 ? 0 : static_cast<int>(ptx::cluster_ctarank());
+    SumState ss = {0, {0, 0}, rank, p.timeout_ns, p.err};
     const long long block = blockIdx.x / CL;
     const float inv_h = 1.0f / static_cast<float>(p.h);
     const int c = (rank * NB_THREADS + threadIdx.x) * 8;
     const bool in = c < p.h;
+    if constexpr (CL > 1) {
+        if (threadIdx.x == 0) {
+            ptx::mbar_init(ptx::smem_u32(&sm.bar[0]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sm.bar[1]), 1);
+            ptx::fence_mbar_init();
+        }
+        __syncwarp();
+        ptx::cluster_sync();  // all of the cluster's barriers exist
+    }
     ptx::griddep_wait();
-    if constexpr (CL > 1) ptx::cluster_sync();  // the CTAs that write here have started, too
 
     auto weight = [&](const void* w) {
         return in ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + c)) : zero4();
@@ -182,7 +224,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
                 sv = fmaf(w[i], v[i], sv);
                 if (PRE_LAYER) sw += w[i];
             }
-            row_sum<CL, PRE_LAYER>(sv, sw, smem, buf, rank);
+            row_sum<CL, PRE_LAYER>(sv, sw, sm, ss);
             const float mv = sv * inv_h, mw = PRE_LAYER ? sw * inv_h : 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[i] = fmaf(cur.r2, w[i] - mw - v[i] * mv, g[i]);
@@ -221,7 +263,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
                     sv = fmaf(w[i], z[i], sv);
                     if (POST_LAYER) sw += w[i];
                 }
-                row_sum<CL, POST_LAYER>(sv, sw, smem, buf, rank);
+                row_sum<CL, POST_LAYER>(sv, sw, sm, ss);
                 const float mv = sv * inv_h, mw = POST_LAYER ? sw * inv_h : 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) g[i] = cur.r1 * (w[i] - mw - z[i] * mv);

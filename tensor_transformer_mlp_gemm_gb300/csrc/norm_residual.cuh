@@ -65,6 +65,8 @@ struct NrBackwardParams {
     // rows of a block: see nr_plan
     long long seqs, blocks, rows_per_block, seqs_per_block;
     int blocks_per_seq;
+    unsigned int* err;           // the device error word and the limit of any one wait
+    unsigned long long timeout_ns;
 };
 
 cudaError_t launch_nr_forward(const NrForwardParams& p, int post, int pre, int sm_count,
