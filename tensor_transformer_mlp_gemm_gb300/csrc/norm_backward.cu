@@ -4,17 +4,20 @@
 // What bounds it: HBM traffic, dOut, dXn, Z and Out read and dX and dZ written once
 // (12 bytes an element).  So everything a row gives, its two data gradients and its
 // share of up to five column sums, comes from one pass: a thread keeps the sums of
-// its 8 columns in registers over all rows of its block, and the next row's vectors
-// are loaded while this one is worked on.
+// its 8 columns in registers over all of its rows.
 //
-// 512 threads hold 4096 columns.  Wider rows take a cluster of 2 or 4 CTAs side by
-// side, whose row sums meet in each other's shared memory: each warp sends its part
-// to every CTA, counted on that CTA's mbarrier, and every warp adds all parts in the
-// same order.  (A cluster barrier instead waits for the row's own loads and stores
-// too: 6600 clocks a row, measured at 917 x 9000.)  A row has two such sums, as dZ
-// needs dX's row sum first.
-// The column sums of a block go to a partial row, and a second kernel adds the blocks
-// in order; a gate whose rows lie in one block is finished there and then.  No atomics.
+// A row has two sums over its columns, one after the other (dZ needs dX's first), and
+// one row at a time spent 2800 clocks on them whatever its width, where 4096 columns
+// are worth 2100 of HBM time.  So a group of threads takes two rows at a time, narrow
+// rows are spread over up to 8 groups of a CTA's 512 threads, and one thread of a group
+// keeps bulk copies of its next rows under way into a ring in shared memory.
+// Rows of more than 4096 columns take a cluster of 2 or 4 CTAs side by side, whose row
+// sums meet in each other's shared memory: each warp sends its part to every CTA,
+// counted on that CTA's mbarrier, and every warp adds all parts in the same order.  (A
+// cluster barrier instead waits for the row's own loads and stores too: 6600 clocks a
+// row, measured at 917 x 9000.)
+// The column sums of a block of rows go to a partial row, and a second kernel adds the
+// blocks in order; a gate whose rows lie in one group is finished there.  No atomics.
 #include <algorithm>
 
 #include "gemm_params.h"
@@ -31,9 +34,20 @@ constexpr int NB_THREADS = 512;
 constexpr int NB_COLS = NB_THREADS * 8;  // columns of one CTA
 constexpr int NB_WARPS = NB_THREADS / 32;
 constexpr int NB_MAX_CLUSTER = 4;
+constexpr int NB_MAX_GROUPS = 8;
+constexpr int NB_ROWS = 2;               // rows a group takes at a time
+constexpr int NB_ARRAYS = 5;             // dOut, dXn, Out, Z, gate
+constexpr int NB_STAGES = 2;             // row pairs in the ring
+constexpr int NB_RING = NB_STAGES * NB_ROWS * NB_ARRAYS * NB_COLS * 2;
 static_assert(NB_COLS * NB_MAX_CLUSTER >= NR_MAX_H, "a cluster holds the widest row");
 
+// CTAs side by side for a row, and groups of a CTA's threads that take rows of their own.
 int cluster_of(long long h) { return h <= NB_COLS ? 1 : h <= 2 * NB_COLS ? 2 : 4; }
+int groups_of(long long h) {
+    int g = 1;
+    while (g < NB_MAX_GROUPS && h <= NB_COLS / (2 * g)) g *= 2;
+    return g;
+}
 
 // A float into a CTA of the cluster, its four bytes counted on that CTA's mbarrier.
 __device__ __forceinline__ void send(uint32_t addr, float v, uint32_t bar) {
@@ -43,92 +57,129 @@ __device__ __forceinline__ void send(uint32_t addr, float v, uint32_t bar) {
                  : "memory");
 }
 
-// What the row sums of a CTA need: the parts [buf][value][CTA * 16 + warp], two
-// mbarriers, and the limit of a wait.
-struct Sums {
-    float part[2][2][NB_MAX_CLUSTER * NB_WARPS];
-    alignas(8) uint64_t bar[2];
+// What the sums of a CTA need: the parts [group][buf][value][slot], a slot for each warp
+// of the row, mbarriers (the cluster's sums, the ring), and the limit of a wait.
+constexpr int NB_VALUES = 2 * NB_ROWS;
+struct Shared {
+    float part[2][NB_VALUES * NB_MAX_CLUSTER * NB_WARPS];  // groups side by side
+    alignas(8) uint64_t sum_bar[2];
+    uint64_t ring_bar[NB_MAX_GROUPS][NB_STAGES];
 };
-struct SumState {
-    int buf;
-    uint32_t phase[2];
-    int rank;
+struct Waits {
     unsigned long long timeout_ns;
     unsigned* err;
 };
 
-// Sums of one or two values over the row (all CTAs of the cluster), in a fixed order.
-// The buffers alternate: a part of the next but one sum can only be sent once every
-// warp has sent its part of the next, and so has read this one.
-template <int CL, bool TWO>
-__device__ __forceinline__ void row_sum(float& a, float& b, Sums& sm, SumState& st) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, buf = st.buf;
-    a = warp_sum(a);
-    if (TWO) b = warp_sum(b);
-    if constexpr (CL == 1) {
-        if (lane == 0) {
-            sm.part[buf][0][warp] = a;
-            if (TWO) sm.part[buf][1][warp] = b;
-        }
-        __syncthreads();
-    } else {
-        const uint32_t bar = ptx::smem_u32(&sm.bar[buf]);
-        if (threadIdx.x == 0)
-            ptx::mbar_arrive_expect_tx(bar, CL * NB_WARPS * (TWO ? 8 : 4));
-        if (lane < CL) {
-            const uint32_t to = static_cast<uint32_t>(lane);
-            const uint32_t rbar = ptx::mapa_shared(bar, to);
-            send(ptx::mapa_shared(ptx::smem_u32(&sm.part[buf][0][st.rank * NB_WARPS + warp]), to), a, rbar);
-            if (TWO)
-                send(ptx::mapa_shared(ptx::smem_u32(&sm.part[buf][1][st.rank * NB_WARPS + warp]), to), b,
-                     rbar);
-        }
-        __syncwarp();
-        if (!ptx::mbar_try_wait(bar, st.phase[buf])) {
-            const uint64_t t0 = ptx::globaltimer_ns();
-            while (!ptx::mbar_try_wait(bar, st.phase[buf])) {
-                if (ptx::globaltimer_ns() - t0 > st.timeout_ns) {
-                    atomicOr(st.err, ERR_EPILOGUE);
-                    break;
-                }
-            }
-        }
-        st.phase[buf] ^= 1u;
-    }
-    float s = 0.0f, t = 0.0f;
-#pragma unroll
-    for (int i = 0; i < (CL * NB_WARPS + 31) / 32; ++i) {
-        if (i * 32 + lane < CL * NB_WARPS) {
-            s += sm.part[buf][0][i * 32 + lane];
-            if (TWO) t += sm.part[buf][1][i * 32 + lane];
+__device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, const Waits& w) {
+    if (ptx::mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (ptx::globaltimer_ns() - t0 > w.timeout_ns) {
+            atomicOr(w.err, ERR_EPILOGUE);
+            return;
         }
     }
-    a = warp_sum(s);
-    if (TWO) b = warp_sum(t);
-    st.buf ^= 1;
 }
 
-template <int POST, int PRE, int CL>
-__global__ void __launch_bounds__(NB_THREADS, 1)
-    nr_backward_kernel(const __grid_constant__ NrBackwardParams p) {
-    constexpr bool Z = POST != NR_ABSENT, POST_NORM = POST >= NR_POST_RMS;
-    constexpr bool POST_LAYER = POST == NR_POST_LAYER, PRE_LAYER = PRE == NR_PRE_LAYER;
-    __shared__ Sums sm;
-    const int rank = CL == 1 ? 0 : static_cast<int>(ptx::cluster_ctarank());
-    SumState ss = {0, {0, 0}, rank, p.timeout_ns, p.err};
-    const long long block = blockIdx.x / CL;
-    const float inv_h = 1.0f / static_cast<float>(p.h);
-    const int c = (rank * NB_THREADS + threadIdx.x) * 8;
-    const bool in = c < p.h;
-    if constexpr (CL > 1) {
-        if (threadIdx.x == 0) {
-            ptx::mbar_init(ptx::smem_u32(&sm.bar[0]), 1);
-            ptx::mbar_init(ptx::smem_u32(&sm.bar[1]), 1);
-            ptx::fence_mbar_init();
+// Sums of N (1, 2 or 4) values over the warp: value n's is left in the 32 / N lanes from
+// n * 32 / N on.  Halving the values at each of the first steps takes 5 or 6 shuffles.
+template <int N>
+__device__ __forceinline__ float warp_sums(const float (&v)[N], int lane) {
+    float x;
+    if constexpr (N == 4) {
+        const bool up = lane & 16, odd = lane & 8;
+        float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
+        a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+        b += __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
+        x = odd ? b : a;
+        x += __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+    } else if constexpr (N == 2) {
+        const bool up = lane & 16;
+        x = up ? v[1] : v[0];
+        x += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], 16);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+    } else {
+        x = v[0];
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+    }
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// Sums of N values over a row: the group's warps, and the cluster's CTAs.  The buffers
+// alternate: a part of the next but one sum can only come once every warp has given its
+// part of the next, and so has read this one.
+template <int CL, int G, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], Shared& sm, int& buf, uint32_t (&phase)[2],
+                                         int group, int rank, const Waits& w) {
+    constexpr int WG = NB_WARPS / G, SLOTS = CL * WG, LP = 32 / N;
+    const int warp = (threadIdx.x >> 5) % WG, lane = threadIdx.x & 31;
+    float* part = sm.part[buf] + group * (NB_VALUES * WG);
+    const float x = warp_sums<N>(v, lane);
+    const int n = lane / LP, slot = rank * WG + warp;
+    if constexpr (CL == 1) {
+        if (lane % LP == 0) part[n * SLOTS + slot] = x;
+        if constexpr (WG > 1)
+            asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(WG * 32) : "memory");
+        else
+            __syncwarp();
+    } else {
+        const uint32_t bar = ptx::smem_u32(&sm.sum_bar[buf]);
+        if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bar, SLOTS * N * 4);
+        // lane n * LP + i sends value n to CTA i
+        if (lane % LP < CL) {
+            const uint32_t to = static_cast<uint32_t>(lane % LP);
+            send(ptx::mapa_shared(ptx::smem_u32(part + n * SLOTS + slot), to), x,
+                 ptx::mapa_shared(bar, to));
         }
         __syncwarp();
-        ptx::cluster_sync();  // all of the cluster's barriers exist
+        wait_on(bar, phase[buf], w);
+        phase[buf] ^= 1u;
     }
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < (SLOTS + LP - 1) / LP; ++i)
+        if (i * LP + lane % LP < SLOTS) t += part[n * SLOTS + i * LP + lane % LP];
+#pragma unroll
+    for (int o = LP / 2; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, t, i * LP);
+    buf ^= 1;
+}
+
+template <int POST, int PRE, int CL, int G>
+__global__ void __launch_bounds__(NB_THREADS, 1)
+    nr_backward_kernel(const __grid_constant__ NrBackwardParams p) {
+    constexpr bool Z = POST != NR_ABSENT, POST_NORM = POST >= NR_POST_RMS, BEFORE = PRE != NR_NONE;
+    constexpr bool POST_LAYER = POST == NR_POST_LAYER, PRE_LAYER = PRE == NR_PRE_LAYER;
+    constexpr int R = NB_ROWS, GT = NB_THREADS / G, ROW = GT * 16;  // a row's bytes in the ring
+    static_assert(CL == 1 || G == 1, "wide rows take whole CTAs");
+    extern __shared__ __align__(128) uint8_t ring_all[];
+    __shared__ Shared sm;
+    const int rank = CL == 1 ? 0 : static_cast<int>(ptx::cluster_ctarank());
+    const int group = threadIdx.x / GT, tid = threadIdx.x % GT, lane = threadIdx.x & 31;
+    const long long block = blockIdx.x / CL;
+    const float inv_h = 1.0f / static_cast<float>(p.h);
+    const int c0 = rank * NB_COLS, c = c0 + tid * 8;
+    const bool in = c < p.h;
+    const Waits waits = {p.timeout_ns, p.err};
+    const bool gate = Z && p.gate != nullptr, dout = p.dout.p[0] != nullptr;
+    uint8_t* ring = ring_all + group * (NB_STAGES * R * NB_ARRAYS * ROW);
+    int buf = 0;
+    uint32_t phase[2] = {0, 0};
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(ptx::smem_u32(&sm.sum_bar[0]), 1);
+        ptx::mbar_init(ptx::smem_u32(&sm.sum_bar[1]), 1);
+        for (int g = 0; g < G; ++g)
+            for (int s = 0; s < NB_STAGES; ++s) ptx::mbar_init(ptx::smem_u32(&sm.ring_bar[g][s]), 1);
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    __syncthreads();
+    if constexpr (CL > 1) ptx::cluster_sync();  // all of the cluster's barriers exist
     ptx::griddep_wait();
 
     auto weight = [&](const void* w) {
@@ -136,172 +187,264 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
     };
     const uint4 w1 = POST_NORM ? weight(p.post_gamma) : zero4();
     const uint4 b1 = POST_LAYER ? weight(p.post_beta) : zero4();
-    const uint4 w2 = PRE != NR_NONE ? weight(p.pre_gamma) : zero4();
+    const uint4 w2 = BEFORE ? weight(p.pre_gamma) : zero4();
 
-    // this block's rows
-    long long row, last, next_gate;
-    if (p.blocks_per_seq > 0) {
-        const long long seq = block / p.blocks_per_seq;
-        const long long first = seq * p.gate_rows;
-        row = first + (block - seq * p.blocks_per_seq) * p.rows_per_block;
-        next_gate = first + p.gate_rows;  // the whole block lies before it
-        last = min(row + p.rows_per_block, next_gate);
+    // this group's rows: a part of a cut gate's, or whole gates
+    const bool cut = p.blocks_per_seq > 0;
+    long long row, last;
+    if (cut) {
+        const long long seq = block / p.blocks_per_seq, first = seq * p.gate_rows;
+        const long long b0 = first + (block - seq * p.blocks_per_seq) * p.rows_per_block;
+        const long long b1r = min(b0 + p.rows_per_block, first + p.gate_rows);
+        const long long per = (p.rows_per_block + G - 1) / G;
+        row = min(b0 + group * per, b1r);
+        last = min(row + per, b1r);
     } else {
-        row = block * p.seqs_per_block * p.gate_rows;
-        next_gate = row + p.gate_rows;
-        last = min(row + p.seqs_per_block * p.gate_rows, p.T);
+        const long long per = p.seqs_per_group * p.gate_rows;
+        row = min((block * G + group) * per, p.T);
+        last = min(row + per, p.T);
     }
-    const bool gate = Z && p.gate != nullptr;
 
-    float s_pre[PRE != NR_NONE ? 8 : 1] = {}, s_pre_b[PRE_LAYER ? 8 : 1] = {};
+    // the ring: one thread of the group has the copies of a row pair under way
+    const int cols = min(NB_COLS / G, p.h - c0);
+    const uint32_t bytes = cols > 0 ? static_cast<uint32_t>(cols) * 2 : 0;
+    auto copy_rows = [&](long long r0, int stage) {
+        const uint32_t bar = ptx::smem_u32(&sm.ring_bar[group][stage]);
+        const int n = r0 + 1 < last ? 2 : 1;
+        const int arrays = (dout ? 1 : 0) + (BEFORE ? 2 : 0) + (Z ? 1 : 0) + (gate ? 1 : 0);
+        ptx::mbar_arrive_expect_tx(bar, bytes * static_cast<uint32_t>(n * arrays));
+        if (bytes == 0) return;
+        for (int i = 0; i < n; ++i) {
+            const long long r = r0 + i;
+            const int k = static_cast<int>(r / p.rows_per_chunk);
+            const long long off = (r - k * p.rows_per_chunk) * p.h + c0;
+            const uint32_t dst = ptx::smem_u32(ring) + (stage * R + i) * (NB_ARRAYS * ROW);
+            auto get = [&](int a, const void* base, long long o) {
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                        dst + a * ROW),
+                    "l"(static_cast<const __nv_bfloat16*>(base) + o), "r"(bytes), "r"(bar)
+                    : "memory");
+            };
+            if (dout) get(0, p.dout.p[k], off);
+            if (BEFORE) {
+                get(1, p.dxn.p[k], off);
+                get(2, p.out.p[k], off);
+            }
+            if (Z) get(3, p.z.p[k], off);
+            if (gate) get(4, p.gate, r / p.gate_rows * p.h + c0);
+        }
+    };
+    if (tid == 0) {
+#pragma unroll
+        for (int s = 0; s < NB_STAGES; ++s)
+            if (row + s * R < last) copy_rows(row + s * R, s);
+    }
+    // lane 4 i + k has statistic k of the pair's row i
+    auto load_stats = [&](long long r0) {
+        const long long r = r0 + (lane >> 2);
+        return lane < 4 * R && r < last && (POST_NORM || BEFORE)
+                   ? __ldg(p.stats + (lane & 3) * p.T + r)
+                   : 0.0f;
+    };
+    float stat = load_stats(row);
+
+    float s_pre[BEFORE ? 8 : 1] = {}, s_pre_b[PRE_LAYER ? 8 : 1] = {};
     float s_post[POST_NORM ? 8 : 1] = {}, s_post_b[POST_LAYER ? 8 : 1] = {};
     float s_gate[Z ? 8 : 1] = {};
-    uint4 gate_v = zero4();
-
-    struct Row {
-        uint4 dout, dxn, z, out;
-        float m1, r1, m2, r2;
-    };
-    auto load = [&](long long r, Row& d) {
-        const int k = static_cast<int>(r / p.rows_per_chunk);
-        const long long off = (r - k * p.rows_per_chunk) * p.h + c;
-        auto get = [&](const void* base) {
-            return in ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + off))
-                      : zero4();
-        };
-        d.dout = p.dout.p[0] ? get(p.dout.p[k]) : zero4();
-        if (PRE != NR_NONE) {
-            d.dxn = get(p.dxn.p[k]);
-            d.out = get(p.out.p[k]);
-            d.m2 = PRE_LAYER ? __ldg(p.stats + 2 * p.T + r) : 0.0f;
-            d.r2 = __ldg(p.stats + 3 * p.T + r);
-        }
-        if (Z) d.z = get(p.z.p[k]);
-        if (POST_NORM) {
-            d.m1 = POST_LAYER ? __ldg(p.stats + r) : 0.0f;
-            d.r1 = __ldg(p.stats + p.T + r);
-        }
-    };
-    auto load_gate = [&](long long r) {
-        if (gate)
-            gate_v = in ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.gate) +
-                                                               r / p.gate_rows * p.h + c))
-                        : zero4();
-    };
-    auto finish_gate = [&](float* dst) {
-        if (in) {
-            reinterpret_cast<float4*>(dst + c)[0] = make_float4(s_gate[0], s_gate[1], s_gate[2], s_gate[3]);
-            reinterpret_cast<float4*>(dst + c)[1] = make_float4(s_gate[4], s_gate[5], s_gate[6], s_gate[7]);
-        }
+    int stage = 0;
+    uint32_t ring_phase = 0;
+    for (; row < last; row += R) {
+        wait_on(ptx::smem_u32(&sm.ring_bar[group][stage]), ring_phase, waits);
+        uint4 q_dout[R], q_dxn[R], q_out[R], q_z[R], q_gate[R];
+        float m1[R], r1[R], m2[R], r2[R];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s_gate[i] = 0.0f;
-    };
-
-    Row cur;
-    if (row < last) {
-        load(row, cur);
-        if constexpr (Z) load_gate(row);
-    }
-    while (row < last) {
-        Row nxt;
-        if (row + 1 < last) load(row + 1, nxt);
-        const int k = static_cast<int>(row / p.rows_per_chunk);
-        const long long off = (row - k * p.rows_per_chunk) * p.h + c;
-        float g[8];
-        unpack(cur.dout, g);
-        if constexpr (PRE != NR_NONE) {
-            float d[8], v[8], w[8];
-            unpack(cur.dxn, d);
-            unpack(cur.out, v);
-            unpack(w2, w);
-            float sv = 0.0f, sw = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] = in ? (v[i] - cur.m2) * cur.r2 : 0.0f;
-                s_pre[i] = fmaf(d[i], v[i], s_pre[i]);
-                if (PRE_LAYER) s_pre_b[i] += d[i];
-                w[i] *= d[i];
-                sv = fmaf(w[i], v[i], sv);
-                if (PRE_LAYER) sw += w[i];
+        for (int i = 0; i < R; ++i) {
+            const bool ok = in && row + i < last;
+            const uint8_t* src = ring + (stage * R + i) * (NB_ARRAYS * ROW) + tid * 16;
+            auto get = [&](int a) { return ok ? *reinterpret_cast<const uint4*>(src + a * ROW) : zero4(); };
+            q_dout[i] = dout ? get(0) : zero4();
+            if (BEFORE) {
+                q_dxn[i] = get(1);
+                q_out[i] = get(2);
             }
-            row_sum<CL, PRE_LAYER>(sv, sw, sm, ss);
-            const float mv = sv * inv_h, mw = PRE_LAYER ? sw * inv_h : 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = fmaf(cur.r2, w[i] - mw - v[i] * mv, g[i]);
+            if (Z) q_z[i] = get(3);
+            q_gate[i] = gate ? get(4) : zero4();
+            // (a row that is not there has statistics 0: nothing comes of it)
+            m1[i] = POST_LAYER ? __shfl_sync(0xffffffffu, stat, 4 * i) : 0.0f;
+            r1[i] = POST_NORM ? __shfl_sync(0xffffffffu, stat, 4 * i + 1) : 0.0f;
+            m2[i] = PRE_LAYER ? __shfl_sync(0xffffffffu, stat, 4 * i + 2) : 0.0f;
+            r2[i] = BEFORE ? __shfl_sync(0xffffffffu, stat, 4 * i + 3) : 0.0f;
         }
-        {
-            float o[8];
+        stat = load_stats(row + R);
+
+        float g[R][8];
+        if constexpr (BEFORE) {
+            constexpr int N = PRE_LAYER ? 2 * R : R;
+            float sums[N];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = Z ? p.alpha * g[i] : g[i];
-            if (in) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dx[k]) + off) = pack(o);
+            for (int i = 0; i < R; ++i) {
+                float d[8], v[8], w[8];
+                unpack(q_dxn[i], d);
+                unpack(q_out[i], v);
+                unpack(w2, w);
+                float sv = 0.0f, sw = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float hat = in ? (v[e] - m2[i]) * r2[i] : 0.0f;
+                    s_pre[e] = fmaf(d[e], hat, s_pre[e]);
+                    if (PRE_LAYER) s_pre_b[e] += d[e];
+                    const float wd = w[e] * d[e];
+                    sv = fmaf(wd, hat, sv);
+                    if (PRE_LAYER) sw += wd;
+                }
+                sums[i] = sv;
+                if (PRE_LAYER) sums[R + i] = sw;
+            }
+            row_sums<CL, G, N>(sums, sm, buf, phase, group, rank, waits);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float d[8], v[8], w[8];
+                unpack(q_dxn[i], d);
+                unpack(q_out[i], v);
+                unpack(w2, w);
+                unpack(q_dout[i], g[i]);
+                const float mv = sums[i] * inv_h, mw = PRE_LAYER ? sums[R + i] * inv_h : 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float hat = (v[e] - m2[i]) * r2[i];
+                    g[i][e] = fmaf(r2[i], w[e] * d[e] - mw - hat * mv, g[i][e]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) unpack(q_dout[i], g[i]);
+            if constexpr (CL > 1 || NB_WARPS / G > 1)
+                asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(GT) : "memory");
+            else
+                __syncwarp();
+        }
+        // every thread of the group has read this stage
+        if (tid == 0 && row + NB_STAGES * R < last) copy_rows(row + NB_STAGES * R, stage);
+        if (++stage == NB_STAGES) {
+            stage = 0;
+            ring_phase ^= 1u;
+        }
+        int k[R];
+        long long off[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            k[i] = static_cast<int>((row + i) / p.rows_per_chunk);
+            off[i] = (row + i - k[i] * p.rows_per_chunk) * p.h + c;
+            if (in && row + i < last) {
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = Z ? p.alpha * g[i][e] : g[i][e];
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dx[k[i]]) + off[i]) = pack(o);
+            }
         }
         if constexpr (Z) {
-            float z[8], w[8], b[8], t[8];
-            unpack(cur.z, z);
+            constexpr int N = POST_LAYER ? 2 * R : R;
+            float sums[N];
+            float w[8], b[8];
             unpack(w1, w);
             unpack(b1, b);
-            if (POST_NORM) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[i] = in ? (z[i] - cur.m1) * cur.r1 : 0.0f;
-            }
-            if (gate) {
-                unpack(gate_v, t);
+            for (int i = 0; i < R; ++i) {
+                float z[8], t[8];
+                unpack(q_z[i], z);
+                unpack(q_gate[i], t);
+                float sv = 0.0f, sw = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float u = POST_NORM ? (POST_LAYER ? fmaf(z[i], w[i], b[i]) : z[i] * w[i]) : z[i];
-                    s_gate[i] = fmaf(g[i], u, s_gate[i]);
-                    g[i] *= t[i];
+                for (int e = 0; e < 8; ++e) {
+                    const float hat = POST_NORM ? (in ? (z[e] - m1[i]) * r1[i] : 0.0f) : z[e];
+                    if (gate) {
+                        const float u = POST_LAYER ? fmaf(hat, w[e], b[e]) : POST_NORM ? hat * w[e] : hat;
+                        s_gate[e] = fmaf(g[i][e], u, s_gate[e]);
+                        g[i][e] *= t[e];
+                    }
+                    if (POST_NORM) {
+                        s_post[e] = fmaf(g[i][e], hat, s_post[e]);
+                        if (POST_LAYER) s_post_b[e] += g[i][e];
+                        const float wd = w[e] * g[i][e];
+                        sv = fmaf(wd, hat, sv);
+                        if (POST_LAYER) sw += wd;
+                    }
+                }
+                if (POST_NORM) {
+                    sums[i] = sv;
+                    if (POST_LAYER) sums[R + i] = sw;
+                }
+                if (gate && !cut && row + i < last && (row + i + 1) % p.gate_rows == 0) {
+                    // the gate's last row: its sum is complete
+                    if (in) {
+                        float4* dst = reinterpret_cast<float4*>(p.dgate + (row + i) / p.gate_rows * p.h + c);
+                        dst[0] = make_float4(s_gate[0], s_gate[1], s_gate[2], s_gate[3]);
+                        dst[1] = make_float4(s_gate[4], s_gate[5], s_gate[6], s_gate[7]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s_gate[e] = 0.0f;
                 }
             }
             if constexpr (POST_NORM) {
-                float sv = 0.0f, sw = 0.0f;
+                row_sums<CL, G, N>(sums, sm, buf, phase, group, rank, waits);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s_post[i] = fmaf(g[i], z[i], s_post[i]);
-                    if (POST_LAYER) s_post_b[i] += g[i];
-                    w[i] *= g[i];
-                    sv = fmaf(w[i], z[i], sv);
-                    if (POST_LAYER) sw += w[i];
+                for (int i = 0; i < R; ++i) {
+                    float z[8];
+                    unpack(q_z[i], z);
+                    const float mv = sums[i] * inv_h, mw = POST_LAYER ? sums[R + i] * inv_h : 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float hat = (z[e] - m1[i]) * r1[i];
+                        g[i][e] = r1[i] * (w[e] * g[i][e] - mw - hat * mv);
+                    }
                 }
-                row_sum<CL, POST_LAYER>(sv, sw, sm, ss);
-                const float mv = sv * inv_h, mw = POST_LAYER ? sw * inv_h : 0.0f;
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] = cur.r1 * (w[i] - mw - z[i] * mv);
-            }
-            if (in) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dz[k]) + off) = pack(g);
-        }
-        ++row;
-        cur = nxt;
-        if constexpr (Z) {
-            if (gate && p.blocks_per_seq == 0 && row == next_gate) {
-                // the gate's last row: its sum is complete
-                finish_gate(p.dgate + (row - 1) / p.gate_rows * p.h);
-                next_gate += p.gate_rows;
-                if (row < last) load_gate(row);
-            }
+            for (int i = 0; i < R; ++i)
+                if (in && row + i < last)
+                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dz[k[i]]) + off[i]) = pack(g[i]);
         }
     }
 
-    // this block's column sums: one partial row for each vector
+    // the block's column sums, the groups' added in order: one partial row for each vector
+    ptx::griddep_launch_dependents();
     int v = 0;
-    const int nv = (PRE != NR_NONE) + PRE_LAYER + POST_NORM + POST_LAYER;
-    float* part = p.part + block * (nv + (gate && p.blocks_per_seq > 0)) * p.h;
+    const int nv = (BEFORE ? 1 : 0) + (PRE_LAYER ? 1 : 0) + (POST_NORM ? 1 : 0) + (POST_LAYER ? 1 : 0);
+    float* part = p.part + block * (nv + (gate && cut ? 1 : 0)) * p.h;
+    float* meet = reinterpret_cast<float*>(ring_all);  // [group][columns]: the ring is done with
     auto put = [&](const float* s) {
-        if (in) {
+        float t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = s[e];
+        if constexpr (G > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) meet[group * (GT * 8) + e * GT + tid] = t[e];
+            __syncthreads();
+            if (group == 0) {
+#pragma unroll
+                for (int q = 1; q < G; ++q)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) t[e] += meet[q * (GT * 8) + e * GT + tid];
+            }
+        }
+        if (in && group == 0) {
             float4* d = reinterpret_cast<float4*>(part + static_cast<long long>(v) * p.h + c);
-            d[0] = make_float4(s[0], s[1], s[2], s[3]);
-            d[1] = make_float4(s[4], s[5], s[6], s[7]);
+            d[0] = make_float4(t[0], t[1], t[2], t[3]);
+            d[1] = make_float4(t[4], t[5], t[6], t[7]);
         }
         ++v;
     };
-    if constexpr (PRE != NR_NONE) put(s_pre);
+    if constexpr (BEFORE) put(s_pre);
     if constexpr (PRE_LAYER) put(s_pre_b);
     if constexpr (POST_NORM) put(s_post);
     if constexpr (POST_LAYER) put(s_post_b);
     if constexpr (Z) {
-        if (gate && p.blocks_per_seq > 0) put(s_gate);
+        if (gate && cut) put(s_gate);
     }
-    ptx::griddep_launch_dependents();
+    // a CTA that has left cannot take a part that is still on its way to it: the last
+    // sums have all been waited for, so none is
 }
 
 // out[c] = sum over the blocks of a vector's partial rows, in block order within
@@ -358,11 +501,24 @@ __global__ void __launch_bounds__(256) nr_finish_kernel(const __grid_constant__ 
     }
 }
 
-template <int POST, int PRE, int CL>
+template <int POST, int PRE, int CL, int G>
 cudaError_t launch_rows(const NrBackwardParams& p, cudaStream_t st) {
+    constexpr int kDevices = 64;
+    static int ready[kDevices] = {};  // the kernel's attribute is set, per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
+        e = cudaFuncSetAttribute(nr_backward_kernel<POST, PRE, CL, G>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, NB_RING);
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.blocks * CL), 1, 1);
     cfg.blockDim = dim3(NB_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = NB_RING;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -373,15 +529,20 @@ cudaError_t launch_rows(const NrBackwardParams& p, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CL > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, nr_backward_kernel<POST, PRE, CL>, p);
+    return cudaLaunchKernelEx(&cfg, nr_backward_kernel<POST, PRE, CL, G>, p);
 }
 
 template <int POST, int PRE>
 cudaError_t launch(const NrBackwardParams& p, cudaStream_t st) {
     const int cl = cluster_of(p.h);
-    return cl == 1 ? launch_rows<POST, PRE, 1>(p, st)
-           : cl == 2 ? launch_rows<POST, PRE, 2>(p, st)
-                     : launch_rows<POST, PRE, 4>(p, st);
+    if (cl == 2) return launch_rows<POST, PRE, 2, 1>(p, st);
+    if (cl == 4) return launch_rows<POST, PRE, 4, 1>(p, st);
+    switch (groups_of(p.h)) {
+        case 1: return launch_rows<POST, PRE, 1, 1>(p, st);
+        case 2: return launch_rows<POST, PRE, 1, 2>(p, st);
+        case 4: return launch_rows<POST, PRE, 1, 4>(p, st);
+        default: return launch_rows<POST, PRE, 1, 8>(p, st);
+    }
 }
 
 template <int POST>
@@ -395,26 +556,31 @@ cudaError_t launch_pre(const NrBackwardParams& p, int pre, cudaStream_t st) {
 }  // namespace
 
 void nr_plan(NrBackwardParams& p, int sm_count) {
-    const long long units = std::max(1, std::min(sm_count, NR_MAX_UNITS) / cluster_of(p.h));
+    const long long blocks = std::max(1, std::min(sm_count, NR_MAX_UNITS) / cluster_of(p.h));
+    const long long groups = groups_of(p.h);
     p.seqs = p.T / p.gate_rows;
-    if (p.seqs >= units) {
-        p.blocks_per_seq = 0;
-        p.seqs_per_block = (p.seqs + units - 1) / units;
-        p.blocks = (p.seqs + p.seqs_per_block - 1) / p.seqs_per_block;
-        p.rows_per_block = 0;
+    p.blocks_per_seq = 0;
+    p.rows_per_block = p.seqs_per_group = 0;
+    if (p.seqs >= blocks * groups) {
+        p.seqs_per_group = (p.seqs + blocks * groups - 1) / (blocks * groups);
+        const long long used = (p.seqs + p.seqs_per_group - 1) / p.seqs_per_group;
+        p.blocks = (used + groups - 1) / groups;
     } else {
-        long long per = std::min(units / p.seqs, p.gate_rows);
+        // at least a row pair for each group
+        const long long most = std::max(1LL, p.gate_rows / (2 * groups));
+        long long per = std::max(1LL, std::min(blocks / p.seqs, most));
         p.rows_per_block = (p.gate_rows + per - 1) / per;
         per = (p.gate_rows + p.rows_per_block - 1) / p.rows_per_block;
         p.blocks_per_seq = static_cast<int>(per);
         p.blocks = p.seqs * per;
-        p.seqs_per_block = 0;
     }
 }
 
 size_t nr_partial_bytes(long long h) {
-    return static_cast<size_t>(NR_MAX_UNITS / cluster_of(h)) * 5 * static_cast<size_t>(h) *
-           sizeof(float);
+    // (gates that are cut may be more than the blocks that run at once, but fewer than
+    // their groups)
+    return static_cast<size_t>(NR_MAX_UNITS / cluster_of(h)) * groups_of(h) * 5 *
+           static_cast<size_t>(h) * sizeof(float);
 }
 
 cudaError_t launch_nr_backward(const NrBackwardParams& p, int post, int pre, cudaStream_t st) {

@@ -63,7 +63,7 @@ struct NrBackwardParams {
     int h;
     float alpha;
     // rows of a block: see nr_plan
-    long long seqs, blocks, rows_per_block, seqs_per_block;
+    long long seqs, blocks, rows_per_block, seqs_per_group;
     int blocks_per_seq;
     unsigned int* err;           // the device error word and the limit of any one wait
     unsigned long long timeout_ns;
@@ -76,7 +76,8 @@ cudaError_t launch_nr_backward(const NrBackwardParams& p, int post, int pre, cud
 
 // Row blocks of the backward pass.  A block never holds part of one gate's rows
 // and part of another's: with few gates each gate's rows are cut into
-// blocks_per_seq blocks, with many a block takes seqs_per_block whole gates.
+// blocks_per_seq blocks, with many each group of a block's threads takes
+// seqs_per_group whole gates (blocks_per_seq = 0).
 void nr_plan(NrBackwardParams& p, int sm_count);
 // The most bytes of partial sums a backward pass of this width needs.
 size_t nr_partial_bytes(long long h);
