@@ -11,7 +11,7 @@ through :mod:`binding`.  Layouts follow the C ABI (include/tpmlp.h):
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
+import functools
 
 import torch
 
@@ -25,51 +25,88 @@ def _up128(n: int) -> int:
     return -(-n // 128)
 
 
-@dataclass
+def _up256(n: int) -> int:
+    return -(-n // 256) * 256
+
+
+class _Packed:
+    """n matrices [T, C] in 8 bits with their scales, side by side in one buffer (an
+    allocation costs more host time than a launch)."""
+
+    def __init__(self, n: int, T: int, C: int, fmt: str, rows: bool, cols: bool, device):
+        self.n, self.T, self.C, self.fmt, self.device = n, T, C, fmt, device
+        self.q = T * C                                       # bytes of one matrix
+        # of its scales; every matrix's start on 16 bytes
+        self.steps = (-(-_up128(C) * T // 4) * 16, _up128(T) * C * 4)
+        # where each part starts: q and scales by rows, then by columns (None: not made)
+        at, self.at = 0, [None, None, None, None]
+        for k, (wanted, size) in enumerate(((rows, self.q), (rows, self.steps[0]),
+                                            (cols, self.q), (cols, self.steps[1]))):
+            if wanted:
+                self.at[k] = at
+                at += _up256(n * size)
+        self.buf = torch.empty(max(at, 256), dtype=torch.uint8, device=device)
+        self.base = self.buf.data_ptr()
+
+    def pointers(self, cols: bool):
+        """(q, scale) pointer arrays by rows or by columns."""
+        q, s = self.base + self.at[2 * cols], self.base + self.at[2 * cols + 1]
+        step = self.steps[cols]
+        return (_array([q + i * self.q for i in range(self.n)]),
+                _array([s + i * step for i in range(self.n)]))
+
+    def view(self, k: int, i: int):
+        """Part k of matrix i as a tensor, or None."""
+        if self.at[k] is None:
+            return None
+        T, C = self.T, self.C
+        if k % 2 == 0:
+            at = self.at[k] + i * self.q
+            return self.buf[at:at + self.q].view(DTYPES[self.fmt]).view(T, C)
+        shape = (_up128(C), T) if k == 1 else (_up128(T), C)
+        at = self.at[k] + i * self.steps[k // 2]
+        return self.buf[at:at + 4 * shape[0] * shape[1]].view(torch.float32).view(shape)
+
+
 class Fp8Tokens:
-    """One matrix of activations in 8 bits: by rows, by columns, or both."""
-    rows: torch.Tensor | None = None
-    row_scale: torch.Tensor | None = None
-    cols: torch.Tensor | None = None
-    col_scale: torch.Tensor | None = None
+    """One matrix of activations in 8 bits: by rows, by columns, or both.  The tensors
+    rows, row_scale, cols and col_scale are None where that grouping is not there."""
+
+    def __init__(self, rows: torch.Tensor | None = None, row_scale: torch.Tensor | None = None,
+                 cols: torch.Tensor | None = None, col_scale: torch.Tensor | None = None):
+        self._pack, self._i = None, 0
+        self._views = {0: rows, 1: row_scale, 2: cols, 3: col_scale}
+
+    @classmethod
+    def _of(cls, pack: _Packed, i: int) -> "Fp8Tokens":
+        x = cls.__new__(cls)
+        x._pack, x._i, x._views = pack, i, {}
+        return x
+
+    def _view(self, k: int):
+        if k not in self._views:
+            self._views[k] = self._pack.view(k, self._i)
+        return self._views[k]
+
+    rows = property(lambda self: self._view(0))
+    row_scale = property(lambda self: self._view(1))
+    cols = property(lambda self: self._view(2))
+    col_scale = property(lambda self: self._view(3))
 
 
 class Fp8Shards:
-    """The shards of one tensor in 8 bits, side by side in one buffer for each kind
-    of output: a sequence of Fp8Tokens (views of the buffers)."""
+    """The shards of one tensor in 8 bits: a sequence of Fp8Tokens."""
 
-    def __init__(self, n: int, T: int, C: int, fmt: str, rows: bool, cols: bool, dev):
-        self.n, self.T, self.C = n, T, C
-        new = lambda d, *shape: torch.empty(shape, dtype=d, device=dev)  # noqa: E731
-        # every shard's scales start on 16 bytes
-        self._pad = -(-_up128(C) * T // 4) * 4
-        self.rows = new(DTYPES[fmt], n, T, C) if rows else None
-        self.row_scale = new(torch.float32, n, self._pad) if rows else None
-        self.cols = new(DTYPES[fmt], n, T, C) if cols else None
-        self.col_scale = new(torch.float32, n, _up128(T), C) if cols else None
+    def __init__(self, pack: _Packed):
+        self._pack = pack
 
     def __len__(self) -> int:
-        return self.n
+        return self._pack.n
 
     def __getitem__(self, i: int) -> Fp8Tokens:
-        if not 0 <= i < self.n:
+        if not 0 <= i < self._pack.n:
             raise IndexError(i)
-        x = Fp8Tokens()
-        if self.rows is not None:
-            k = _up128(self.C)
-            x.rows, x.row_scale = self.rows[i], self.row_scale[i, :k * self.T].view(k, self.T)
-        if self.cols is not None:
-            x.cols, x.col_scale = self.cols[i], self.col_scale[i]
-        return x
-
-    def pointers(self, cols: bool):
-        """(q, scale) pointer arrays, one entry for each shard."""
-        q, s = (self.cols, self.col_scale) if cols else (self.rows, self.row_scale)
-        size = self.T * self.C
-        step = 4 * (_up128(self.T) * self.C if cols else self._pad)
-        a, b = q.data_ptr(), s.data_ptr()
-        return (_array([a + i * size for i in range(self.n)]),
-                _array([b + i * step for i in range(self.n)]))
+        return Fp8Tokens._of(self._pack, i)
 
 
 def _format(name: str) -> int:
@@ -90,17 +127,6 @@ def _check_like(x: torch.Tensor, shape: tuple, dtype, device, what: str) -> None
                          f"{device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
 
 
-def _empty_tokens(T: int, C: int, fmt: str, rows: bool, cols: bool, dev) -> Fp8Tokens:
-    x = Fp8Tokens()
-    if rows:
-        x.rows = torch.empty(T, C, dtype=DTYPES[fmt], device=dev)
-        x.row_scale = torch.empty(_up128(C), T, dtype=torch.float32, device=dev)
-    if cols:
-        x.cols = torch.empty(T, C, dtype=DTYPES[fmt], device=dev)
-        x.col_scale = torch.empty(_up128(T), C, dtype=torch.float32, device=dev)
-    return x
-
-
 def _array(ptrs):
     return (ctypes.c_void_p * len(ptrs))(*ptrs)
 
@@ -109,11 +135,15 @@ def _pointers(xs):
     return _array([x.data_ptr() for x in xs])
 
 
+_quant = functools.lru_cache(maxsize=256)(
+    lambda T, C, ld, n, code: binding.make_fp8_quant(T, C, ld, n, code, code))
+
+
 def _quantize(parts, code: int, scale_ld: int, rows, cols, stream) -> None:
     """One launch over `parts` [T, C]; rows, cols: (q, scale) pointer arrays or None."""
     T, C = parts[0].shape
     dev = parts[0].device
-    quant = binding.make_fp8_quant(T, C, scale_ld, len(parts), code, code)
+    quant = _quant(T, C, scale_ld, len(parts), code)
     q_rows, s_rows = rows or (None, None)
     q_cols, s_cols = cols or (None, None)
     with binding.on_device(dev):
@@ -150,21 +180,24 @@ def quantize_tokens(X, fmt: str = "e4m3", rows: bool = True, cols: bool = False,
         raise ValueError("choose rows, cols or both")
     T, dev = tc * n, first.device
     if out is None:
-        out = _empty_tokens(T, C, fmt, rows, cols, dev)
+        pack = _Packed(1, T, C, fmt, rows, cols, dev)
+        out = Fp8Tokens._of(pack, 0)
+        at = [None if a is None else pack.base + a for a in pack.at]
     else:
-        if rows:
-            _check_like(out.rows, (T, C), DTYPES[fmt], dev, "out.rows")
-            _check_like(out.row_scale, (_up128(C), T), torch.float32, dev, "out.row_scale")
-        if cols:
-            _check_like(out.cols, (T, C), DTYPES[fmt], dev, "out.cols")
-            _check_like(out.col_scale, (_up128(T), C), torch.float32, dev, "out.col_scale")
+        at = [None] * 4
+        for wanted, k, shape in ((rows, 0, (_up128(C), T)), (cols, 2, (_up128(T), C))):
+            if wanted:
+                q, scale = out._view(k), out._view(k + 1)
+                if q is None or scale is None:
+                    raise ValueError("out has no buffers for a grouping that is wanted")
+                _check_like(q, (T, C), DTYPES[fmt], dev, "out")
+                _check_like(scale, shape, torch.float32, dev, "out's scales")
+                at[k], at[k + 1] = q.data_ptr(), scale.data_ptr()
 
-    def part(x, step):
-        at = x.data_ptr()
-        return _array([at + j * step for j in range(n)])
-    _quantize(chunks, code, max(T, 1),
-              (part(out.rows, tc * C), part(out.row_scale, tc * 4)) if rows else None,
-              (part(out.cols, tc * C), part(out.col_scale, tc // 128 * C * 4)) if cols else None, stream)
+    def part(k: int, step: int):
+        return _array([at[k] + j * step for j in range(n)])
+    _quantize(chunks, code, max(T, 1), (part(0, tc * C), part(1, tc * 4)) if rows else None,
+              (part(2, tc * C), part(3, tc // 128 * C * 4)) if cols else None, stream)
     return out
 
 
@@ -177,10 +210,10 @@ def quantize_shards(shards, fmt: str = "e4m3", rows: bool = True, cols: bool = F
     if not (rows or cols):
         raise ValueError("choose rows, cols or both")
     T, C = shards[0].shape
-    out = Fp8Shards(len(shards), T, C, fmt, rows, cols, shards[0].device)
-    _quantize(shards, code, max(T, 1), out.pointers(False) if rows else None,
-              out.pointers(True) if cols else None, stream)
-    return out
+    pack = _Packed(len(shards), T, C, fmt, rows, cols, shards[0].device)
+    _quantize(shards, code, max(T, 1), pack.pointers(False) if rows else None,
+              pack.pointers(True) if cols else None, stream)
+    return Fp8Shards(pack)
 
 
 def quantize_weight(W: torch.Tensor, fmt: str = "e4m3", stream=None) -> tuple:
@@ -284,12 +317,13 @@ class DeviceFp8Linear:
 
     def _tokens(self, x, cols: bool):
         shape, n = self._x
-        if isinstance(x, Fp8Shards) and (x.n, x.T, x.C) == (n, *shape):
-            q = x.cols if cols else x.rows
-            if q is None or q.dtype != self._x_dtype or q.device != self.device:
-                raise ValueError(f"the input is not quantised by {'columns' if cols else 'rows'} in "
-                                 f"{self.x_format} on {self.device}")
-            return x.pointers(cols)
+        pack = x._pack if isinstance(x, (Fp8Shards, Fp8Tokens)) else None
+        if pack is not None and pack.n == n and (n == 1 or isinstance(x, Fp8Shards)):
+            if ((pack.T, pack.C) != shape or pack.fmt != self.x_format or pack.device != self.device
+                    or pack.at[2 * cols] is None):
+                raise ValueError(f"an input quantised by {'columns' if cols else 'rows'} in "
+                                 f"{self.x_format}, {shape} on {self.device}, is needed")
+            return pack.pointers(cols)
         x = [x] if isinstance(x, Fp8Tokens) else list(x)
         if len(x) != n:
             raise ValueError(f"{n} quantised inputs are needed, got {len(x)}")
