@@ -208,6 +208,9 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
     // the ring: one thread of the group has the copies of a row pair under way
     const int cols = min(NB_COLS / G, p.h - c0);
     const uint32_t bytes = cols > 0 ? static_cast<uint32_t>(cols) * 2 : 0;
+    // (a row's token chunk and gate are stepped, not divided out: the divisions were
+    // half of all instructions)
+    Stepper copy_chunk(row, 1, p.rows_per_chunk), copy_gate(row, 1, p.gate_rows);
     auto copy_rows = [&](long long r0, int stage) {
         const uint32_t bar = ptx::smem_u32(&sm.ring_bar[group][stage]);
         const int n = r0 + 1 < last ? 2 : 1;
@@ -215,9 +218,8 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
         ptx::mbar_arrive_expect_tx(bar, bytes * static_cast<uint32_t>(n * arrays));
         if (bytes == 0) return;
         for (int i = 0; i < n; ++i) {
-            const long long r = r0 + i;
-            const int k = static_cast<int>(r / p.rows_per_chunk);
-            const long long off = (r - k * p.rows_per_chunk) * p.h + c0;
+            const int k = copy_chunk.q;
+            const long long off = static_cast<long long>(copy_chunk.r) * p.h + c0;
             const uint32_t dst = ptx::smem_u32(ring) + (stage * R + i) * (NB_ARRAYS * ROW);
             auto get = [&](int a, const void* base, long long o) {
                 asm volatile(
@@ -232,7 +234,9 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
                 get(2, p.out.p[k], off);
             }
             if (Z) get(3, p.z.p[k], off);
-            if (gate) get(4, p.gate, r / p.gate_rows * p.h + c0);
+            if (gate) get(4, p.gate, static_cast<long long>(copy_gate.q) * p.h + c0);
+            copy_chunk.step();
+            copy_gate.step();
         }
     };
     if (tid == 0) {
@@ -254,6 +258,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
     float s_gate[Z ? 8 : 1] = {};
     int stage = 0;
     uint32_t ring_phase = 0;
+    Stepper chunk(row, 1, p.rows_per_chunk), seq(row, 1, p.gate_rows);
     for (; row < last; row += R) {
         wait_on(ptx::smem_u32(&sm.ring_bar[group][stage]), ring_phase, waits);
         uint4 q_dout[R], q_dxn[R], q_out[R], q_z[R], q_gate[R];
@@ -334,8 +339,9 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
         long long off[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            k[i] = static_cast<int>((row + i) / p.rows_per_chunk);
-            off[i] = (row + i - k[i] * p.rows_per_chunk) * p.h + c;
+            k[i] = chunk.q;
+            off[i] = static_cast<long long>(chunk.r) * p.h + c;
+            chunk.step();
             if (in && row + i < last) {
                 float o[8];
 #pragma unroll
@@ -375,10 +381,14 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
                     sums[i] = sv;
                     if (POST_LAYER) sums[R + i] = sw;
                 }
-                if (gate && !cut && row + i < last && (row + i + 1) % p.gate_rows == 0) {
+                const int seq_q = seq.q;
+                const bool seq_end = seq.r + 1 == seq.n;
+                seq.step();
+                if (gate && !cut && row + i < last && seq_end) {
                     // the gate's last row: its sum is complete
                     if (in) {
-                        float4* dst = reinterpret_cast<float4*>(p.dgate + (row + i) / p.gate_rows * p.h + c);
+                        float4* dst = reinterpret_cast<float4*>(
+                            p.dgate + static_cast<long long>(seq_q) * p.h + c);
                         dst[0] = make_float4(s_gate[0], s_gate[1], s_gate[2], s_gate[3]);
                         dst[1] = make_float4(s_gate[4], s_gate[5], s_gate[6], s_gate[7]);
                     }

@@ -28,6 +28,27 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0, 0, 0, 0); }
 
+// Quotient and remainder of start, start + stride, start + 2 stride, ... by n, all of
+// them below 2^31: divided once, then stepped.
+struct Stepper {
+    int q, r, dq, dr, n;
+    __device__ __forceinline__ Stepper(long long start, long long stride, long long by) {
+        n = static_cast<int>(by);
+        q = static_cast<int>(start) / n;
+        r = static_cast<int>(start) - q * n;
+        dq = static_cast<int>(stride) / n;
+        dr = static_cast<int>(stride) - dq * n;
+    }
+    __device__ __forceinline__ void step() {
+        q += dq;
+        r += dr;
+        if (r >= n) {
+            r -= n;
+            ++q;
+        }
+    }
+};
+
 // The sum of v over the warp, the same in every lane and every run.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
