@@ -6,11 +6,14 @@
 // that stays in registers: a CTA takes a row at a time, a thread one or two
 // 16-byte vectors of it, and a row costs one block sum for each rms and two for
 // each layer norm (mean, then the squares of what is left: no cancellation).
+// One thread keeps bulk copies of the CTA's next two rows (X, Z, gate) under way into
+// shared memory: loaded when they were needed, rows spent half their time waiting.
 // A CTA walks rows a grid apart; its columns' weights come from L1 at each row
 // (kept in registers they spill or halve the rows in flight), and the row's token
 // chunk and gate are stepped, not divided out: three 64-bit divisions a row and
 // thread were 40 % of the instructions.
 #include "fp8_cvt.cuh"
+#include "gemm_params.h"
 #include "norm_device.cuh"
 #include "norm_residual.cuh"
 #include "ptx.cuh"
@@ -19,6 +22,8 @@ namespace tpmlp {
 namespace {
 
 using namespace nr;
+
+constexpr int NF_STAGES = 2;  // rows in the ring
 
 // Sum of v over the CTA, in a fixed order; `buf` alternates from call to call,
 // so one barrier is enough.
@@ -62,8 +67,21 @@ __device__ __forceinline__ void row_stats(const float (&x)[V][8], const bool (&i
 
 template <int POST, int PRE, int V>
 __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant__ NrForwardParams p) {
+    extern __shared__ __align__(128) uint8_t ring[];  // [stage][X, Z, gate][row]
     __shared__ float smem[2][32];
+    __shared__ alignas(8) uint64_t bar[NF_STAGES];
     int buf = 0;
+    const uint32_t bytes = static_cast<uint32_t>(p.h) * 2;
+    const uint32_t slot = (bytes + 127u) & ~127u;
+    constexpr bool Z = POST != NR_ABSENT;
+    const bool gated = Z && p.gate != nullptr;
+    const uint32_t arrays = 1 + (Z ? 1 : 0) + (gated ? 1 : 0);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NF_STAGES; ++i) ptx::mbar_init(ptx::smem_u32(&bar[i]), 1);
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    __syncthreads();
     const float inv_h = 1.0f / static_cast<float>(p.h);
     int c[V];
     bool in[V];
@@ -73,8 +91,34 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
         c[j] = (j * blockDim.x + threadIdx.x) * 8;
         in[j] = c[j] < p.h;
     }
-    Stepper chunk(blockIdx.x, gridDim.x, p.rows_per_chunk), gate(blockIdx.x, gridDim.x, p.gate_rows);
-    for (long long row = blockIdx.x; row < p.T; row += gridDim.x, chunk.step(), gate.step()) {
+    Stepper chunk(blockIdx.x, gridDim.x, p.rows_per_chunk);
+    Stepper copy_chunk(blockIdx.x, gridDim.x, p.rows_per_chunk), copy_gate(blockIdx.x, gridDim.x, p.gate_rows);
+    // (thread 0, row after row of this CTA)
+    auto copy_row = [&](int stage) {
+        const uint32_t b = ptx::smem_u32(&bar[stage]);
+        const uint32_t dst = ptx::smem_u32(ring) + static_cast<uint32_t>(stage) * 3 * slot;
+        ptx::mbar_arrive_expect_tx(b, bytes * arrays);
+        auto get = [&](uint32_t a, const void* base, long long row) {
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                    dst + a * slot),
+                "l"(static_cast<const __nv_bfloat16*>(base) + row * p.h), "r"(bytes), "r"(b)
+                : "memory");
+        };
+        get(0, p.x.p[copy_chunk.q], copy_chunk.r);
+        if (Z) get(1, p.z.p[copy_chunk.q], copy_chunk.r);
+        if (gated) get(2, p.gate, copy_gate.q);
+        copy_chunk.step();
+        copy_gate.step();
+    };
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < NF_STAGES; ++i)
+            if (blockIdx.x + static_cast<long long>(i) * gridDim.x < p.T) copy_row(i);
+    }
+    int stage = 0;
+    uint32_t phase = 0;
+    for (long long row = blockIdx.x; row < p.T; row += gridDim.x, chunk.step()) {
         const int k = chunk.q;
         const long long off = static_cast<long long>(chunk.r) * p.h;
         auto at = [&](const void* base, int j) {
@@ -85,25 +129,39 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
                          : zero4(),
                    f);
         };
-        uint4 xv[V], zv[V], gv[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            xv[j] = in[j] ? __ldg(at(p.x.p[k], j)) : zero4();
-            if (POST != NR_ABSENT) zv[j] = in[j] ? __ldg(at(p.z.p[k], j)) : zero4();
-            if (POST != NR_ABSENT && p.gate)
-                gv[j] = in[j] ? __ldg(reinterpret_cast<const uint4*>(
-                                    static_cast<const __nv_bfloat16*>(p.gate) +
-                                    static_cast<long long>(gate.q) * p.h + c[j]))
-                              : zero4();
+        const uint8_t* src = ring + stage * 3 * slot;
+        auto here = [&](int a, int j, float (&f)[8]) {
+            unpack(in[j] ? *reinterpret_cast<const uint4*>(src + a * slot + c[j] * 2) : zero4(), f);
+        };
+        // the stage is read for the last time: the copy of the row NF_STAGES rows on
+        auto next = [&] {
+            if (threadIdx.x == 0 && row + static_cast<long long>(NF_STAGES) * gridDim.x < p.T)
+                copy_row(stage);
+            if (++stage == NF_STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        };
+        {
+            const uint32_t b = ptx::smem_u32(&bar[stage]);
+            if (!ptx::mbar_try_wait(b, phase)) {
+                const uint64_t t0 = ptx::globaltimer_ns();
+                while (!ptx::mbar_try_wait(b, phase)) {
+                    if (ptx::globaltimer_ns() - t0 > p.timeout_ns) {
+                        atomicOr(p.err, ERR_EPILOGUE);
+                        break;
+                    }
+                }
+            }
         }
         float v[V][8];
         if constexpr (POST == NR_ABSENT) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) unpack(xv[j], v[j]);
+            for (int j = 0; j < V; ++j) here(0, j, v[j]);
         } else {
             float mean = 0.0f, rstd = 1.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) unpack(zv[j], v[j]);
+            for (int j = 0; j < V; ++j) here(1, j, v[j]);
             if constexpr (POST >= NR_POST_RMS) {
                 row_stats<POST == NR_POST_LAYER, V>(v, in, inv_h, p.eps, mean, rstd, smem, buf);
                 if (threadIdx.x == 0 && p.stats) {
@@ -114,7 +172,7 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 float x[8], w[8], b[8];
-                unpack(xv[j], x);
+                here(0, j, x);
                 if (POST >= NR_POST_RMS) {
                     weight(p.post_gamma, j, w);
                     if (POST == NR_POST_LAYER) weight(p.post_beta, j, b);
@@ -123,8 +181,8 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
                         v[j][i] = POST == NR_POST_LAYER ? fmaf((v[j][i] - mean) * rstd, w[i], b[i])
                                                         : v[j][i] * rstd * w[i];
                 }
-                if (p.gate) {
-                    unpack(gv[j], w);
+                if (gated) {
+                    here(2, j, w);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[j][i] *= w[i];
                 }
@@ -138,6 +196,7 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
         if constexpr (PRE != NR_NONE) {
             float mean, rstd;
             row_stats<PRE == NR_PRE_LAYER, V>(v, in, inv_h, p.eps, mean, rstd, smem, buf);
+            next();
             if (threadIdx.x == 0 && p.stats) {
                 p.stats[2 * p.T + row] = mean;
                 p.stats[3 * p.T + row] = rstd;
@@ -165,6 +224,9 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
                     }
                 }
             }
+        } else {
+            __syncthreads();
+            next();
         }
     }
     ptx::griddep_launch_dependents();
@@ -177,18 +239,33 @@ cudaError_t launch(const NrForwardParams& p, int sm_count, cudaStream_t st) {
     const int V = vectors <= 256 ? 1 : 2;
     int threads = 128;
     while (threads * V < vectors) threads *= 2;
+    const int smem = NF_STAGES * 3 * ((p.h * 2 + 127) / 128 * 128);
+    // 64 registers a thread let 1024 threads onto an SM; their rings always fit
     const long long resident = static_cast<long long>(sm_count) * (1024 / threads);
+    auto kernel = V == 1 ? nr_forward_kernel<POST, PRE, 1> : nr_forward_kernel<POST, PRE, 2>;
+    constexpr int kDevices = 64;
+    static int ready[kDevices][2] = {};  // the kernel's attribute is set, per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    if (!__atomic_load_n(&ready[dev][V - 1], __ATOMIC_ACQUIRE)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 NF_STAGES * 3 * NR_MAX_H * 2);
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&ready[dev][V - 1], 1, __ATOMIC_RELEASE);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.T < resident ? p.T : resident), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return V == 1 ? cudaLaunchKernelEx(&cfg, nr_forward_kernel<POST, PRE, 1>, p)
-                  : cudaLaunchKernelEx(&cfg, nr_forward_kernel<POST, PRE, 2>, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int POST>

@@ -49,6 +49,8 @@ struct NrForwardParams {
     long long T, rows_per_chunk, gate_rows;
     int h, q_format;
     float eps, alpha;
+    unsigned int* err;           // the device error word and the limit of any one wait
+    unsigned long long timeout_ns;
 };
 
 struct NrBackwardParams {
