@@ -63,9 +63,12 @@ __device__ __forceinline__ uint2 cvt8(const uint4& v, const Scale& sc, int fmt) 
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        o[j] = sc.fine ? cvt2(lo_f(w[j]) * sc.inv, hi_f(w[j]) * sc.inv, fmt) : 0u;
-    return make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+    for (int j = 0; j < 4; ++j) {
+        const float2 f =
+            __fmul2_rn(make_float2(lo_f(w[j]), hi_f(w[j])), make_float2(sc.inv, sc.inv));
+        o[j] = cvt2(f.x, f.y, fmt);
+    }
+    return sc.fine ? make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16)) : make_uint2(0u, 0u);
 }
 
 }  // namespace q8

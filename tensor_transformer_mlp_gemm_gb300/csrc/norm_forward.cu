@@ -32,43 +32,48 @@ __device__ __forceinline__ float block_sum(float v, float (*smem)[32], int& buf)
     v = warp_sum(v);
     if (lane == 0) smem[buf][warp] = v;
     __syncthreads();
-    const float t = warp_sum(lane < warps ? smem[buf][lane] : 0.0f);
+    float t = 0.0f;
+    for (int w = 0; w < warps; w += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&smem[buf][w]);
+        t += (f.x + f.y) + (f.z + f.w);
+    }
     buf ^= 1;
     return t;
 }
 
 // rms and layer statistics of the CTA's row (columns outside it hold zeros)
 template <bool LAYER, int V>
-__device__ __forceinline__ void row_stats(const float (&x)[V][8], const bool (&in)[V], float inv_h,
+__device__ __forceinline__ void row_stats(const float2 (&x)[V][4], const bool (&in)[V], float inv_h,
                                           float eps, float& mean, float& rstd, float (*smem)[32],
                                           int& buf) {
     mean = 0.0f;
     if (LAYER) {
-        float s = 0.0f;
+        float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += x[j][i];
-        mean = block_sum(s, smem, buf) * inv_h;
+            for (int i = 0; i < 4; ++i) s = __fadd2_rn(s, x[j][i]);
+        mean = block_sum(s.x + s.y, smem, buf) * inv_h;
     }
-    float q = 0.0f;
+    float2 q = make_float2(0.0f, 0.0f);
+    const float2 m = make_float2(-mean, -mean);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        if (in[j]) {
+        if (!LAYER || in[j]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = x[j][i] - mean;
-                q = fmaf(d, d, q);
+            for (int i = 0; i < 4; ++i) {
+                const float2 d = LAYER ? __fadd2_rn(x[j][i], m) : x[j][i];
+                q = __ffma2_rn(d, d, q);
             }
         }
     }
-    rstd = rsqrtf(block_sum(q, smem, buf) * inv_h + eps);
+    rstd = rsqrtf(block_sum(q.x + q.y, smem, buf) * inv_h + eps);
 }
 
 template <int POST, int PRE, int V>
 __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant__ NrForwardParams p) {
     extern __shared__ __align__(128) uint8_t ring[];  // [stage][X, Z, gate][row]
-    __shared__ float smem[2][32];
+    __shared__ alignas(16) float smem[2][32];
     __shared__ alignas(8) uint64_t bar[NF_STAGES];
     int buf = 0;
     const uint32_t bytes = static_cast<uint32_t>(p.h) * 2;
@@ -124,13 +129,13 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
         auto at = [&](const void* base, int j) {
             return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + off + c[j]);
         };
-        auto weight = [&](const void* w, int j, float (&f)[8]) {
+        auto weight = [&](const void* w, int j, float2 (&f)[4]) {
             unpack(in[j] ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + c[j]))
                          : zero4(),
                    f);
         };
         const uint8_t* src = ring + stage * 3 * slot;
-        auto here = [&](int a, int j, float (&f)[8]) {
+        auto here = [&](int a, int j, float2 (&f)[4]) {
             unpack(in[j] ? *reinterpret_cast<const uint4*>(src + a * slot + c[j] * 2) : zero4(), f);
         };
         // the stage is read for the last time: the copy of the row NF_STAGES rows on
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
                 }
             }
         }
-        float v[V][8];
+        float2 v[V][4];
         if constexpr (POST == NR_ABSENT) {
 #pragma unroll
             for (int j = 0; j < V; ++j) here(0, j, v[j]);
@@ -169,25 +174,28 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
                     p.stats[p.T + row] = rstd;
                 }
             }
+            const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
+            const float2 a2 = make_float2(p.alpha, p.alpha);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                float x[8], w[8], b[8];
+                float2 x[4], w[4], b[4];
                 here(0, j, x);
                 if (POST >= NR_POST_RMS) {
                     weight(p.post_gamma, j, w);
                     if (POST == NR_POST_LAYER) weight(p.post_beta, j, b);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[j][i] = POST == NR_POST_LAYER ? fmaf((v[j][i] - mean) * rstd, w[i], b[i])
-                                                        : v[j][i] * rstd * w[i];
+                    for (int i = 0; i < 4; ++i)
+                        v[j][i] = POST == NR_POST_LAYER
+                                      ? __ffma2_rn(__fmul2_rn(__fadd2_rn(v[j][i], m2), r2), w[i], b[i])
+                                      : __fmul2_rn(__fmul2_rn(v[j][i], r2), w[i]);
                 }
                 if (gated) {
                     here(2, j, w);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] *= w[i];
+                    for (int i = 0; i < 4; ++i) v[j][i] = __fmul2_rn(v[j][i], w[i]);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] = fmaf(p.alpha, x[i], v[j][i]);
+                for (int i = 0; i < 4; ++i) v[j][i] = __ffma2_rn(a2, x[i], v[j][i]);
                 const uint4 o = pack(v[j]);
                 if (in[j]) *const_cast<uint4*>(at(p.out[k], j)) = o;
                 unpack(o, v[j]);  // N_pre reads what was stored
@@ -201,25 +209,37 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
                 p.stats[2 * p.T + row] = mean;
                 p.stats[3 * p.T + row] = rstd;
             }
+            const float2 m2 = make_float2(-mean, -mean), r2 = make_float2(rstd, rstd);
+            uint4 o[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                float w[8], b[8];
+                float2 w[4], b[4];
                 weight(p.pre_gamma, j, w);
                 if (PRE == NR_PRE_LAYER) weight(p.pre_beta, j, b);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[j][i] = PRE == NR_PRE_LAYER ? fmaf((v[j][i] - mean) * rstd, w[i], b[i])
-                                                  : v[j][i] * rstd * w[i];
-                const uint4 o = in[j] ? pack(v[j]) : zero4();
-                if (in[j] && p.xn[0]) *const_cast<uint4*>(at(p.xn[k], j)) = o;
-                if (p.q) {
-                    // 16 threads hold a group of 128
-                    uint32_t m = q8::largest(o);
+                for (int i = 0; i < 4; ++i)
+                    v[j][i] = PRE == NR_PRE_LAYER
+                                  ? __ffma2_rn(__fmul2_rn(__fadd2_rn(v[j][i], m2), r2), w[i], b[i])
+                                  : __fmul2_rn(__fmul2_rn(v[j][i], r2), w[i]);
+                o[j] = in[j] ? pack(v[j]) : zero4();
+                if (in[j] && p.xn[0]) *const_cast<uint4*>(at(p.xn[k], j)) = o[j];
+            }
+            if (p.q) {
+                // 16 threads hold a group of 128; two groups' maxima share a word
+                uint32_t m[(V + 1) / 2];
 #pragma unroll
-                    for (int s = 8; s >= 1; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-                    const q8::Scale sc = q8::scale_of(m, p.q_format);
+                for (int j = 0; j < V; j += 2)
+                    m[j / 2] = q8::largest(o[j]) | (j + 1 < V ? q8::largest(o[j + 1 < V ? j + 1 : j]) << 16 : 0u);
+#pragma unroll
+                for (int s = 8; s >= 1; s >>= 1)
+#pragma unroll
+                    for (int j = 0; j < (V + 1) / 2; ++j)
+                        m[j] = __vmaxu2(m[j], __shfl_xor_sync(0xffffffffu, m[j], s));
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const q8::Scale sc = q8::scale_of(j & 1 ? m[j / 2] >> 16 : m[j / 2] & 0xFFFFu, p.q_format);
                     if (in[j]) {
-                        *reinterpret_cast<uint2*>(p.q + row * p.h + c[j]) = q8::cvt8(o, sc, p.q_format);
+                        *reinterpret_cast<uint2*>(p.q + row * p.h + c[j]) = q8::cvt8(o[j], sc, p.q_format);
                         if ((threadIdx.x & 15) == 0) p.q_scale[(c[j] >> 7) * p.T + row] = sc.s;
                     }
                 }
@@ -235,10 +255,10 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
 template <int POST, int PRE>
 cudaError_t launch(const NrForwardParams& p, int sm_count, cudaStream_t st) {
     const long long vectors = p.h / 8;
-    // two vectors a thread from 2048 columns on (256 threads), at most 1024 threads
-    const int V = vectors <= 256 ? 1 : 2;
-    int threads = 128;
-    while (threads * V < vectors) threads *= 2;
+    // Two vectors a thread as soon as they fill four warps (a 2048-wide row of 16384 in
+    // 49 us; with one vector a thread 59), whole warps in fours, at most 1024 threads.
+    const int V = vectors <= 128 ? 1 : 2;
+    const int threads = static_cast<int>((vectors + 128 * V - 1) / (128 * V)) * 128;
     const int smem = NF_STAGES * 3 * ((p.h * 2 + 127) / 128 * 128);
     // 64 registers a thread let 1024 threads onto an SM; their rings always fit
     const long long resident = static_cast<long long>(sm_count) * (1024 / threads);
