@@ -11,7 +11,9 @@
 // are worth 2100 of HBM time.  So a group of threads takes two rows at a time, narrow
 // rows are spread over up to 8 groups of a CTA's 512 threads, and one thread of a group
 // keeps bulk copies of its next rows under way into a ring in shared memory.
-// Rows of more than 4096 columns take a cluster of 2 or 4 CTAs side by side, whose row
+// Rows of more than 4096 columns take a cluster of 2 to 4 CTAs side by side, and as many
+// clusters as run at once (46 of 3 and 36 of 4 on 152 SMs: two more made a second round
+// and doubled the time), whose row
 // sums meet in each other's shared memory: each warp sends its part to every CTA,
 // counted on that CTA's mbarrier, and every warp adds all parts in the same order.  (A
 // cluster barrier instead waits for the row's own loads and stores too: 6600 clocks a
@@ -42,7 +44,7 @@ constexpr int NB_RING = NB_STAGES * NB_ROWS * NB_ARRAYS * NB_COLS * 2;
 static_assert(NB_COLS * NB_MAX_CLUSTER >= NR_MAX_H, "a cluster holds the widest row");
 
 // CTAs side by side for a row, and groups of a CTA's threads that take rows of their own.
-int cluster_of(long long h) { return h <= NB_COLS ? 1 : h <= 2 * NB_COLS ? 2 : 4; }
+int cluster_of(long long h) { return static_cast<int>((h + NB_COLS - 1) / NB_COLS); }
 int groups_of(long long h) {
     int g = 1;
     while (g < NB_MAX_GROUPS && h <= NB_COLS / (2 * g)) g *= 2;
@@ -253,9 +255,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
     };
     float stat = load_stats(row);
 
-    float s_pre[BEFORE ? 8 : 1] = {}, s_pre_b[PRE_LAYER ? 8 : 1] = {};
-    float s_post[POST_NORM ? 8 : 1] = {}, s_post_b[POST_LAYER ? 8 : 1] = {};
-    float s_gate[Z ? 8 : 1] = {};
+    float2 s_pre[4] = {}, s_pre_b[4] = {}, s_post[4] = {}, s_post_b[4] = {}, s_gate[4] = {};
     int stage = 0;
     uint32_t ring_phase = 0;
     Stepper chunk(row, 1, p.rows_per_chunk), seq(row, 1, p.gate_rows);
@@ -280,45 +280,51 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
             r1[i] = POST_NORM ? __shfl_sync(0xffffffffu, stat, 4 * i + 1) : 0.0f;
             m2[i] = PRE_LAYER ? __shfl_sync(0xffffffffu, stat, 4 * i + 2) : 0.0f;
             r2[i] = BEFORE ? __shfl_sync(0xffffffffu, stat, 4 * i + 3) : 0.0f;
+            // (nor of columns outside the row, which hold zeros)
+            if (POST_LAYER && !in) m1[i] = 0.0f;
+            if (PRE_LAYER && !in) m2[i] = 0.0f;
         }
         stat = load_stats(row + R);
 
-        float g[R][8];
+        float2 g[R][4];
         if constexpr (BEFORE) {
             constexpr int N = PRE_LAYER ? 2 * R : R;
             float sums[N];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                float d[8], v[8], w[8];
+                float2 d[4], v[4], w[4];
                 unpack(q_dxn[i], d);
                 unpack(q_out[i], v);
                 unpack(w2, w);
-                float sv = 0.0f, sw = 0.0f;
+                const float2 m = both(-m2[i]), r = both(r2[i]);
+                float2 sv = both(0.0f), sw = both(0.0f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float hat = in ? (v[e] - m2[i]) * r2[i] : 0.0f;
-                    s_pre[e] = fmaf(d[e], hat, s_pre[e]);
-                    if (PRE_LAYER) s_pre_b[e] += d[e];
-                    const float wd = w[e] * d[e];
-                    sv = fmaf(wd, hat, sv);
-                    if (PRE_LAYER) sw += wd;
+                for (int e = 0; e < 4; ++e) {
+                    const float2 hat = __fmul2_rn(PRE_LAYER ? __fadd2_rn(v[e], m) : v[e], r);
+                    s_pre[e] = __ffma2_rn(d[e], hat, s_pre[e]);
+                    if (PRE_LAYER) s_pre_b[e] = __fadd2_rn(s_pre_b[e], d[e]);
+                    const float2 wd = __fmul2_rn(w[e], d[e]);
+                    sv = __ffma2_rn(wd, hat, sv);
+                    if (PRE_LAYER) sw = __fadd2_rn(sw, wd);
                 }
-                sums[i] = sv;
-                if (PRE_LAYER) sums[R + i] = sw;
+                sums[i] = sv.x + sv.y;
+                if (PRE_LAYER) sums[R + i] = sw.x + sw.y;
             }
             row_sums<CL, G, N>(sums, sm, buf, phase, group, rank, waits);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                float d[8], v[8], w[8];
+                float2 d[4], v[4], w[4];
                 unpack(q_dxn[i], d);
                 unpack(q_out[i], v);
                 unpack(w2, w);
                 unpack(q_dout[i], g[i]);
-                const float mv = sums[i] * inv_h, mw = PRE_LAYER ? sums[R + i] * inv_h : 0.0f;
+                const float2 m = both(-m2[i]), r = both(r2[i]), mv = both(-sums[i] * inv_h),
+                             mw = both(PRE_LAYER ? -sums[R + i] * inv_h : 0.0f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float hat = (v[e] - m2[i]) * r2[i];
-                    g[i][e] = fmaf(r2[i], w[e] * d[e] - mw - hat * mv, g[i][e]);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 hat = __fmul2_rn(PRE_LAYER ? __fadd2_rn(v[e], m) : v[e], r);
+                    const float2 wd = PRE_LAYER ? __ffma2_rn(w[e], d[e], mw) : __fmul2_rn(w[e], d[e]);
+                    g[i][e] = __ffma2_rn(r, __ffma2_rn(hat, mv, wd), g[i][e]);
                 }
             }
         } else {
@@ -343,43 +349,47 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
             off[i] = static_cast<long long>(chunk.r) * p.h + c;
             chunk.step();
             if (in && row + i < last) {
-                float o[8];
+                float2 o[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = Z ? p.alpha * g[i][e] : g[i][e];
+                for (int e = 0; e < 4; ++e) o[e] = Z ? __fmul2_rn(both(p.alpha), g[i][e]) : g[i][e];
                 *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dx[k[i]]) + off[i]) = pack(o);
             }
         }
         if constexpr (Z) {
             constexpr int N = POST_LAYER ? 2 * R : R;
             float sums[N];
-            float w[8], b[8];
+            float2 w[4], b[4];
             unpack(w1, w);
             unpack(b1, b);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                float z[8], t[8];
+                float2 z[4], t[4];
                 unpack(q_z[i], z);
                 unpack(q_gate[i], t);
-                float sv = 0.0f, sw = 0.0f;
+                const float2 m = both(-m1[i]), r = both(r1[i]);
+                float2 sv = both(0.0f), sw = both(0.0f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float hat = POST_NORM ? (in ? (z[e] - m1[i]) * r1[i] : 0.0f) : z[e];
+                for (int e = 0; e < 4; ++e) {
+                    const float2 hat =
+                        POST_NORM ? __fmul2_rn(POST_LAYER ? __fadd2_rn(z[e], m) : z[e], r) : z[e];
                     if (gate) {
-                        const float u = POST_LAYER ? fmaf(hat, w[e], b[e]) : POST_NORM ? hat * w[e] : hat;
-                        s_gate[e] = fmaf(g[i][e], u, s_gate[e]);
-                        g[i][e] *= t[e];
+                        const float2 u = POST_LAYER  ? __ffma2_rn(hat, w[e], b[e])
+                                         : POST_NORM ? __fmul2_rn(hat, w[e])
+                                                     : hat;
+                        s_gate[e] = __ffma2_rn(g[i][e], u, s_gate[e]);
+                        g[i][e] = __fmul2_rn(g[i][e], t[e]);
                     }
                     if (POST_NORM) {
-                        s_post[e] = fmaf(g[i][e], hat, s_post[e]);
-                        if (POST_LAYER) s_post_b[e] += g[i][e];
-                        const float wd = w[e] * g[i][e];
-                        sv = fmaf(wd, hat, sv);
-                        if (POST_LAYER) sw += wd;
+                        s_post[e] = __ffma2_rn(g[i][e], hat, s_post[e]);
+                        if (POST_LAYER) s_post_b[e] = __fadd2_rn(s_post_b[e], g[i][e]);
+                        const float2 wd = __fmul2_rn(w[e], g[i][e]);
+                        sv = __ffma2_rn(wd, hat, sv);
+                        if (POST_LAYER) sw = __fadd2_rn(sw, wd);
                     }
                 }
                 if (POST_NORM) {
-                    sums[i] = sv;
-                    if (POST_LAYER) sums[R + i] = sw;
+                    sums[i] = sv.x + sv.y;
+                    if (POST_LAYER) sums[R + i] = sw.x + sw.y;
                 }
                 const int seq_q = seq.q;
                 const bool seq_end = seq.r + 1 == seq.n;
@@ -389,24 +399,27 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
                     if (in) {
                         float4* dst = reinterpret_cast<float4*>(
                             p.dgate + static_cast<long long>(seq_q) * p.h + c);
-                        dst[0] = make_float4(s_gate[0], s_gate[1], s_gate[2], s_gate[3]);
-                        dst[1] = make_float4(s_gate[4], s_gate[5], s_gate[6], s_gate[7]);
+                        dst[0] = make_float4(s_gate[0].x, s_gate[0].y, s_gate[1].x, s_gate[1].y);
+                        dst[1] = make_float4(s_gate[2].x, s_gate[2].y, s_gate[3].x, s_gate[3].y);
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) s_gate[e] = 0.0f;
+                    for (int e = 0; e < 4; ++e) s_gate[e] = both(0.0f);
                 }
             }
             if constexpr (POST_NORM) {
                 row_sums<CL, G, N>(sums, sm, buf, phase, group, rank, waits);
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    float z[8];
+                    float2 z[4];
                     unpack(q_z[i], z);
-                    const float mv = sums[i] * inv_h, mw = POST_LAYER ? sums[R + i] * inv_h : 0.0f;
+                    const float2 m = both(-m1[i]), r = both(r1[i]), mv = both(-sums[i] * inv_h),
+                                 mw = both(POST_LAYER ? -sums[R + i] * inv_h : 0.0f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float hat = (z[e] - m1[i]) * r1[i];
-                        g[i][e] = r1[i] * (w[e] * g[i][e] - mw - hat * mv);
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 hat = __fmul2_rn(POST_LAYER ? __fadd2_rn(z[e], m) : z[e], r);
+                        const float2 wd =
+                            POST_LAYER ? __ffma2_rn(w[e], g[i][e], mw) : __fmul2_rn(w[e], g[i][e]);
+                        g[i][e] = __fmul2_rn(r, __ffma2_rn(hat, mv, wd));
                     }
                 }
             }
@@ -423,10 +436,10 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
     const int nv = (BEFORE ? 1 : 0) + (PRE_LAYER ? 1 : 0) + (POST_NORM ? 1 : 0) + (POST_LAYER ? 1 : 0);
     float* part = p.part + block * (nv + (gate && cut ? 1 : 0)) * p.h;
     float* meet = reinterpret_cast<float*>(ring_all);  // [group][columns]: the ring is done with
-    auto put = [&](const float* s) {
+    auto put = [&](const float2 (&s)[4]) {
         float t[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = s[e];
+        for (int e = 0; e < 8; ++e) t[e] = e & 1 ? s[e / 2].y : s[e / 2].x;
         if constexpr (G > 1) {
             __syncthreads();
 #pragma unroll
@@ -511,11 +524,12 @@ __global__ void __launch_bounds__(256) nr_finish_kernel(const __grid_constant__ 
     }
 }
 
+constexpr int kDevices = 64;
+
+// The kernel's attribute, set once a device.
 template <int POST, int PRE, int CL, int G>
-cudaError_t launch_rows(const NrBackwardParams& p, cudaStream_t st) {
-    constexpr int kDevices = 64;
-    static int ready[kDevices] = {};  // the kernel's attribute is set, per device
-    int dev = 0;
+cudaError_t prepare(int& dev) {
+    static int ready[kDevices] = {};
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
@@ -525,27 +539,64 @@ cudaError_t launch_rows(const NrBackwardParams& p, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.blocks * CL), 1, 1);
+    return cudaSuccess;
+}
+
+// attr: two of them, the cluster's first
+void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, long long blocks, int cl) {
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks * cl), 1, 1);
     cfg.blockDim = dim3(NB_THREADS, 1, 1);
     cfg.dynamicSmemBytes = NB_RING;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CL;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cl);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CL > 1 ? 2 : 1;
+    cfg.numAttrs = 2;
+}
+
+template <int POST, int PRE, int CL, int G>
+cudaError_t launch_rows(const NrBackwardParams& p, cudaStream_t st) {
+    int dev = 0;
+    const cudaError_t e = prepare<POST, PRE, CL, G>(dev);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    configure(cfg, attr, p.blocks, CL);
+    cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, nr_backward_kernel<POST, PRE, CL, G>, p);
+}
+
+// Clusters of CL CTAs that run at once (asked once a device; every variant of the kernel
+// takes the same threads and shared memory).
+template <int CL>
+cudaError_t resident(long long& clusters) {
+    static int known[kDevices] = {};
+    int dev = 0;
+    cudaError_t e = prepare<NR_ABSENT, NR_PRE_RMS, CL, 1>(dev);
+    if (e != cudaSuccess) return e;
+    int n = __atomic_load_n(&known[dev], __ATOMIC_ACQUIRE);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        configure(cfg, attr, 1, CL);
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, nr_backward_kernel<NR_ABSENT, NR_PRE_RMS, CL, 1>, &cfg);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        __atomic_store_n(&known[dev], n, __ATOMIC_RELEASE);
+    }
+    clusters = n;
+    return cudaSuccess;
 }
 
 template <int POST, int PRE>
 cudaError_t launch(const NrBackwardParams& p, cudaStream_t st) {
     const int cl = cluster_of(p.h);
     if (cl == 2) return launch_rows<POST, PRE, 2, 1>(p, st);
+    if (cl == 3) return launch_rows<POST, PRE, 3, 1>(p, st);
     if (cl == 4) return launch_rows<POST, PRE, 4, 1>(p, st);
     switch (groups_of(p.h)) {
         case 1: return launch_rows<POST, PRE, 1, 1>(p, st);
@@ -565,8 +616,15 @@ cudaError_t launch_pre(const NrBackwardParams& p, int pre, cudaStream_t st) {
 
 }  // namespace
 
-void nr_plan(NrBackwardParams& p, int sm_count) {
-    const long long blocks = std::max(1, std::min(sm_count, NR_MAX_UNITS) / cluster_of(p.h));
+cudaError_t nr_plan(NrBackwardParams& p, int sm_count) {
+    const int cl = cluster_of(p.h);
+    long long blocks = sm_count;
+    cudaError_t e = cudaSuccess;
+    if (cl == 2) e = resident<2>(blocks);
+    if (cl == 3) e = resident<3>(blocks);
+    if (cl == 4) e = resident<4>(blocks);
+    if (e != cudaSuccess) return e;
+    blocks = std::max(1LL, std::min(blocks, static_cast<long long>(NR_MAX_UNITS / cl)));
     const long long groups = groups_of(p.h);
     p.seqs = p.T / p.gate_rows;
     p.blocks_per_seq = 0;
@@ -584,6 +642,7 @@ void nr_plan(NrBackwardParams& p, int sm_count) {
         p.blocks_per_seq = static_cast<int>(per);
         p.blocks = p.seqs * per;
     }
+    return cudaSuccess;
 }
 
 size_t nr_partial_bytes(long long h) {

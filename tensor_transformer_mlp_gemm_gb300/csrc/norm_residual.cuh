@@ -80,7 +80,7 @@ cudaError_t launch_nr_backward(const NrBackwardParams& p, int post, int pre, cud
 // and part of another's: with few gates each gate's rows are cut into
 // blocks_per_seq blocks, with many each group of a block's threads takes
 // seqs_per_group whole gates (blocks_per_seq = 0).
-void nr_plan(NrBackwardParams& p, int sm_count);
+cudaError_t nr_plan(NrBackwardParams& p, int sm_count);
 // The most bytes of partial sums a backward pass of this width needs.
 size_t nr_partial_bytes(long long h);
 
