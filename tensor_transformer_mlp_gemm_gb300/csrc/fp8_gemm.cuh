@@ -54,9 +54,11 @@ struct Fp8GemmParams {
 cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, int out, cudaStream_t st);
 
 // The same (bf16 output, B scaled per block) for few rows of A: tiles of 128 columns
-// by fp8_small_rows() rows of A, K cut over up to 8 CTAs of a cluster.
-cudaError_t launch_fp8_small(const Fp8GemmParams& p, int sm_count, cudaStream_t st);
-// Rows of A of a tile, which is also the box of A's maps.
-inline int fp8_small_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+// by `rows` rows of A, which is also the box of A's maps, with K cut over up to 8 CTAs
+// of a cluster.
+cudaError_t launch_fp8_small(const Fp8GemmParams& p, int rows, cudaStream_t st);
+// Those rows for a product of this shape on the current device; 0: it has rows and
+// columns enough for the pairs.
+cudaError_t fp8_small_rows(int M, int N, int groups, int& rows);
 
 }  // namespace tpmlp

@@ -128,15 +128,13 @@ bool encode_operand(CUtensorMap* m, const Operand& o, int i, int K, int rows, in
     return o.mn ? encode_bytes(m, o.q[i], rows, K, 128) : encode_bytes(m, o.q[i], K, rows, box);
 }
 
-// Rows of A up to which the few-rows kernel is taken.
-constexpr int kFewRows = 128;
-
 tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int kind, cudaStream_t st) {
     Fp8GemmParams p;
     std::memset(&p, 0, sizeof(p));
-    const bool few = d.out_kind == F8_BF16_BLOCK && d.M <= kFewRows;
+    int few = 0;  // rows of a tile of the few-rows kernel
+    if (d.out_kind == F8_BF16_BLOCK) TPMLP_CUDA(fp8_small_rows(d.M, d.N, d.groups, few));
     for (int i = 0; i < d.a.n; ++i) {
-        if (!encode_operand(&p.a_map[i], d.a, i, d.K, d.M, few ? fp8_small_rows(d.M) : 128))
+        if (!encode_operand(&p.a_map[i], d.a, i, d.K, d.M, few ? few : 128))
             return TPMLP_ERR_UNSUPPORTED;
         p.sa[i] = static_cast<const float*>(d.a.s[i]);
     }
@@ -172,7 +170,7 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int kind, cuda
     p.err = dev->err;
     p.timeout_ns = g_timeout_ns;
     TPMLP_CUDA(timed(kind, 1, st, [&] {
-        return few ? launch_fp8_small(p, dev->sm_count, st) : launch_fp8_gemm(p, d.out_kind, st);
+        return few ? launch_fp8_small(p, few, st) : launch_fp8_gemm(p, d.out_kind, st);
     }));
     return TPMLP_OK;
 }

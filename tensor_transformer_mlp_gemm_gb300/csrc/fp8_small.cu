@@ -3,11 +3,13 @@
 //
 // What bounds it: the weights' bytes.  256 x 256 tiles leave most SMs without work
 // then (a 12288-wide layer has 48), so here the tensor cores' 128 rows are 128
-// features of the weight and their columns are the tokens (16 to 128 of them), and
-// the K axis is cut over the CTAs of a cluster: enough CTAs for two on every SM,
-// each with about 100 KB of weights on the way.  The parts meet in distributed
+// features of the weight and their columns are the tokens (16 to 256 of them), and
+// the K axis is cut over the CTAs of a cluster: two CTAs for an SM up to 64 tokens,
+// with about 100 KB of weights on the way each.  The parts meet in distributed
 // shared memory: each CTA leaves its sums in its own, and adds a share of the
 // tokens over all of them, in the order of the CTAs.
+// Measured with cold caches, launch included: one token, 12288 -> 12288 features in 39 us
+// (151 MB; 22 us at the copy rate), 4096 -> 12288 in 18 us; 48 tokens 43 and 20 us.
 //
 // CTA layout (256 threads):
 //   warp 0       TMA producer: 128 features and the tile's tokens for each K block
@@ -31,18 +33,21 @@ constexpr int S_WARPS = 4;       // scale and output warps
 constexpr int S_MAX_SPLIT = 8;   // the portable cluster size
 constexpr int S_AHEAD = 4;       // K blocks whose scales are under way
 
-// Up to 64 tokens two CTAs fit an SM; with 128 one, whose ring is as deep as both.
+// Up to 64 tokens two CTAs fit an SM; from 128 on one, whose ring is as deep as both.
 template <int TN>
 struct Small {
-    static constexpr int kStages = TN == 16 ? 6 : TN == 32 ? 5 : TN == 64 ? 4 : 6;
+    static constexpr int kStages = TN == 16 ? 6 : TN == 32 ? 5 : TN == 64 ? 4 : TN == 128 ? 6 : 4;
     static constexpr int kStageBytes = F8_BOX_BYTES + TN * 128;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
     static constexpr int kSums = TN < 32 ? 32 : TN;      // columns of sums
     static constexpr int kScaleB = 4;                    // a slot: 4 columns for A, then B's
     static constexpr int kColsB = TN < 32 ? 1 : TN / 32;
-    static constexpr int kTmemCols = kSums + kStages * 8 <= 128 ? 128 : 256;
+    static constexpr int kSlot = kColsB <= 4 ? 8 : 16;   // columns of a slot
+    static constexpr int kTmemCols = kSums + kStages * kSlot <= 128   ? 128
+                                     : kSums + kStages * kSlot <= 256 ? 256
+                                                                      : 512;
     static constexpr int kPerSm = TN <= 64 ? 2 : 1;
-    static_assert(kSums + kStages * 8 <= 256, "tensor memory");
+    static_assert(kSums + kStages * kSlot <= 512 / kPerSm, "tensor memory");
     static_assert(TN * 128 * 4 <= kStages * kStageBytes, "the sums fit where the operands were");
     static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 };
@@ -164,7 +169,7 @@ __global__ void __launch_bounds__(S_THREADS, Small<TN>::kPerSm)
             if (!ok) break;
             ptx::tc_fence_after();
             const uint32_t step = stage * (C::kStageBytes >> 4);
-            const uint32_t sf = tmem + C::kSums + stage * 8;
+            const uint32_t sf = tmem + C::kSums + stage * C::kSlot;
             if (elect_one()) {
 #pragma unroll
                 for (uint32_t i = 0; i < 4; ++i)
@@ -219,10 +224,16 @@ __global__ void __launch_bounds__(S_THREADS, Small<TN>::kPerSm)
                                                       p.timeout_ns, p.err, ERR_PRODUCER));
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    const uint32_t t = lanes + C::kSums + stage * 8;
+                    const uint32_t t = lanes + C::kSums + stage * C::kSlot;
                     store_cols4(t, w);
+                    if constexpr (C::kColsB == 8) {
+                        store_cols8(t + C::kScaleB, x);
+                    } else if constexpr (C::kColsB == 4) {
+                        store_cols4(t + C::kScaleB, x);
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < C::kColsB; ++c) store_col(t + C::kScaleB + c, x[c]);
+                        for (int c = 0; c < C::kColsB; ++c) store_col(t + C::kScaleB + c, x[c]);
+                    }
                     store_wait();
                     ptx::tc_fence_before();
                     __syncwarp();
@@ -299,55 +310,100 @@ __global__ void __launch_bounds__(S_THREADS, Small<TN>::kPerSm)
     }
 }
 
+// attr: two of them, the cluster's first
 template <int TN>
-cudaError_t launch(const Fp8GemmParams& p, int sm_count, cudaStream_t st) {
-    using C = Small<TN>;
+void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int splits) {
+    cfg.gridDim = dim3(static_cast<unsigned>(splits), 1, 1);
+    cfg.blockDim = dim3(S_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Small<TN>::kSmem;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+}
+
+// Clusters of each size that a device runs at once with one CTA on an SM (a cluster lies
+// in one group of SMs: 15 of 8 CTAs and 36 of 4 on 152 SMs).
+template <int TN>
+cudaError_t resident(const int*& clusters) {
     constexpr int kDevices = 64;
-    static int ready[kDevices] = {};  // the kernel's attribute is set, per device
+    static int known[kDevices][S_MAX_SPLIT + 1] = {};
+    static int ready[kDevices] = {};  // asked once a device, with the kernel's attribute
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
     if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
         e = cudaFuncSetAttribute(fp8_small_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 C::kSmem);
+                                 Small<TN>::kSmem);
         if (e != cudaSuccess) return e;
+        for (int c = 1; c <= S_MAX_SPLIT; ++c) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[2];
+            configure<TN>(cfg, attr, c);
+            cfg.numAttrs = 1;
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, fp8_small_kernel<TN>, &cfg);
+            if (e != cudaSuccess) return e;
+            __atomic_store_n(&known[dev][c], n, __ATOMIC_RELAXED);
+        }
         __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
     }
+    clusters = known[dev];
+    return cudaSuccess;
+}
+
+template <int TN>
+cudaError_t launch(const Fp8GemmParams& p, cudaStream_t st) {
+    const int* clusters = nullptr;
+    const cudaError_t e = resident<TN>(clusters);
+    if (e != cudaSuccess) return e;
     const long long tiles = static_cast<long long>((p.N + 127) / 128) * p.groups;
     const long long rows = (p.M + TN - 1) / TN;
     const long long nk = static_cast<long long>((p.K + F8_BK - 1) / F8_BK) * p.ksegs;
-    // the widest split whose CTAs all run at once and still have a K block each
-    int splits = 1;
-    while (splits < S_MAX_SPLIT && tiles * rows * splits * 2 <= static_cast<long long>(C::kPerSm) * sm_count &&
-           splits * 2 <= nk)
-        splits *= 2;
+    // The widest split whose CTAs all run at once and still have a K block each.  128
+    // tokens, 12288 -> 4608 features (36 tiles): 4 parts 22 us, 3 or 5 parts 25 or 33;
+    // 48 tokens, 12288 -> 12288 (96 tiles): 2 parts 43 us, 1 or 4 parts 53 or 47.
+    int splits = static_cast<int>(nk < S_MAX_SPLIT ? nk : S_MAX_SPLIT);
+    while (splits > 1 && tiles * rows > static_cast<long long>(Small<TN>::kPerSm) * clusters[splits])
+        --splits;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), static_cast<unsigned>(rows), 1);
-    cfg.blockDim = dim3(S_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = st;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    configure<TN>(cfg, attr, splits);
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), static_cast<unsigned>(rows), 1);
+    cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, fp8_small_kernel<TN>, p, splits);
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_small(const Fp8GemmParams& p, int sm_count, cudaStream_t st) {
-    switch (fp8_small_rows(p.M)) {
-        case 16: return launch<16>(p, sm_count, st);
-        case 32: return launch<32>(p, sm_count, st);
-        case 64: return launch<64>(p, sm_count, st);
-        default: return launch<128>(p, sm_count, st);
+cudaError_t fp8_small_rows(int M, int N, int groups, int& rows) {
+    rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    if (M <= 128) return cudaSuccess;
+    const int* clusters = nullptr;
+    const cudaError_t e = resident<256>(clusters);
+    if (e != cudaSuccess) return e;
+    // Pairs on 256 x 256 tiles are faster unless so few tiles that K can be cut in four
+    // here.  256 tokens: 12288 -> 4096 features (32 tiles) 29 us here and 37 on pairs,
+    // 4096 -> 4096 18 and 20; 2064 -> 8240 (65 tiles, cut in two) 22 and 16.
+    const long long tiles = static_cast<long long>((N + 127) / 128) * groups;
+    rows = tiles * ((M + 255LL) / 256) <= clusters[4] ? 256 : 0;
+    return cudaSuccess;
+}
+
+cudaError_t launch_fp8_small(const Fp8GemmParams& p, int rows, cudaStream_t st) {
+    switch (rows) {
+        case 16: return launch<16>(p, st);
+        case 32: return launch<32>(p, st);
+        case 64: return launch<64>(p, st);
+        case 128: return launch<128>(p, st);
+        case 256: return launch<256>(p, st);
     }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace tpmlp

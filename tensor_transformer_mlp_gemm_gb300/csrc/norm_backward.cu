@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
         ptx::mbar_arrive_expect_tx(bar, bytes * static_cast<uint32_t>(n * arrays));
         if (bytes == 0) return;
         for (int i = 0; i < n; ++i) {
-            const int k = copy_chunk.q;
+            const uint32_t k = copy_chunk.q;
             const long long off = static_cast<long long>(copy_chunk.r) * p.h + c0;
             const uint32_t dst = ptx::smem_u32(ring) + (stage * R + i) * (NB_ARRAYS * ROW);
             auto get = [&](int a, const void* base, long long o) {
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
             stage = 0;
             ring_phase ^= 1u;
         }
-        int k[R];
+        uint32_t k[R];
         long long off[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
                     sums[i] = sv.x + sv.y;
                     if (POST_LAYER) sums[R + i] = sw.x + sw.y;
                 }
-                const int seq_q = seq.q;
+                const uint32_t seq_q = seq.q;
                 const bool seq_end = seq.r + 1 == seq.n;
                 seq.step();
                 if (gate && !cut && row + i < last && seq_end) {

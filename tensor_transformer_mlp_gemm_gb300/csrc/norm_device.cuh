@@ -32,13 +32,13 @@ __device__ __forceinline__ uint4 zero4() { return make_uint4(0, 0, 0, 0); }
 // Quotient and remainder of start, start + stride, start + 2 stride, ... by n, all of
 // them below 2^31: divided once, then stepped.
 struct Stepper {
-    int q, r, dq, dr, n;
+    uint32_t q, r, dq, dr, n;  // (r + dr may pass 2^31)
     __device__ __forceinline__ Stepper(long long start, long long stride, long long by) {
-        n = static_cast<int>(by);
-        q = static_cast<int>(start) / n;
-        r = static_cast<int>(start) - q * n;
-        dq = static_cast<int>(stride) / n;
-        dr = static_cast<int>(stride) - dq * n;
+        n = static_cast<uint32_t>(by);
+        q = static_cast<uint32_t>(start) / n;
+        r = static_cast<uint32_t>(start) - q * n;
+        dq = static_cast<uint32_t>(stride) / n;
+        dr = static_cast<uint32_t>(stride) - dq * n;
     }
     __device__ __forceinline__ void step() {
         q += dq;

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
     int stage = 0;
     uint32_t phase = 0;
     for (long long row = blockIdx.x; row < p.T; row += gridDim.x, chunk.step()) {
-        const int k = chunk.q;
+        const uint32_t k = chunk.q;
         const long long off = static_cast<long long>(chunk.r) * p.h;
         auto at = [&](const void* base, int j) {
             return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + off + c[j]);

@@ -61,11 +61,10 @@ class _Packed:
             return None
         T, C = self.T, self.C
         if k % 2 == 0:
-            at = self.at[k] + i * self.q
-            return self.buf[at:at + self.q].view(DTYPES[self.fmt]).view(T, C)
+            return self.buf.view(DTYPES[self.fmt]).as_strided((T, C), (C, 1), self.at[k] + i * self.q)
         shape = (_up128(C), T) if k == 1 else (_up128(T), C)
-        at = self.at[k] + i * self.steps[k // 2]
-        return self.buf[at:at + 4 * shape[0] * shape[1]].view(torch.float32).view(shape)
+        return self.buf.view(torch.float32).as_strided(
+            shape, (shape[1], 1), (self.at[k] + i * self.steps[k // 2]) // 4)
 
 
 class Fp8Tokens:
@@ -251,7 +250,8 @@ class DeviceFp8Linear:
         need = binding.tpmlp_fp8_linear_workspace_bytes(self.dims)
         if need == 0:
             raise ValueError(f"unsupported dims for an 8-bit linear layer: {w}")
-        self.Wq, self.Ws, self.b = list(Wq), list(Ws), b
+        # (pointers of the layer's own buffers are marshalled once, so it keeps them)
+        self._Wq, self._Ws, self.b = tuple(Wq), tuple(Ws), b
         if not b.is_cuda:
             raise ValueError(f"the layer's tensors must be CUDA tensors, got b on {b.device}")
         self.device = dev = b.device
@@ -276,19 +276,29 @@ class DeviceFp8Linear:
             raise ValueError(f"the workspace needs {need} bytes")
         self.ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8,
                                                                       device=dev)
-        # pointer arrays of the layer's own buffers, marshalled once
         self._weights = (_pointers(self.Wq), _pointers(self.Ws))
-        self._own = {"Y": (self.Y, _pointers(self.Y)), "dX": (self.dX, _pointers(self.dX))}
 
-    def _outputs(self, name: str):
-        """The pointer array of a list of the layer's buffers (which a caller may have
-        replaced)."""
-        xs = getattr(self, name)
-        kept, arr = self._own[name]
-        if xs is not kept:
-            arr = _pointers(self._list(xs, self._y if name == "Y" else self._dx, name))
-            self._own[name] = (xs, arr)
-        return arr
+    # lists of their own: to exchange a buffer, set the attribute
+    Wq = property(lambda self: list(self._Wq))
+    Ws = property(lambda self: list(self._Ws))
+
+    @property
+    def Y(self):
+        return list(self._Y)
+
+    @Y.setter
+    def Y(self, xs):
+        self._Y = tuple(self._list(xs, self._y, "Y"))
+        self._y_ptrs = _pointers(self._Y)
+
+    @property
+    def dX(self):
+        return list(self._dX)
+
+    @dX.setter
+    def dX(self, xs):
+        self._dX = tuple(self._list(xs, self._dx, "dX"))
+        self._dx_ptrs = _pointers(self._dX)
 
     def _weight_grads(self):
         # fp32 gradients, four times the weights' bytes: made by the first backward call
@@ -349,7 +359,7 @@ class DeviceFp8Linear:
     def forward(self, x, Y=None, stream=None) -> None:
         """x: by rows, as ``quantize`` makes it (column: Fp8Tokens, row: t of them)."""
         q, s = self._tokens(x, cols=False)
-        Y = self._outputs("Y") if Y is None else _pointers(self._list(Y, self._y, "Y"))
+        Y = self._y_ptrs if Y is None else _pointers(self._list(Y, self._y, "Y"))
         with binding.on_device(self.device):
             stream = binding.stream_on(self.device, stream)
             if self.column:
@@ -364,7 +374,7 @@ class DeviceFp8Linear:
         ``quantize`` makes it."""
         q, s = self._tokens(x, cols=True)
         dY = _pointers(self._list(dY, self._y, "dY"))
-        dX = self._outputs("dX") if dX is None else _pointers(self._list(dX, self._dx, "dX"))
+        dX = self._dx_ptrs if dX is None else _pointers(self._list(dX, self._dx, "dX"))
         dW, db = self._weight_grads()
         with binding.on_device(self.device):
             stream = binding.stream_on(self.device, stream)
