@@ -250,6 +250,17 @@ def stream_on(device: torch.device, stream) -> int:
     return _stream(stream)
 
 
+def allocate_on(device: torch.device, stream):
+    """Context in which PyTorch allocates for `stream` (a call that makes its outputs
+    itself: a block freed by the current stream could still be in use there)."""
+    if stream is None:
+        return _HERE
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
 def _opt(xs):
     """A pointer array, or NULL for None."""
     return None if xs is None else _arr(xs)

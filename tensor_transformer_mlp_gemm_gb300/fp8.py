@@ -33,7 +33,8 @@ class _Packed:
     """n matrices [T, C] in 8 bits with their scales, side by side in one buffer (an
     allocation costs more host time than a launch)."""
 
-    def __init__(self, n: int, T: int, C: int, fmt: str, rows: bool, cols: bool, device):
+    def __init__(self, n: int, T: int, C: int, fmt: str, rows: bool, cols: bool, device,
+                 stream=None):
         self.n, self.T, self.C, self.fmt, self.device = n, T, C, fmt, device
         self.q = T * C                                       # bytes of one matrix
         # of its scales; every matrix's start on 16 bytes
@@ -45,7 +46,8 @@ class _Packed:
             if wanted:
                 self.at[k] = at
                 at += _up256(n * size)
-        self.buf = torch.empty(max(at, 256), dtype=torch.uint8, device=device)
+        with binding.allocate_on(device, stream):
+            self.buf = torch.empty(max(at, 256), dtype=torch.uint8, device=device)
         self.base = self.buf.data_ptr()
 
     def pointers(self, cols: bool):
@@ -179,7 +181,7 @@ def quantize_tokens(X, fmt: str = "e4m3", rows: bool = True, cols: bool = False,
         raise ValueError("choose rows, cols or both")
     T, dev = tc * n, first.device
     if out is None:
-        pack = _Packed(1, T, C, fmt, rows, cols, dev)
+        pack = _Packed(1, T, C, fmt, rows, cols, dev, stream)
         out = Fp8Tokens._of(pack, 0)
         at = [None if a is None else pack.base + a for a in pack.at]
     else:
@@ -209,7 +211,7 @@ def quantize_shards(shards, fmt: str = "e4m3", rows: bool = True, cols: bool = F
     if not (rows or cols):
         raise ValueError("choose rows, cols or both")
     T, C = shards[0].shape
-    pack = _Packed(len(shards), T, C, fmt, rows, cols, shards[0].device)
+    pack = _Packed(len(shards), T, C, fmt, rows, cols, shards[0].device, stream)
     _quantize(shards, code, max(T, 1), pack.pointers(False) if rows else None,
               pack.pointers(True) if cols else None, stream)
     return Fp8Shards(pack)
@@ -220,8 +222,9 @@ def quantize_weight(W: torch.Tensor, fmt: str = "e4m3", stream=None) -> tuple:
     code = _format(fmt)
     _check_bf16(W, "W")
     r, c = W.shape
-    q = torch.empty(r, c, dtype=DTYPES[fmt], device=W.device)
-    s = torch.empty(_up128(r), _up128(c), dtype=torch.float32, device=W.device)
+    with binding.allocate_on(W.device, stream):
+        q = torch.empty(r, c, dtype=DTYPES[fmt], device=W.device)
+        s = torch.empty(_up128(r), _up128(c), dtype=torch.float32, device=W.device)
     with binding.on_device(W.device):
         binding.tpmlp_fp8_quantize_weight(W, r, c, code, q, s, binding.stream_on(W.device, stream))
     return q, s
@@ -300,14 +303,15 @@ class DeviceFp8Linear:
         self._dX = tuple(self._list(xs, self._dx, "dX"))
         self._dx_ptrs = _pointers(self._dX)
 
-    def _weight_grads(self):
+    def _weight_grads(self, stream=None):
         # fp32 gradients, four times the weights' bytes: made by the first backward call
         if self._grads is None:
-            shape = self.Wq[0].shape
-            self._grads = ([torch.empty(shape, dtype=torch.float32, device=self.device)
-                            for _ in range(self.w.t)],
-                           torch.empty(self.w.out_features, dtype=torch.float32,
-                                       device=self.device))
+            shape = self._Wq[0].shape
+            with binding.allocate_on(self.device, stream):
+                self._grads = ([torch.empty(shape, dtype=torch.float32, device=self.device)
+                                for _ in range(self.w.t)],
+                               torch.empty(self.w.out_features, dtype=torch.float32,
+                                           device=self.device))
         return self._grads
 
     @property
@@ -375,7 +379,7 @@ class DeviceFp8Linear:
         q, s = self._tokens(x, cols=True)
         dY = _pointers(self._list(dY, self._y, "dY"))
         dX = self._dx_ptrs if dX is None else _pointers(self._list(dX, self._dx, "dX"))
-        dW, db = self._weight_grads()
+        dW, db = self._weight_grads(stream)
         with binding.on_device(self.device):
             stream = binding.stream_on(self.device, stream)
             if self.column:

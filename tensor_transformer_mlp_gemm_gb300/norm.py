@@ -130,18 +130,21 @@ class DeviceNormResidual:
                 self.pre_beta, _pointers(self._Out) if z else None, self._Xn and _pointers(self._Xn),
                 self.q, self.q_scale, self.stats, binding.stream_on(self.device, stream))
 
-    def _gradients(self):
+    def _gradients(self, stream=None):
+        # made by the first backward call
         if self._grads is None:
             vec = lambda: torch.empty(self.hidden, dtype=torch.float32, device=self.device)  # noqa: E731
-            self._grads = {
-                "dX": self._rows(), "dZ": self._rows(),
-                "dpost_gamma": vec() if self.post != "none" else None,
-                "dpost_beta": vec() if self.post == "layer" else None,
-                "dpre_gamma": vec() if self.pre != "none" else None,
-                "dpre_beta": vec() if self.pre == "layer" else None,
-                "dgate": torch.empty(self.tokens // self.gate_rows, self.hidden, dtype=torch.float32,
-                                     device=self.device) if self.gate_rows else None,
-                "ws": torch.empty(self._need, dtype=torch.uint8, device=self.device)}
+            with binding.allocate_on(self.device, stream):
+                self._grads = {
+                    "dX": self._rows(), "dZ": self._rows(),
+                    "dpost_gamma": vec() if self.post != "none" else None,
+                    "dpost_beta": vec() if self.post == "layer" else None,
+                    "dpre_gamma": vec() if self.pre != "none" else None,
+                    "dpre_beta": vec() if self.pre == "layer" else None,
+                    "dgate": torch.empty(self.tokens // self.gate_rows, self.hidden,
+                                         dtype=torch.float32, device=self.device)
+                    if self.gate_rows else None,
+                    "ws": torch.empty(self._need, dtype=torch.uint8, device=self.device)}
         return self._grads
 
     dX = property(lambda self: self._one(self._gradients()["dX"]))
@@ -164,7 +167,7 @@ class DeviceNormResidual:
         stats = self.stats if stats is None else stats
         _check_like(stats, (4, self.tokens), torch.float32, self.device, "stats")
         self._check_gate(gate, z)
-        d = self._gradients()
+        d = self._gradients(stream)
         opt = lambda x, what: None if x is None else _pointers(self._list(x, what))  # noqa: E731
         with binding.on_device(self.device):
             binding.tpmlp_norm_backward(
