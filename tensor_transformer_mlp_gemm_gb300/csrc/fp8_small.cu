@@ -9,7 +9,7 @@
 // shared memory: each CTA leaves its sums in its own, and adds a share of the
 // tokens over all of them, in the order of the CTAs.
 // Measured with cold caches, launch included: one token, 12288 -> 12288 features in 39 us
-// (151 MB; 22 us at the copy rate), 4096 -> 12288 in 18 us; 48 tokens 43 and 20 us.
+// (151 MB; 22 us at the copy rate), 4096 -> 12288 in 18 us; 48 tokens 39 and 20 us.
 //
 // CTA layout (256 threads):
 //   warp 0       TMA producer: 128 features and the tile's tokens for each K block
@@ -326,8 +326,14 @@ void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int splits) {
     cfg.numAttrs = 2;
 }
 
-// Clusters of each size that a device runs at once with one CTA on an SM (a cluster lies
-// in one group of SMs: 15 of 8 CTAs and 36 of 4 on 152 SMs).
+// Stands in for the kernel where the runtime is asked how many of its clusters run at
+// once: of a kernel that allocates tensor memory it counts one CTA on an SM, whatever it
+// allocates.  (Never launched; as many registers as two CTAs may have.)
+template <int TN>
+__global__ void __launch_bounds__(S_THREADS, Small<TN>::kPerSm) fp8_small_stand_in() {}
+
+// Clusters of each size that a device runs at once (a cluster lies in one group of SMs:
+// with two CTAs on an SM 97 of 3, 74 of 4 and 36 of 8 on 152 SMs).
 template <int TN>
 cudaError_t resident(const int*& clusters) {
     constexpr int kDevices = 64;
@@ -341,13 +347,16 @@ cudaError_t resident(const int*& clusters) {
         e = cudaFuncSetAttribute(fp8_small_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Small<TN>::kSmem);
         if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(fp8_small_stand_in<TN>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Small<TN>::kSmem);
+        if (e != cudaSuccess) return e;
         for (int c = 1; c <= S_MAX_SPLIT; ++c) {
             cudaLaunchConfig_t cfg = {};
             cudaLaunchAttribute attr[2];
             configure<TN>(cfg, attr, c);
             cfg.numAttrs = 1;
             int n = 0;
-            e = cudaOccupancyMaxActiveClusters(&n, fp8_small_kernel<TN>, &cfg);
+            e = cudaOccupancyMaxActiveClusters(&n, fp8_small_stand_in<TN>, &cfg);
             if (e != cudaSuccess) return e;
             __atomic_store_n(&known[dev][c], n, __ATOMIC_RELAXED);
         }
@@ -367,10 +376,9 @@ cudaError_t launch(const Fp8GemmParams& p, cudaStream_t st) {
     const long long nk = static_cast<long long>((p.K + F8_BK - 1) / F8_BK) * p.ksegs;
     // The widest split whose CTAs all run at once and still have a K block each.  128
     // tokens, 12288 -> 4608 features (36 tiles): 4 parts 22 us, 3 or 5 parts 25 or 33;
-    // 48 tokens, 12288 -> 12288 (96 tiles): 2 parts 43 us, 1 or 4 parts 53 or 47.
+    // 48 tokens, 12288 -> 12288 (96 tiles): 3 parts 39 us, 2 or 4 parts 43 or 47.
     int splits = static_cast<int>(nk < S_MAX_SPLIT ? nk : S_MAX_SPLIT);
-    while (splits > 1 && tiles * rows > static_cast<long long>(Small<TN>::kPerSm) * clusters[splits])
-        --splits;
+    while (splits > 1 && tiles * rows > clusters[splits]) --splits;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     configure<TN>(cfg, attr, splits);
