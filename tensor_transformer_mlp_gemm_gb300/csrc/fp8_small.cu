@@ -33,10 +33,13 @@ constexpr int S_WARPS = 4;       // scale and output warps
 constexpr int S_MAX_SPLIT = 8;   // the portable cluster size
 constexpr int S_AHEAD = 4;       // K blocks whose scales are under way
 
-// Up to 64 tokens two CTAs fit an SM; from 128 on one, whose ring is as deep as both.
-template <int TN>
+// Up to 64 tokens two CTAs take an SM, at 256 one.  At 128 either: one with a ring as
+// deep as two have together, or two.  One is faster while K can be cut in two with it
+// (12288 -> 4608 features 22 us, two 25), two for wider layers (12288 -> 12288 43 us,
+// one 53).
+template <int TN, int PER_SM>
 struct Small {
-    static constexpr int kStages = TN == 16 ? 6 : TN == 32 ? 5 : TN == 64 ? 4 : TN == 128 ? 6 : 4;
+    static constexpr int kStages = TN == 16 ? 6 : TN == 32 ? 5 : TN == 64 ? 4 : TN == 256 ? 4 : PER_SM == 2 ? 3 : 6;
     static constexpr int kStageBytes = F8_BOX_BYTES + TN * 128;
     static constexpr int kSmem = 1024 + kStages * kStageBytes + 256;
     static constexpr int kSums = TN < 32 ? 32 : TN;      // columns of sums
@@ -46,7 +49,7 @@ struct Small {
     static constexpr int kTmemCols = kSums + kStages * kSlot <= 128   ? 128
                                      : kSums + kStages * kSlot <= 256 ? 256
                                                                       : 512;
-    static constexpr int kPerSm = TN <= 64 ? 2 : 1;
+    static constexpr int kPerSm = PER_SM;
     static_assert(kSums + kStages * kSlot <= 512 / kPerSm, "tensor memory");
     static_assert(TN * 128 * 4 <= kStages * kStageBytes, "the sums fit where the operands were");
     static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
@@ -70,10 +73,10 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-template <int TN>
-__global__ void __launch_bounds__(S_THREADS, Small<TN>::kPerSm)
+template <int TN, int PER_SM>
+__global__ void __launch_bounds__(S_THREADS, Small<TN, PER_SM>::kPerSm)
     fp8_small_kernel(const __grid_constant__ Fp8GemmParams p, int splits) {
-    using C = Small<TN>;
+    using C = Small<TN, PER_SM>;
     constexpr int NST = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -311,11 +314,11 @@ __global__ void __launch_bounds__(S_THREADS, Small<TN>::kPerSm)
 }
 
 // attr: two of them, the cluster's first
-template <int TN>
+template <int TN, int PER_SM>
 void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int splits) {
     cfg.gridDim = dim3(static_cast<unsigned>(splits), 1, 1);
     cfg.blockDim = dim3(S_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = Small<TN>::kSmem;
+    cfg.dynamicSmemBytes = Small<TN, PER_SM>::kSmem;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
     attr[0].val.clusterDim.y = 1;
@@ -329,12 +332,12 @@ void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int splits) {
 // Stands in for the kernel where the runtime is asked how many of its clusters run at
 // once: of a kernel that allocates tensor memory it counts one CTA on an SM, whatever it
 // allocates.  (Never launched; as many registers as two CTAs may have.)
-template <int TN>
-__global__ void __launch_bounds__(S_THREADS, Small<TN>::kPerSm) fp8_small_stand_in() {}
+template <int TN, int PER_SM>
+__global__ void __launch_bounds__(S_THREADS, Small<TN, PER_SM>::kPerSm) fp8_small_stand_in() {}
 
 // Clusters of each size that a device runs at once (a cluster lies in one group of SMs:
 // with two CTAs on an SM 97 of 3, 74 of 4 and 36 of 8 on 152 SMs).
-template <int TN>
+template <int TN, int PER_SM>
 cudaError_t resident(const int*& clusters) {
     constexpr int kDevices = 64;
     static int known[kDevices][S_MAX_SPLIT + 1] = {};
@@ -344,19 +347,19 @@ cudaError_t resident(const int*& clusters) {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
     if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
-        e = cudaFuncSetAttribute(fp8_small_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Small<TN>::kSmem);
+        e = cudaFuncSetAttribute(fp8_small_kernel<TN, PER_SM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Small<TN, PER_SM>::kSmem);
         if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(fp8_small_stand_in<TN>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Small<TN>::kSmem);
+        e = cudaFuncSetAttribute(fp8_small_stand_in<TN, PER_SM>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Small<TN, PER_SM>::kSmem);
         if (e != cudaSuccess) return e;
         for (int c = 1; c <= S_MAX_SPLIT; ++c) {
             cudaLaunchConfig_t cfg = {};
             cudaLaunchAttribute attr[2];
-            configure<TN>(cfg, attr, c);
+            configure<TN, PER_SM>(cfg, attr, c);
             cfg.numAttrs = 1;
             int n = 0;
-            e = cudaOccupancyMaxActiveClusters(&n, fp8_small_stand_in<TN>, &cfg);
+            e = cudaOccupancyMaxActiveClusters(&n, fp8_small_stand_in<TN, PER_SM>, &cfg);
             if (e != cudaSuccess) return e;
             __atomic_store_n(&known[dev][c], n, __ATOMIC_RELAXED);
         }
@@ -366,10 +369,10 @@ cudaError_t resident(const int*& clusters) {
     return cudaSuccess;
 }
 
-template <int TN>
+template <int TN, int PER_SM>
 cudaError_t launch(const Fp8GemmParams& p, cudaStream_t st) {
     const int* clusters = nullptr;
-    const cudaError_t e = resident<TN>(clusters);
+    const cudaError_t e = resident<TN, PER_SM>(clusters);
     if (e != cudaSuccess) return e;
     const long long tiles = static_cast<long long>((p.N + 127) / 128) * p.groups;
     const long long rows = (p.M + TN - 1) / TN;
@@ -381,10 +384,10 @@ cudaError_t launch(const Fp8GemmParams& p, cudaStream_t st) {
     while (splits > 1 && tiles * rows > clusters[splits]) --splits;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    configure<TN>(cfg, attr, splits);
+    configure<TN, PER_SM>(cfg, attr, splits);
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), static_cast<unsigned>(rows), 1);
     cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, fp8_small_kernel<TN>, p, splits);
+    return cudaLaunchKernelEx(&cfg, fp8_small_kernel<TN, PER_SM>, p, splits);
 }
 
 }  // namespace
@@ -393,7 +396,7 @@ cudaError_t fp8_small_rows(int M, int N, int groups, int& rows) {
     rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     if (M <= 128) return cudaSuccess;
     const int* clusters = nullptr;
-    const cudaError_t e = resident<256>(clusters);
+    const cudaError_t e = resident<256, 1>(clusters);
     if (e != cudaSuccess) return e;
     // Pairs on 256 x 256 tiles are faster unless so few tiles that K can be cut in four
     // here.  256 tokens: 12288 -> 4096 features (32 tiles) 29 us here and 37 on pairs,
@@ -405,11 +408,17 @@ cudaError_t fp8_small_rows(int M, int N, int groups, int& rows) {
 
 cudaError_t launch_fp8_small(const Fp8GemmParams& p, int rows, cudaStream_t st) {
     switch (rows) {
-        case 16: return launch<16>(p, st);
-        case 32: return launch<32>(p, st);
-        case 64: return launch<64>(p, st);
-        case 128: return launch<128>(p, st);
-        case 256: return launch<256>(p, st);
+        case 16: return launch<16, 2>(p, st);
+        case 32: return launch<32, 2>(p, st);
+        case 64: return launch<64, 2>(p, st);
+        case 128: {
+            const int* clusters = nullptr;
+            const cudaError_t e = resident<128, 1>(clusters);
+            if (e != cudaSuccess) return e;
+            const long long tiles = static_cast<long long>((p.N + 127) / 128) * p.groups;
+            return tiles <= clusters[2] ? launch<128, 1>(p, st) : launch<128, 2>(p, st);
+        }
+        case 256: return launch<256, 1>(p, st);
     }
     return cudaErrorInvalidValue;
 }

@@ -301,7 +301,8 @@ def test_threads():
     ("row", 1280, 2064, 2576, 3, 1),
     ("column", 257, 272, 1552, 1, 1),     # one row into a second tile
     ("column", 130, 400, 528, 1, 1),      # tiles of 256 tokens
-    ("row", 256, 6160, 144, 5, 2)])
+    ("row", 256, 6160, 144, 5, 2),
+    ("column", 100, 272, 9984, 1, 1)])    # two CTAs on an SM with 128 tokens each
 def test_linear_more_shapes(split, T, din, dout, t, chunks):
     lay, X, dY = f8._layer(custom_linear(T, din, dout, t, split, seq_chunks=chunks), T + din)
     x = lay.quantize(X, cols=True)
