@@ -8,10 +8,14 @@
 // each layer norm (mean, then the squares of what is left: no cancellation).
 // One thread keeps bulk copies of the CTA's next two rows (X, Z, gate) under way into
 // shared memory: loaded when they were needed, rows spent half their time waiting.
-// A CTA walks rows a grid apart; its columns' weights come from L1 at each row
-// (kept in registers they spill or halve the rows in flight), and the row's token
-// chunk and gate are stepped, not divided out: three 64-bit divisions a row and
-// thread were 40 % of the instructions.
+// What is left is bound by instructions, issued in 71 % of all cycles (ncu), so fp32
+// values go two at a time (packed fma, 16384 x 4096 with 8-bit Xn 113 -> 98 us).
+// A CTA walks rows a grid apart; its columns' weights come from L1 at each row (in
+// registers they spill: layer norms 106 -> 139 us), and the row's token chunk and gate
+// are stepped, not divided out: three 64-bit divisions a row and thread were 40 % of
+// the instructions.
+// Measured, rms norms and a gate, cold caches, launch included: 16384 x 4096 in 88 us
+// (6.1 TB/s), with 8-bit Xn 96; 8192 x 8192 88; 2048 x 12288 43; 16384 x 1024 29.
 #include "fp8_cvt.cuh"
 #include "gemm_params.h"
 #include "norm_device.cuh"
@@ -70,7 +74,7 @@ __device__ __forceinline__ void row_stats(const float2 (&x)[V][4], const bool (&
     rstd = rsqrtf(block_sum(q.x + q.y, smem, buf) * inv_h + eps);
 }
 
-template <int POST, int PRE, int V>
+template <int POST, int PRE, int V, bool FULL>
 __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant__ NrForwardParams p) {
     extern __shared__ __align__(128) uint8_t ring[];  // [stage][X, Z, gate][row]
     __shared__ alignas(16) float smem[2][32];
@@ -94,7 +98,7 @@ __global__ void __launch_bounds__(1024) nr_forward_kernel(const __grid_constant_
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         c[j] = (j * blockDim.x + threadIdx.x) * 8;
-        in[j] = c[j] < p.h;
+        in[j] = FULL || c[j] < p.h;
     }
     Stepper chunk(blockIdx.x, gridDim.x, p.rows_per_chunk);
     Stepper copy_chunk(blockIdx.x, gridDim.x, p.rows_per_chunk), copy_gate(blockIdx.x, gridDim.x, p.gate_rows);
@@ -262,18 +266,23 @@ cudaError_t launch(const NrForwardParams& p, int sm_count, cudaStream_t st) {
     const int smem = NF_STAGES * 3 * ((p.h * 2 + 127) / 128 * 128);
     // 64 registers a thread let 1024 threads onto an SM; their rings always fit
     const long long resident = static_cast<long long>(sm_count) * (1024 / threads);
-    auto kernel = V == 1 ? nr_forward_kernel<POST, PRE, 1> : nr_forward_kernel<POST, PRE, 2>;
+    // a row that fills every thread needs no test of its columns (layer norms at 16384 x
+    // 4096 113 -> 106 us)
+    const bool full = static_cast<long long>(threads) * V * 8 == p.h;
+    auto kernel = V == 1 ? (full ? nr_forward_kernel<POST, PRE, 1, true> : nr_forward_kernel<POST, PRE, 1, false>)
+                         : (full ? nr_forward_kernel<POST, PRE, 2, true> : nr_forward_kernel<POST, PRE, 2, false>);
+    const int variant = (V - 1) * 2 + (full ? 1 : 0);
     constexpr int kDevices = 64;
-    static int ready[kDevices][2] = {};  // the kernel's attribute is set, per device
+    static int ready[kDevices][4] = {};  // the kernel's attribute is set, per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
-    if (!__atomic_load_n(&ready[dev][V - 1], __ATOMIC_ACQUIRE)) {
+    if (!__atomic_load_n(&ready[dev][variant], __ATOMIC_ACQUIRE)) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  NF_STAGES * 3 * NR_MAX_H * 2);
         if (e != cudaSuccess) return e;
-        __atomic_store_n(&ready[dev][V - 1], 1, __ATOMIC_RELEASE);
+        __atomic_store_n(&ready[dev][variant], 1, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.T < resident ? p.T : resident), 1, 1);
