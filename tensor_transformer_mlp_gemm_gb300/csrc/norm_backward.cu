@@ -32,7 +32,8 @@ namespace {
 
 using namespace nr;
 
-constexpr int NB_THREADS = 512;
+constexpr int NB_THREADS = 512;          // of a CTA, or 384 of some clusters'
+constexpr int NB_FEWER = 384;
 constexpr int NB_COLS = NB_THREADS * 8;  // columns of one CTA
 constexpr int NB_WARPS = NB_THREADS / 32;
 constexpr int NB_MAX_CLUSTER = 4;
@@ -43,8 +44,13 @@ constexpr int NB_STAGES = 2;             // row pairs in the ring
 constexpr int NB_RING = NB_STAGES * NB_ROWS * NB_ARRAYS * NB_COLS * 2;
 static_assert(NB_COLS * NB_MAX_CLUSTER >= NR_MAX_H, "a cluster holds the widest row");
 
-// CTAs side by side for a row, and groups of a CTA's threads that take rows of their own.
+// CTAs side by side for a row, their threads, and groups of a CTA's threads that take rows
+// of their own.
 int cluster_of(long long h) { return static_cast<int>((h + NB_COLS - 1) / NB_COLS); }
+int threads_of(long long h) {
+    const int cl = cluster_of(h);
+    return cl > 1 && h <= static_cast<long long>(cl) * NB_FEWER * 8 ? NB_FEWER : NB_THREADS;
+}
 int groups_of(long long h) {
     int g = 1;
     while (g < NB_MAX_GROUPS && h <= NB_COLS / (2 * g)) g *= 2;
@@ -113,10 +119,10 @@ __device__ __forceinline__ float warp_sums(const float (&v)[N], int lane) {
 // Sums of N values over a row: the group's warps, and the cluster's CTAs.  The buffers
 // alternate: a part of the next but one sum can only come once every warp has given its
 // part of the next, and so has read this one.
-template <int CL, int G, int N>
+template <int CL, int WG, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], Shared& sm, int& buf, uint32_t (&phase)[2],
                                          int group, int rank, const Waits& w) {
-    constexpr int WG = NB_WARPS / G, SLOTS = CL * WG, LP = 32 / N;
+    constexpr int SLOTS = CL * WG, LP = 32 / N;
     const int warp = (threadIdx.x >> 5) % WG, lane = threadIdx.x & 31;
     float* part = sm.part[buf] + group * (NB_VALUES * WG);
     const float x = warp_sums<N>(v, lane);
@@ -151,12 +157,12 @@ __device__ __forceinline__ void row_sums(float (&v)[N], Shared& sm, int& buf, ui
     buf ^= 1;
 }
 
-template <int POST, int PRE, int CL, int G>
-__global__ void __launch_bounds__(NB_THREADS, 1)
+template <int POST, int PRE, int CL, int G, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
     nr_backward_kernel(const __grid_constant__ NrBackwardParams p) {
     constexpr bool Z = POST != NR_ABSENT, POST_NORM = POST >= NR_POST_RMS, BEFORE = PRE != NR_NONE;
     constexpr bool POST_LAYER = POST == NR_POST_LAYER, PRE_LAYER = PRE == NR_PRE_LAYER;
-    constexpr int R = NB_ROWS, GT = NB_THREADS / G, ROW = GT * 16;  // a row's bytes in the ring
+    constexpr int R = NB_ROWS, GT = THREADS / G, WG = GT / 32, ROW = GT * 16;  // a row's bytes in the ring
     static_assert(CL == 1 || G == 1, "wide rows take whole CTAs");
     extern __shared__ __align__(128) uint8_t ring_all[];
     __shared__ Shared sm;
@@ -164,7 +170,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
     const int group = threadIdx.x / GT, tid = threadIdx.x % GT, lane = threadIdx.x & 31;
     const long long block = blockIdx.x / CL;
     const float inv_h = 1.0f / static_cast<float>(p.h);
-    const int c0 = rank * NB_COLS, c = c0 + tid * 8;
+    const int c0 = rank * (THREADS * 8), c = c0 + tid * 8;
     const bool in = c < p.h;
     const Waits waits = {p.timeout_ns, p.err};
     const bool gate = Z && p.gate != nullptr, dout = p.dout.p[0] != nullptr;
@@ -208,7 +214,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
     }
 
     // the ring: one thread of the group has the copies of a row pair under way
-    const int cols = min(NB_COLS / G, p.h - c0);
+    const int cols = min(GT * 8, p.h - c0);
     const uint32_t bytes = cols > 0 ? static_cast<uint32_t>(cols) * 2 : 0;
     // (a row's token chunk and gate are stepped, not divided out: the divisions were
     // half of all instructions)
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
                 sums[i] = sv.x + sv.y;
                 if (PRE_LAYER) sums[R + i] = sw.x + sw.y;
             }
-            row_sums<CL, G, N>(sums, sm, buf, phase, group, rank, waits);
+            row_sums<CL, WG, N>(sums, sm, buf, phase, group, rank, waits);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 float2 d[4], v[4], w[4];
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
         } else {
 #pragma unroll
             for (int i = 0; i < R; ++i) unpack(q_dout[i], g[i]);
-            if constexpr (CL > 1 || NB_WARPS / G > 1)
+            if constexpr (CL > 1 || WG > 1)
                 asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(GT) : "memory");
             else
                 __syncwarp();
@@ -407,7 +413,7 @@ __global__ void __launch_bounds__(NB_THREADS, 1)
                 }
             }
             if constexpr (POST_NORM) {
-                row_sums<CL, G, N>(sums, sm, buf, phase, group, rank, waits);
+                row_sums<CL, WG, N>(sums, sm, buf, phase, group, rank, waits);
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     float2 z[4];
@@ -527,14 +533,14 @@ __global__ void __launch_bounds__(256) nr_finish_kernel(const __grid_constant__ 
 constexpr int kDevices = 64;
 
 // The kernel's attribute, set once a device.
-template <int POST, int PRE, int CL, int G>
+template <int POST, int PRE, int CL, int G, int THREADS>
 cudaError_t prepare(int& dev) {
     static int ready[kDevices] = {};
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
     if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
-        e = cudaFuncSetAttribute(nr_backward_kernel<POST, PRE, CL, G>,
+        e = cudaFuncSetAttribute(nr_backward_kernel<POST, PRE, CL, G, THREADS>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, NB_RING);
         if (e != cudaSuccess) return e;
         __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
@@ -543,9 +549,10 @@ cudaError_t prepare(int& dev) {
 }
 
 // attr: two of them, the cluster's first
-void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, long long blocks, int cl) {
+void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, long long blocks, int cl,
+               int threads) {
     cfg.gridDim = dim3(static_cast<unsigned>(blocks * cl), 1, 1);
-    cfg.blockDim = dim3(NB_THREADS, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = NB_RING;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(cl);
@@ -557,33 +564,33 @@ void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, long long blo
     cfg.numAttrs = 2;
 }
 
-template <int POST, int PRE, int CL, int G>
+template <int POST, int PRE, int CL, int G, int THREADS = NB_THREADS>
 cudaError_t launch_rows(const NrBackwardParams& p, cudaStream_t st) {
     int dev = 0;
-    const cudaError_t e = prepare<POST, PRE, CL, G>(dev);
+    const cudaError_t e = prepare<POST, PRE, CL, G, THREADS>(dev);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    configure(cfg, attr, p.blocks, CL);
+    configure(cfg, attr, p.blocks, CL, THREADS);
     cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, nr_backward_kernel<POST, PRE, CL, G>, p);
+    return cudaLaunchKernelEx(&cfg, nr_backward_kernel<POST, PRE, CL, G, THREADS>, p);
 }
 
 // Clusters of CL CTAs that run at once (asked once a device; every variant of the kernel
-// takes the same threads and shared memory).
+// takes an SM for itself).
 template <int CL>
 cudaError_t resident(long long& clusters) {
     static int known[kDevices] = {};
     int dev = 0;
-    cudaError_t e = prepare<NR_ABSENT, NR_PRE_RMS, CL, 1>(dev);
+    cudaError_t e = prepare<NR_ABSENT, NR_PRE_RMS, CL, 1, NB_THREADS>(dev);
     if (e != cudaSuccess) return e;
     int n = __atomic_load_n(&known[dev], __ATOMIC_ACQUIRE);
     if (n == 0) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[2];
-        configure(cfg, attr, 1, CL);
+        configure(cfg, attr, 1, CL, NB_THREADS);
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&n, nr_backward_kernel<NR_ABSENT, NR_PRE_RMS, CL, 1>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, nr_backward_kernel<NR_ABSENT, NR_PRE_RMS, CL, 1, NB_THREADS>, &cfg);
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorInvalidConfiguration;
         __atomic_store_n(&known[dev], n, __ATOMIC_RELEASE);
@@ -595,6 +602,10 @@ cudaError_t resident(long long& clusters) {
 template <int POST, int PRE>
 cudaError_t launch(const NrBackwardParams& p, cudaStream_t st) {
     const int cl = cluster_of(p.h);
+    if (threads_of(p.h) == NB_FEWER) {
+        if (cl == 2) return launch_rows<POST, PRE, 2, 1, NB_FEWER>(p, st);
+        return launch_rows<POST, PRE, 3, 1, NB_FEWER>(p, st);
+    }
     if (cl == 2) return launch_rows<POST, PRE, 2, 1>(p, st);
     if (cl == 3) return launch_rows<POST, PRE, 3, 1>(p, st);
     if (cl == 4) return launch_rows<POST, PRE, 4, 1>(p, st);
