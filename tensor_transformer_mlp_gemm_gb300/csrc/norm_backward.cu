@@ -11,15 +11,19 @@
 // are worth 2100 of HBM time.  So a group of threads takes two rows at a time, narrow
 // rows are spread over up to 8 groups of a CTA's 512 threads, and one thread of a group
 // keeps bulk copies of its next rows under way into a ring in shared memory.
-// Rows of more than 4096 columns take a cluster of 2 to 4 CTAs side by side, and as many
-// clusters as run at once (46 of 3 and 36 of 4 on 152 SMs: two more made a second round
-// and doubled the time), whose row
+// Rows of more than 4096 columns take a cluster of 2 to 4 CTAs side by side, whose row
 // sums meet in each other's shared memory: each warp sends its part to every CTA,
 // counted on that CTA's mbarrier, and every warp adds all parts in the same order.  (A
 // cluster barrier instead waits for the row's own loads and stores too: 6600 clocks a
-// row, measured at 917 x 9000.)
+// row, measured at 917 x 9000.)  The CTAs have 384 threads where those hold the row:
+// they have registers for everything (layer norms, 917 x 9000: 43 us, with 512 threads
+// and spills 53; 2048 x 12288: 104 us as 4 x 384, 111 as 3 x 512).  As many clusters are
+// launched as run at once (46 of 3 and 36 of 4 on 152 SMs): two more made a second round
+// and doubled the time.
 // The column sums of a block of rows go to a partial row, and a second kernel adds the
 // blocks in order; a gate whose rows lie in one group is finished there.  No atomics.
+// Measured, rms norms and 8 gates, cold caches, launches included: 16384 x 4096 in 139 us
+// (5.8 TB/s), layer norms 184; 8192 x 8192 168; 2048 x 12288 82; 16384 x 1024 55.
 #include <algorithm>
 
 #include "gemm_params.h"
@@ -32,8 +36,8 @@ namespace {
 
 using namespace nr;
 
-constexpr int NB_THREADS = 512;          // of a CTA, or 384 of some clusters'
-constexpr int NB_FEWER = 384;
+constexpr int NB_THREADS = 512;          // of a CTA
+constexpr int NB_FEWER = 384;            // of a CTA of some clusters
 constexpr int NB_COLS = NB_THREADS * 8;  // columns of one CTA
 constexpr int NB_WARPS = NB_THREADS / 32;
 constexpr int NB_MAX_CLUSTER = 4;
@@ -46,7 +50,9 @@ static_assert(NB_COLS * NB_MAX_CLUSTER >= NR_MAX_H, "a cluster holds the widest 
 
 // CTAs side by side for a row, their threads, and groups of a CTA's threads that take rows
 // of their own.
-int cluster_of(long long h) { return static_cast<int>((h + NB_COLS - 1) / NB_COLS); }
+int cluster_of(long long h) {
+    return h <= NB_COLS ? 1 : h <= 2 * NB_COLS ? 2 : h <= 3 * NB_FEWER * 8 ? 3 : 4;
+}
 int threads_of(long long h) {
     const int cl = cluster_of(h);
     return cl > 1 && h <= static_cast<long long>(cl) * NB_FEWER * 8 ? NB_FEWER : NB_THREADS;
@@ -582,15 +588,15 @@ template <int CL>
 cudaError_t resident(long long& clusters) {
     static int known[kDevices] = {};
     int dev = 0;
-    cudaError_t e = prepare<NR_ABSENT, NR_PRE_RMS, CL, 1, NB_THREADS>(dev);
+    cudaError_t e = prepare<NR_ABSENT, NR_PRE_RMS, CL, 1, NB_FEWER>(dev);
     if (e != cudaSuccess) return e;
     int n = __atomic_load_n(&known[dev], __ATOMIC_ACQUIRE);
     if (n == 0) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[2];
-        configure(cfg, attr, 1, CL, NB_THREADS);
+        configure(cfg, attr, 1, CL, NB_FEWER);
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&n, nr_backward_kernel<NR_ABSENT, NR_PRE_RMS, CL, 1, NB_THREADS>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, nr_backward_kernel<NR_ABSENT, NR_PRE_RMS, CL, 1, NB_FEWER>, &cfg);
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorInvalidConfiguration;
         __atomic_store_n(&known[dev], n, __ATOMIC_RELEASE);
@@ -604,10 +610,10 @@ cudaError_t launch(const NrBackwardParams& p, cudaStream_t st) {
     const int cl = cluster_of(p.h);
     if (threads_of(p.h) == NB_FEWER) {
         if (cl == 2) return launch_rows<POST, PRE, 2, 1, NB_FEWER>(p, st);
-        return launch_rows<POST, PRE, 3, 1, NB_FEWER>(p, st);
+        if (cl == 3) return launch_rows<POST, PRE, 3, 1, NB_FEWER>(p, st);
+        return launch_rows<POST, PRE, 4, 1, NB_FEWER>(p, st);
     }
     if (cl == 2) return launch_rows<POST, PRE, 2, 1>(p, st);
-    if (cl == 3) return launch_rows<POST, PRE, 3, 1>(p, st);
     if (cl == 4) return launch_rows<POST, PRE, 4, 1>(p, st);
     switch (groups_of(p.h)) {
         case 1: return launch_rows<POST, PRE, 1, 1>(p, st);

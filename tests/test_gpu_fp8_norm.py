@@ -313,6 +313,17 @@ def test_linear_more_shapes(split, T, din, dout, t, chunks):
     f8._check_backward(lay, x, dY, "e4m3")
 
 
+@pytest.mark.parametrize("T,h,gate_rows,post,pre", [
+    (90, 6152, 30, "layer", "layer"),     # clusters of two: 512 threads a CTA, then 384
+    (61, 6144, 61, "rms", "layer"),
+    (40, 9224, 8, "layer", "rms"),        # clusters of four
+    (31, 3208, 31, "layer", "layer"),
+    (50, 4096, 0, "none", "layer"),
+    (9, 1032, 3, "rms", "layer")])
+def test_norm_more_widths(T, h, gate_rows, post, pre):
+    nm.test_norm(T, h, gate_rows, post, pre)
+
+
 @pytest.mark.parametrize("split", ["column", "row"])
 def test_linear_empty(split):
     lay, X, dY = f8._layer(custom_linear(0, 256, 512, 2, split), 1)
