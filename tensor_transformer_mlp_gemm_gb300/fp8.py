@@ -275,8 +275,9 @@ class DeviceFp8Linear:
         self.Y = [torch.empty(self._y[0], dtype=bf, device=dev) for _ in range(self._y[1])]
         self.dX = [torch.empty(self._dx[0], dtype=bf, device=dev) for _ in range(self._dx[1])]
         self._grads = None
-        if workspace is not None and workspace.numel() * workspace.element_size() < need:
-            raise ValueError(f"the workspace needs {need} bytes")
+        if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()
+                                      or workspace.numel() * workspace.element_size() < need):
+            raise ValueError(f"the workspace needs {need} contiguous bytes on {dev}")
         self.ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8,
                                                                       device=dev)
         self._weights = (_pointers(self.Wq), _pointers(self.Ws))

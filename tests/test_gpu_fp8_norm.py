@@ -414,6 +414,7 @@ def test_python_refusals():
         lambda: fp8.DeviceFp8Linear(lay.w, lay.Wq, [s[:1].contiguous() for s in lay.Ws], lay.b),
         lambda: fp8.DeviceFp8Linear(lay.w, lay.Wq, lay.Ws, lay.b, w_format="e5m2"),
         lambda: fp8.DeviceFp8Linear(lay.w, lay.Wq, lay.Ws, lay.b, workspace=lay.ws[:16]),
+        lambda: fp8.DeviceFp8Linear(lay.w, lay.Wq, lay.Ws, lay.b, workspace=lay.ws.cpu()),
         lambda: n.forward(d["X"], d["Z"]),                          # its gate is missing
         lambda: n.forward(d["X"], gate=d["gate"]),                  # a gate without Z
         lambda: n.forward(d["X"], d["Z"], d["gate"][:4].contiguous()),
