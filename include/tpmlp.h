@@ -330,7 +330,7 @@ tpmlp_status tpmlp_sp_backward(const tpmlp_dims* dims, const tpmlp_sp_params* sp
  *   weight    blocks of 128 x 128:          s fp32 [ceil(R/128), ceil(C/128)]
  * Conventions, chunking, errors and workspace rules as for the bf16 linear
  * layers, with features and shards multiples of 16 (else
- * TPMLP_ERR_UNSUPPORTED). */
+ * TPMLP_ERR_UNSUPPORTED); scales (s) may start at any multiple of 4 bytes. */
 typedef enum {
     TPMLP_FP8_E4M3 = 0, /* 4 exponent bits, 3 mantissa bits, no infinities */
     TPMLP_FP8_E5M2 = 1  /* 5 exponent bits, 2 mantissa bits */
@@ -445,7 +445,8 @@ tpmlp_status tpmlp_fp8_row_linear_backward(const tpmlp_linear_dims* dims,
  * seq_chunks rows; Xq and Xs are whole.  hidden: a multiple of 8 (16 with Xq), at most
  * 16384; else TPMLP_ERR_UNSUPPORTED.  gate_rows divides tokens, eps >= 0, else
  * TPMLP_ERR_INVALID_ARG.  With tokens = 0 the forward does nothing and the backward
- * zeroes the gammas' and betas' gradients.  The workspace is scratch of one call. */
+ * zeroes the gammas' and betas' gradients.  stats and Xs may start at any multiple of 4
+ * bytes.  The workspace is scratch of one call. */
 typedef enum {
     TPMLP_NORM_NONE = 0,
     TPMLP_NORM_RMS = 1,

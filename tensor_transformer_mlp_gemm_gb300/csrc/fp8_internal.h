@@ -1,5 +1,5 @@
-// fp8_internal.h -- host-side helpers of the 8-bit calls: tensor maps of 8-bit
-// operands through the library's map cache.
+// fp8_internal.h -- host-side helpers of the 8-bit calls: checks of scale pointers, and
+// tensor maps of 8-bit operands through the library's map cache.
 #pragma once
 
 #include <cuda.h>
@@ -21,6 +21,21 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 extern EncodeTiledFn g_encode;
 extern MapCache g_maps;
 extern unsigned long long g_timeout_ns;
+
+// Scales are read and written one at a time: a part of a larger array may start anywhere.
+inline tpmlp_status check_scale(const void* p) {
+    if (!p) return TPMLP_ERR_INVALID_ARG;
+    return reinterpret_cast<uintptr_t>(p) % 4 ? TPMLP_ERR_UNSUPPORTED : TPMLP_OK;
+}
+
+inline tpmlp_status check_scales(const void* const* p, int n) {
+    if (!p) return TPMLP_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        const tpmlp_status s = check_scale(p[i]);
+        if (s != TPMLP_OK) return s;
+    }
+    return TPMLP_OK;
+}
 
 // Row-major 8-bit matrix [outer, inner] (inner a multiple of 16), fetched as
 // boxes of 128 bytes x `box_outer` rows with the 128-byte swizzle; what lies

@@ -257,10 +257,10 @@ tpmlp_status forward(Split k, const tpmlp_linear_dims* dims, const tpmlp_fp8_for
     const int nx = col ? 1 : s.t, ny = col ? s.t : s.chunks;
     TPMLP_TRY(check_ptr(b));
     TPMLP_TRY(check_ptrs(Wq, s.t));
-    TPMLP_TRY(check_ptrs(Ws, s.t));
+    TPMLP_TRY(check_scales(Ws, s.t));
     if (s.T > 0) {
         TPMLP_TRY(check_ptrs(Xq, nx));
-        TPMLP_TRY(check_ptrs(Xs, nx));
+        TPMLP_TRY(check_scales(Xs, nx));
         TPMLP_TRY(check_ptrs(reinterpret_cast<const void* const*>(Y), ny));
         TPMLP_TRY(check_ptr(workspace));
     }
@@ -298,13 +298,13 @@ tpmlp_status backward(Split k, const tpmlp_linear_dims* dims, const tpmlp_fp8_fo
     const bool col = k == Split::Column;
     const int nx = col ? 1 : s.t, ndy = col ? s.t : s.chunks, ndx = col ? s.chunks : s.t;
     TPMLP_TRY(check_ptrs(Wq, s.t));
-    TPMLP_TRY(check_ptrs(Ws, s.t));
+    TPMLP_TRY(check_scales(Ws, s.t));
     TPMLP_TRY(check_ptrs(reinterpret_cast<const void* const*>(dW), s.t));
     TPMLP_TRY(check_ptr(db));
     if (s.T > 0) {
         TPMLP_TRY(check_ptrs(dY, ndy));
         TPMLP_TRY(check_ptrs(Xq, nx));
-        TPMLP_TRY(check_ptrs(Xs, nx));
+        TPMLP_TRY(check_scales(Xs, nx));
         TPMLP_TRY(check_ptrs(reinterpret_cast<const void* const*>(dX), ndx));
         TPMLP_TRY(check_ptr(workspace));
     }
@@ -383,11 +383,11 @@ TPMLP_API tpmlp_status tpmlp_fp8_quantize(const tpmlp_fp8_quant* d, const void* 
         TPMLP_TRY(check_ptrs(src, n));
         if (rows) {
             TPMLP_TRY(check_ptrs(reinterpret_cast<const void* const*>(q_rows), n));
-            TPMLP_TRY(check_ptrs(reinterpret_cast<const void* const*>(s_rows), n));
+            TPMLP_TRY(check_scales(reinterpret_cast<const void* const*>(s_rows), n));
         }
         if (cols) {
             TPMLP_TRY(check_ptrs(reinterpret_cast<const void* const*>(q_cols), n));
-            TPMLP_TRY(check_ptrs(reinterpret_cast<const void* const*>(s_cols), n));
+            TPMLP_TRY(check_scales(reinterpret_cast<const void* const*>(s_cols), n));
         }
     }
     DeviceInfo* dev = nullptr;
@@ -425,7 +425,7 @@ TPMLP_API tpmlp_status tpmlp_fp8_quantize_weight(const void* W, int64_t in, int6
     if (out % 16 != 0 || in > lim || out > lim) return TPMLP_ERR_UNSUPPORTED;
     TPMLP_TRY(check_ptr(W));
     TPMLP_TRY(check_ptr(q));
-    TPMLP_TRY(check_ptr(s));
+    TPMLP_TRY(check_scale(s));
     DeviceInfo* dev = nullptr;
     TPMLP_TRY(device_info(&dev));
     Fp8QuantParams p;

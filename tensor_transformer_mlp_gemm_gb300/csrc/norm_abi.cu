@@ -108,9 +108,9 @@ TPMLP_API tpmlp_status tpmlp_norm_forward(const tpmlp_norm_params* params, const
     if (gate) TPMLP_TRY(check_ptr(gate));
     if (Xq) {
         TPMLP_TRY(check_ptr(Xq));
-        TPMLP_TRY(check_ptr(Xs));
+        TPMLP_TRY(check_scale(Xs));
     }
-    if (stats) TPMLP_TRY(check_ptr(stats));
+    if (stats) TPMLP_TRY(check_scale(stats));
     DeviceInfo* dev = nullptr;
     TPMLP_TRY(device_info(&dev));
     if (d.tokens == 0) return TPMLP_OK;
@@ -176,7 +176,7 @@ TPMLP_API tpmlp_status tpmlp_norm_backward(const tpmlp_norm_params* params, cons
     if (d.tokens > 0) {
         TPMLP_TRY(check_weight(gate, gate != nullptr));
         TPMLP_TRY(check_weight(dgate, gate != nullptr));
-        if (post || pre) TPMLP_TRY(check_ptr(stats));
+        if (post || pre) TPMLP_TRY(check_scale(stats));
         TPMLP_TRY(check_ptr(workspace));
     }
     DeviceInfo* dev = nullptr;

@@ -8,7 +8,13 @@ import torch
 from tensor_transformer_mlp_gemm_gb300.inputs import custom_linear
 
 OK_PTR = 0x10000  # 16-byte aligned, never followed
-BAD_PTR = OK_PTR + 8
+BAD_PTR = OK_PTR + 8  # not on 16 bytes
+BAD_SCALE = OK_PTR + 2
+SCALES = ("s", "Xs", "Ws", "stats")
+
+
+def bad_of(name):
+    return BAD_SCALE if name in SCALES else BAD_PTR
 
 
 @pytest.fixture(scope="module")
@@ -52,9 +58,9 @@ def test_quantize(b):
     assert _quantize(b, src=arr(None)) == INV and _quantize(b, src=arr(BAD_PTR)) == UNS
     for name in ("q", "s"):
         assert _quantize(b, **{name: arr(None)}) == INV
-        assert _quantize(b, **{name: arr(BAD_PTR)}) == UNS
+        assert _quantize(b, **{name: arr(bad_of(name))}) == UNS
         assert _quantize(b, col=True, **{name + "c": arr(None)}) == INV
-        assert _quantize(b, col=True, **{name + "c": arr(BAD_PTR)}) == UNS
+        assert _quantize(b, col=True, **{name + "c": arr(bad_of(name))}) == UNS
     # one half of a pair
     d, one = b.make_fp8_quant(256, 128, 256, 1, 0, 0), arr(OK_PTR)
     call = b.library().tpmlp_fp8_quantize
@@ -71,7 +77,7 @@ def test_quantize_weight(b):
     assert call(OK_PTR, 128, 120, 0, OK_PTR, OK_PTR, None) == UNS
     assert call(OK_PTR, 1 << 31, 128, 0, OK_PTR, OK_PTR, None) == UNS
     for i in range(3):
-        for bad, want in ((None, INV), (BAD_PTR, UNS)):
+        for bad, want in ((None, INV), (BAD_SCALE if i == 2 else BAD_PTR, UNS)):
             p = [OK_PTR] * 3
             p[i] = bad
             assert call(p[0], 128, 128, 0, p[1], p[2], None) == want
@@ -121,10 +127,10 @@ def test_linear(b, split, back):
     for name in lists:
         assert call(**{name: None}) == INV
         assert call(**{name: arr(OK_PTR, None)}) == INV
-        assert call(**{name: arr(OK_PTR, BAD_PTR)}) == UNS
+        assert call(**{name: arr(OK_PTR, bad_of(name))}) == UNS
     for name in (["db", "ws"] if back else ["b", "ws"]) + (["Xq", "Xs"] if col else []):
         assert call(**{name: None}) == INV
-        assert call(**{name: BAD_PTR}) == UNS
+        assert call(**{name: bad_of(name)}) == UNS
 
 
 def test_linear_workspace(b):
@@ -189,7 +195,7 @@ def test_norm_pointers(b, back):
             assert _norm(b, back, **{name: arr(OK_PTR, None)}) == INV, name
             assert _norm(b, back, **{name: arr(OK_PTR, BAD_PTR)}) == UNS, name
         else:
-            assert _norm(b, back, **{name: BAD_PTR}) == UNS, name
+            assert _norm(b, back, **{name: bad_of(name)}) == UNS, name
     # what a kind does not have must not be there
     rest = ("dpost_gamma", "dpost_beta", "dpre_gamma", "dpre_beta") if back else ("pre_beta",)
     for kw in ([dict(post="none", post_gamma=OK_PTR), dict(post="rms", post_beta=OK_PTR),

@@ -366,6 +366,39 @@ def test_buffers_are_exchanged():
     assert _equal(Y + lay.Y, want[:2] * 2)
 
 
+@pytest.mark.parametrize("split,T,din,dout,t", [("column", 219, 592, 2432, 8), ("row", 32, 2208, 1040, 2),
+                                                ("column", 4, 832, 4608, 8), ("row", 1300, 2432, 2320, 8)])
+def test_scales_inside_larger_arrays(split, T, din, dout, t):
+    """Scales of all shards in one array: a shard's start on 4 bytes."""
+    from tensor_transformer_mlp_gemm_gb300 import fp8
+    lay, X, dY = f8._layer(custom_linear(T, din, dout, t, split), T)
+    x = lay.quantize(X, cols=True)
+    lay.forward(x)
+    lay.backward(dY, x)
+    _sync()
+
+    def together(xs):
+        flat = torch.cat([torch.zeros(1, device="cuda")] + [v.reshape(-1) for v in xs])[1:]
+        return [v.view(xs[0].shape) for v in flat.split(xs[0].numel())]
+    own = fp8.DeviceFp8Linear(lay.w, lay.Wq, together(lay.Ws), lay.b)
+    xs = [x] if split == "column" else list(x)
+    parts = [fp8.Fp8Tokens(v.rows, r, v.cols, c) for v, r, c in
+             zip(xs, together([v.row_scale for v in xs]), together([v.col_scale for v in xs]))]
+    assert any(s.data_ptr() % 16 for s in own.Ws) and all(p.row_scale.data_ptr() % 16 for p in parts[:1])
+    own.forward(parts)
+    own.backward(dY, parts)
+    _sync()
+    assert _equal(own.Y + own.dX + own.dW + [own.db], lay.Y + lay.dX + lay.dW + [lay.db])
+    # and as outputs
+    out = fp8.Fp8Tokens(torch.empty_like(xs[0].rows), together([torch.empty_like(xs[0].row_scale)])[0],
+                        torch.empty_like(xs[0].cols), together([torch.empty_like(xs[0].col_scale)])[0])
+    src = X if split == "column" else X[0]
+    fp8.quantize_tokens(src, cols=True, out=out)
+    _sync()
+    assert _equal([out.rows, out.row_scale, out.cols, out.col_scale],
+                  [xs[0].rows, xs[0].row_scale, xs[0].cols, xs[0].col_scale])
+
+
 def test_quantize_into_buffers():
     from tensor_transformer_mlp_gemm_gb300 import fp8
     g = f8._gen(1)
