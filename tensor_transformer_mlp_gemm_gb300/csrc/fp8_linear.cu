@@ -124,8 +124,14 @@ struct Product {
     int chunk_rows;    // > 0: rows per token chunk
 };
 
-bool encode_operand(CUtensorMap* m, const Operand& o, int i, int K, int rows, int box) {
-    return o.mn ? encode_bytes(m, o.q[i], rows, K, 128) : encode_bytes(m, o.q[i], K, rows, box);
+bool encode_operand(CUtensorMap* m, const Operand& o, int K, int rows, int box) {
+    if (!(o.mn ? encode_bytes(m, o.q[0], rows, K, 128) : encode_bytes(m, o.q[0], K, rows, box)))
+        return false;
+    for (int i = 1; i < o.n; ++i) {
+        m[i] = m[0];
+        if (!set_address(&m[i], o.q[i])) return false;
+    }
+    return true;
 }
 
 tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int kind, cudaStream_t st) {
@@ -133,15 +139,11 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int kind, cuda
     std::memset(&p, 0, sizeof(p));
     int few = 0;  // rows of a tile of the few-rows kernel
     if (d.out_kind == F8_BF16_BLOCK) TPMLP_CUDA(fp8_small_rows(d.M, d.N, d.groups, few));
-    for (int i = 0; i < d.a.n; ++i) {
-        if (!encode_operand(&p.a_map[i], d.a, i, d.K, d.M, few ? few : 128))
-            return TPMLP_ERR_UNSUPPORTED;
-        p.sa[i] = static_cast<const float*>(d.a.s[i]);
-    }
-    for (int i = 0; i < d.b.n; ++i) {
-        if (!encode_operand(&p.b_map[i], d.b, i, d.K, d.N, 128)) return TPMLP_ERR_UNSUPPORTED;
-        p.sb[i] = static_cast<const float*>(d.b.s[i]);
-    }
+    if (!encode_operand(p.a_map, d.a, d.K, d.M, few ? few : 128) ||
+        !encode_operand(p.b_map, d.b, d.K, d.N, 128))
+        return TPMLP_ERR_UNSUPPORTED;
+    for (int i = 0; i < d.a.n; ++i) p.sa[i] = static_cast<const float*>(d.a.s[i]);
+    for (int i = 0; i < d.b.n; ++i) p.sb[i] = static_cast<const float*>(d.b.s[i]);
     for (int i = 0; i < d.nout; ++i) p.out[i] = d.out[i];
     p.sa_kb = d.sa_kb;
     p.sb_kb = d.sb_kb;
