@@ -23,12 +23,16 @@
 //                columns 128 ((w - 8) / 4) .. into registers, frees the accumulator
 //                for the next tile's MMAs, and writes from there
 // Tensor memory: 256 columns of sums, then 6 x 16 columns of scales.  Two
-// accumulators of 256 columns leave none for the scales; with one, the MMAs wait
-// about 1000 clocks a tile for it to be read.
-// What bounds it: the tensor cores, 512 clocks for each K block of a tile.  Measured:
-// 2048 x 12288 x 36864 in 525 us (3.5 PFLOP/s, the tensor pipe busy in 86 % of the
-// cycles), 16384 x 4096 x 4096 in 165 us; fp32 outputs of 512 x 4096 each, K = 16384, in
-// 180 us (256 tiles for 76 pairs: the fourth round is a third full).
+// accumulators of 256 columns leave none for the scales; with one, the MMAs wait for it
+// to be read.
+// What bounds it: the tensor cores, 512 clocks for each K block of a tile, and nearly as
+// much the 32 KB that each CTA takes from L2 for it: with MMAs of 64 columns instead of
+// 256 and the same copies, 19456 x 8192 x 1024 took 77 us instead of 94.  (So MMAs of
+// fewer columns for a last, narrow tile gained nothing.)  Short K pays for the hand-over
+// of the accumulator and the output, about 3000 clocks a tile.  Measured: 2048 x 12288 x
+// 36864 in 525 us (3.5 PFLOP/s, the tensor pipe busy in 86 % of the cycles), 16384 x 4096
+// x 4096 in 163 us; fp32 outputs of 512 x 4096 each, K = 16384, in 180 us (256 tiles for
+// 76 pairs: the fourth round is a third full), of 1536 x 12288, K = 2048, in 227 us.
 //
 // Every wait is bounded as in the bf16 GEMM: a wait that expires sets a flag
 // that ends the CTA's roles, copies and MMAs in flight are drained (bounded),
@@ -405,11 +409,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             __syncwarp();
             if (lane == 0) arrive_relaxed_cluster(even_free);
 
-            // 64 bytes of each of the warp's 32 rows at a time are turned round in
-            // shared memory and leave as whole sectors, 8 rows to a store
-            // instruction.  (Bulk stores waited for each other's staging, 8600
+            // The warp's rows are turned round in shared memory and leave as whole
+            // sectors: 64 bytes of all 32 rows at a time, 8 rows to a store instruction,
+            // or of fp32 outputs, where the stores count, 128 bytes of 16 rows, 4 rows to
+            // an instruction (1 K block a tile, 4432 x 7744: 35 us instead of 39; bf16
+            // outputs so 8 % slower).  (Bulk stores waited for each other's staging, 8600
             // clocks a tile; each thread storing along its own row, 32 rows to an
-            // instruction, took 9800; this takes 4100; measured.)
+            // instruction, took 9800; this takes about 6500.)
             if (n >= p.N || row0 >= p.M) continue;
             int part = g, y0 = row0;
             if (p.chunk_rows > 0) {
@@ -417,38 +423,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 y0 -= part * p.chunk_rows;
             }
             constexpr int ELEM = F32 ? 4 : 2;
-            constexpr int W = 64 / ELEM, V = 16 / ELEM;  // columns a step, columns a vector
+            constexpr int SEG = F32 ? 128 : 64;       // bytes of a row at a time
+            constexpr int ROWS = 2048 / SEG;          // rows that the buffer takes
+            constexpr int W = SEG / ELEM, V = 16 / ELEM, VECS = SEG / 16;
+            auto swizzle = [](int r) { return F32 ? r & 7 : (r >> 1) & 3; };
             uint8_t* out = static_cast<uint8_t*>(p.out[part]) +
                            (static_cast<long long>(y0) * p.N + n) * ELEM;
-            const int sw = (lane >> 1) & 3, rr = lane >> 2, rv = lane & 3;
+            const int lr = lane % ROWS, rr = lane / VECS, rv = lane % VECS;
 #pragma unroll
             for (int c = 0; c < 128 / W; ++c) {
-                if (n + c * W < p.N) {  // (the same for the whole warp)
-                    __syncwarp();
+                if (n + c * W >= p.N) break;  // (the same for the whole warp)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float* x = acc + c * W + q * V;
-                        uint4 u;
-                        if constexpr (F32) {
-                            u = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
-                                           __float_as_uint(x[2]), __float_as_uint(x[3]));
-                        } else {
-                            const float4* b = reinterpret_cast<const float4*>(bias_buf + c * W + q * V);
-                            const float4 b0 = b[0], b1 = b[1];
-                            u = make_uint4(bf16x2(x[0] + b0.x, x[1] + b0.y), bf16x2(x[2] + b0.z, x[3] + b0.w),
-                                           bf16x2(x[4] + b1.x, x[5] + b1.y), bf16x2(x[6] + b1.z, x[7] + b1.w));
+                for (int h = 0; h < 32; h += ROWS) {
+                    __syncwarp();
+                    if (lane - lr == h) {
+#pragma unroll
+                        for (int q = 0; q < VECS; ++q) {
+                            const float* x = acc + c * W + q * V;
+                            uint4 u;
+                            if constexpr (F32) {
+                                u = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                               __float_as_uint(x[2]), __float_as_uint(x[3]));
+                            } else {
+                                const float4* b =
+                                    reinterpret_cast<const float4*>(bias_buf + c * W + q * V);
+                                const float4 b0 = b[0], b1 = b[1];
+                                u = make_uint4(bf16x2(x[0] + b0.x, x[1] + b0.y),
+                                               bf16x2(x[2] + b0.z, x[3] + b0.w),
+                                               bf16x2(x[4] + b1.x, x[5] + b1.y),
+                                               bf16x2(x[6] + b1.z, x[7] + b1.w));
+                            }
+                            *reinterpret_cast<uint4*>(turn + lr * SEG + ((q ^ swizzle(lr)) << 4)) = u;
                         }
-                        *reinterpret_cast<uint4*>(turn + lane * 64 + ((q ^ sw) << 4)) = u;
                     }
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int r = rr + 8 * i;
+                        const int r = rr + (32 / VECS) * i;
                         const uint4 u = *reinterpret_cast<const uint4*>(
-                            turn + r * 64 + ((rv ^ ((r >> 1) & 3)) << 4));
-                        if (row0 + r < p.M && n + c * W + rv * V < p.N)
-                            *reinterpret_cast<uint4*>(out + static_cast<long long>(r) * p.N * ELEM +
-                                                      c * 64 + rv * 16) = u;
+                            turn + r * SEG + ((rv ^ swizzle(r)) << 4));
+                        if (row0 + h + r < p.M && n + c * W + rv * V < p.N)
+                            *reinterpret_cast<uint4*>(out + static_cast<long long>(h + r) * p.N * ELEM +
+                                                      c * SEG + rv * 16) = u;
                     }
                 }
             }
