@@ -32,7 +32,7 @@
 // of the accumulator and the output, about 3000 clocks a tile.  Measured: 2048 x 12288 x
 // 36864 in 525 us (3.5 PFLOP/s, the tensor pipe busy in 86 % of the cycles), 16384 x 4096
 // x 4096 in 163 us; fp32 outputs of 512 x 4096 each, K = 16384, in 180 us (256 tiles for
-// 76 pairs: the fourth round is a third full), of 1536 x 12288, K = 2048, in 227 us.
+// 76 pairs: the fourth wave is a third full), of 1536 x 12288, K = 2048, in 227 us.
 //
 // Every wait is bounded as in the bf16 GEMM: a wait that expires sets a flag
 // that ends the CTA's roles, copies and MMAs in flight are drained (bounded),

@@ -18,7 +18,7 @@
 // row, measured at 917 x 9000.)  The CTAs have 384 threads where those hold the row:
 // they have registers for everything (layer norms, 917 x 9000: 43 us, with 512 threads
 // and spills 53; 2048 x 12288: 104 us as 4 x 384, 111 as 3 x 512).  As many clusters are
-// launched as run at once (46 of 3 and 36 of 4 on 152 SMs): two more made a second round
+// launched as run at once (46 of 3 and 36 of 4 on 152 SMs): two more made a second wave
 // and doubled the time.
 // The column sums of a block of rows go to a partial row, and a second kernel adds the
 // blocks in order; a gate whose rows lie in one group is finished there.  No atomics.
