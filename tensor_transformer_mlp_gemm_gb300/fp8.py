@@ -49,24 +49,25 @@ class _Packed:
         with binding.allocate_on(device, stream):
             self.buf = torch.empty(max(at, 256), dtype=torch.uint8, device=device)
         self.base = self.buf.data_ptr()
+        self._typed = [None, None]                           # the buffer as 8-bit values, as fp32
 
     def pointers(self, cols: bool):
         """(q, scale) pointer arrays by rows or by columns."""
-        q, s = self.base + self.at[2 * cols], self.base + self.at[2 * cols + 1]
-        step = self.steps[cols]
-        return (_array([q + i * self.q for i in range(self.n)]),
-                _array([s + i * step for i in range(self.n)]))
+        return (_strided(self.base + self.at[2 * cols], self.q, self.n),
+                _strided(self.base + self.at[2 * cols + 1], self.steps[cols], self.n))
 
     def view(self, k: int, i: int):
         """Part k of matrix i as a tensor, or None."""
         if self.at[k] is None:
             return None
-        T, C = self.T, self.C
-        if k % 2 == 0:
-            return self.buf.view(DTYPES[self.fmt]).as_strided((T, C), (C, 1), self.at[k] + i * self.q)
+        T, C, scales = self.T, self.C, k % 2
+        typed = self._typed[scales]
+        if typed is None:
+            typed = self._typed[scales] = self.buf.view(torch.float32 if scales else DTYPES[self.fmt])
+        if not scales:
+            return typed.as_strided((T, C), (C, 1), self.at[k] + i * self.q)
         shape = (_up128(C), T) if k == 1 else (_up128(T), C)
-        return self.buf.view(torch.float32).as_strided(
-            shape, (shape[1], 1), (self.at[k] + i * self.steps[k // 2]) // 4)
+        return typed.as_strided(shape, (shape[1], 1), (self.at[k] + i * self.steps[k // 2]) // 4)
 
 
 class Fp8Tokens:
@@ -128,12 +129,16 @@ def _check_like(x: torch.Tensor, shape: tuple, dtype, device, what: str) -> None
                          f"{device}, got {x.dtype} {tuple(x.shape)} on {x.device}")
 
 
-def _array(ptrs):
-    return (ctypes.c_void_p * len(ptrs))(*ptrs)
+_ARRAYS = [ctypes.c_void_p * n for n in range(9)]
 
 
 def _pointers(xs):
-    return _array([x.data_ptr() for x in xs])
+    return _ARRAYS[len(xs)](*[x.data_ptr() for x in xs])
+
+
+def _strided(start: int, step: int, n: int):
+    """The pointers start, start + step, ... (n of them)."""
+    return _ARRAYS[n](*range(start, start + n * step, step)) if step else _ARRAYS[n](*[start] * n)
 
 
 _quant = functools.lru_cache(maxsize=256)(
@@ -195,10 +200,11 @@ def quantize_tokens(X, fmt: str = "e4m3", rows: bool = True, cols: bool = False,
                 _check_like(scale, shape, torch.float32, dev, "out's scales")
                 at[k], at[k + 1] = q.data_ptr(), scale.data_ptr()
 
-    def part(k: int, step: int):
-        return _array([at[k] + j * step for j in range(n)])
-    _quantize(chunks, code, max(T, 1), (part(0, tc * C), part(1, tc * 4)) if rows else None,
-              (part(2, tc * C), part(3, tc // 128 * C * 4)) if cols else None, stream)
+    # token chunk j's part of each output
+    _quantize(chunks, code, max(T, 1),
+              (_strided(at[0], tc * C, n), _strided(at[1], tc * 4, n)) if rows else None,
+              (_strided(at[2], tc * C, n), _strided(at[3], tc // 128 * C * 4, n)) if cols else None,
+              stream)
     return out
 
 
