@@ -37,7 +37,7 @@ namespace {
 using namespace nr;
 
 constexpr int NB_THREADS = 512;          // of a CTA
-constexpr int NB_FEWER = 384;            // of a CTA of some clusters
+constexpr int NB_FEWER = 384;            // where they hold the row
 constexpr int NB_COLS = NB_THREADS * 8;  // columns of one CTA
 constexpr int NB_WARPS = NB_THREADS / 32;
 constexpr int NB_MAX_CLUSTER = 4;
@@ -53,14 +53,15 @@ static_assert(NB_COLS * NB_MAX_CLUSTER >= NR_MAX_H, "a cluster holds the widest 
 int cluster_of(long long h) {
     return h <= NB_COLS ? 1 : h <= 2 * NB_COLS ? 2 : h <= 3 * NB_FEWER * 8 ? 3 : 4;
 }
-int threads_of(long long h) {
-    const int cl = cluster_of(h);
-    return cl > 1 && h <= static_cast<long long>(cl) * NB_FEWER * 8 ? NB_FEWER : NB_THREADS;
-}
 int groups_of(long long h) {
     int g = 1;
     while (g < NB_MAX_GROUPS && h <= NB_COLS / (2 * g)) g *= 2;
     return g;
+}
+int threads_of(long long h) {
+    // (a group is whole warps)
+    const int cl = cluster_of(h), g = groups_of(h);
+    return g <= 4 && h * g <= static_cast<long long>(cl) * NB_FEWER * 8 ? NB_FEWER : NB_THREADS;
 }
 
 // A float into a CTA of the cluster, its four bytes counted on that CTA's mbarrier.
@@ -607,15 +608,18 @@ cudaError_t resident(long long& clusters) {
 
 template <int POST, int PRE>
 cudaError_t launch(const NrBackwardParams& p, cudaStream_t st) {
-    const int cl = cluster_of(p.h);
+    const int cl = cluster_of(p.h), g = groups_of(p.h);
     if (threads_of(p.h) == NB_FEWER) {
         if (cl == 2) return launch_rows<POST, PRE, 2, 1, NB_FEWER>(p, st);
         if (cl == 3) return launch_rows<POST, PRE, 3, 1, NB_FEWER>(p, st);
-        return launch_rows<POST, PRE, 4, 1, NB_FEWER>(p, st);
+        if (cl == 4) return launch_rows<POST, PRE, 4, 1, NB_FEWER>(p, st);
+        if (g == 1) return launch_rows<POST, PRE, 1, 1, NB_FEWER>(p, st);
+        if (g == 2) return launch_rows<POST, PRE, 1, 2, NB_FEWER>(p, st);
+        return launch_rows<POST, PRE, 1, 4, NB_FEWER>(p, st);
     }
     if (cl == 2) return launch_rows<POST, PRE, 2, 1>(p, st);
     if (cl == 4) return launch_rows<POST, PRE, 4, 1>(p, st);
-    switch (groups_of(p.h)) {
+    switch (g) {
         case 1: return launch_rows<POST, PRE, 1, 1>(p, st);
         case 2: return launch_rows<POST, PRE, 1, 2>(p, st);
         case 4: return launch_rows<POST, PRE, 1, 4>(p, st);
