@@ -9,21 +9,23 @@
 // A row has two sums over its columns, one after the other (dZ needs dX's first), and
 // one row at a time spent 2800 clocks on them whatever its width, where 4096 columns
 // are worth 2100 of HBM time.  So a group of threads takes two rows at a time, narrow
-// rows are spread over up to 8 groups of a CTA's 512 threads, and one thread of a group
+// rows are spread over up to 6 groups of a CTA's threads, and one thread of a group
 // keeps bulk copies of its next rows under way into a ring in shared memory.
 // Rows of more than 4096 columns take a cluster of 2 to 4 CTAs side by side, whose row
 // sums meet in each other's shared memory: each warp sends its part to every CTA,
 // counted on that CTA's mbarrier, and every warp adds all parts in the same order.  (A
 // cluster barrier instead waits for the row's own loads and stores too: 6600 clocks a
-// row, measured at 917 x 9000.)  The CTAs have 384 threads where those hold the row:
-// they have registers for everything (layer norms, 917 x 9000: 43 us, with 512 threads
-// and spills 53; 2048 x 12288: 104 us as 4 x 384, 111 as 3 x 512).  As many clusters are
-// launched as run at once (46 of 3 and 36 of 4 on 152 SMs): two more made a second wave
-// and doubled the time.
+// row, measured at 917 x 9000.)  As many clusters are launched as run at once (46 of 3
+// and 36 of 4 on 152 SMs): two more made a second wave and doubled the time.
+// A CTA has 384 threads where those hold the row or rows: they have registers for
+// everything.  With 512 instead, rms and layer norms at 16384 x 2560 took 131 and 166 us,
+// now 115 and 136; 16384 x 1536 90 and 115, now 70 and 80; 16384 x 1024, as 3 groups
+// instead of 4, 55 and 71, now 51 and 59; 917 x 9000 layer 53, now 43; 2048 x 12288 layer
+// 111 as 3 x 512, 105 as 4 x 384.
 // The column sums of a block of rows go to a partial row, and a second kernel adds the
 // blocks in order; a gate whose rows lie in one group is finished there.  No atomics.
 // Measured, rms norms and 8 gates, cold caches, launches included: 16384 x 4096 in 139 us
-// (5.8 TB/s), layer norms 184; 8192 x 8192 168; 2048 x 12288 82; 16384 x 1024 55.
+// (5.8 TB/s), layer norms 184; 8192 x 8192 168; 2048 x 12288 82; 16384 x 1024 51.
 #include <algorithm>
 
 #include "gemm_params.h"
@@ -41,27 +43,27 @@ constexpr int NB_FEWER = 384;            // where they hold the row
 constexpr int NB_COLS = NB_THREADS * 8;  // columns of one CTA
 constexpr int NB_WARPS = NB_THREADS / 32;
 constexpr int NB_MAX_CLUSTER = 4;
-constexpr int NB_MAX_GROUPS = 8;
+constexpr int NB_MAX_GROUPS = 6;
 constexpr int NB_ROWS = 2;               // rows a group takes at a time
 constexpr int NB_ARRAYS = 5;             // dOut, dXn, Out, Z, gate
 constexpr int NB_STAGES = 2;             // row pairs in the ring
 constexpr int NB_RING = NB_STAGES * NB_ROWS * NB_ARRAYS * NB_COLS * 2;
 static_assert(NB_COLS * NB_MAX_CLUSTER >= NR_MAX_H, "a cluster holds the widest row");
 
-// CTAs side by side for a row, their threads, and groups of a CTA's threads that take rows
-// of their own.
+// CTAs side by side for a row, groups of a CTA's threads that take rows of their own, and
+// the CTA's threads: 384 unless only 512 hold one or two rows.
 int cluster_of(long long h) {
     return h <= NB_COLS ? 1 : h <= 2 * NB_COLS ? 2 : h <= 3 * NB_FEWER * 8 ? 3 : 4;
 }
 int groups_of(long long h) {
-    int g = 1;
-    while (g < NB_MAX_GROUPS && h <= NB_COLS / (2 * g)) g *= 2;
-    return g;
+    if (h > NB_COLS / 2) return 1;
+    for (int g : {6, 4, 3})
+        if (h * g <= NB_FEWER * 8) return g;
+    return 2;
 }
 int threads_of(long long h) {
-    // (a group is whole warps)
-    const int cl = cluster_of(h), g = groups_of(h);
-    return g <= 4 && h * g <= static_cast<long long>(cl) * NB_FEWER * 8 ? NB_FEWER : NB_THREADS;
+    return h * groups_of(h) <= static_cast<long long>(cluster_of(h)) * NB_FEWER * 8 ? NB_FEWER
+                                                                                    : NB_THREADS;
 }
 
 // A float into a CTA of the cluster, its four bytes counted on that CTA's mbarrier.
@@ -615,16 +617,13 @@ cudaError_t launch(const NrBackwardParams& p, cudaStream_t st) {
         if (cl == 4) return launch_rows<POST, PRE, 4, 1, NB_FEWER>(p, st);
         if (g == 1) return launch_rows<POST, PRE, 1, 1, NB_FEWER>(p, st);
         if (g == 2) return launch_rows<POST, PRE, 1, 2, NB_FEWER>(p, st);
-        return launch_rows<POST, PRE, 1, 4, NB_FEWER>(p, st);
+        if (g == 3) return launch_rows<POST, PRE, 1, 3, NB_FEWER>(p, st);
+        if (g == 4) return launch_rows<POST, PRE, 1, 4, NB_FEWER>(p, st);
+        return launch_rows<POST, PRE, 1, 6, NB_FEWER>(p, st);
     }
     if (cl == 2) return launch_rows<POST, PRE, 2, 1>(p, st);
     if (cl == 4) return launch_rows<POST, PRE, 4, 1>(p, st);
-    switch (g) {
-        case 1: return launch_rows<POST, PRE, 1, 1>(p, st);
-        case 2: return launch_rows<POST, PRE, 1, 2>(p, st);
-        case 4: return launch_rows<POST, PRE, 1, 4>(p, st);
-        default: return launch_rows<POST, PRE, 1, 8>(p, st);
-    }
+    return g == 1 ? launch_rows<POST, PRE, 1, 1>(p, st) : launch_rows<POST, PRE, 1, 2>(p, st);
 }
 
 template <int POST>
