@@ -25,7 +25,8 @@
 // The column sums of a block of rows go to a partial row, and a second kernel adds the
 // blocks in order; a gate whose rows lie in one group is finished there.  No atomics.
 // Measured, rms norms and 8 gates, cold caches, launches included: 16384 x 4096 in 139 us
-// (5.8 TB/s), layer norms 184; 8192 x 8192 168; 2048 x 12288 82; 16384 x 1024 51.
+// (5.8 TB/s), layer norms 168; 8192 x 8192 168 and 199; 2048 x 12288 82; 16384 x 2048 85;
+// 16384 x 1024 51.
 #include <algorithm>
 
 #include "gemm_params.h"
@@ -173,6 +174,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr bool POST_LAYER = POST == NR_POST_LAYER, PRE_LAYER = PRE == NR_PRE_LAYER;
     constexpr int R = NB_ROWS, GT = THREADS / G, WG = GT / 32, ROW = GT * 16;  // a row's bytes in the ring
     static_assert(CL == 1 || G == 1, "wide rows take whole CTAs");
+    // Z and the gate are read from the ring when they are needed, not held from the start:
+    // that spilled (layer norms, 16384 x 4096 182 us instead of 168; rms norms, 16384 x
+    // 2048 94 instead of 85).  Where they fit they are held, and the stage is free sooner
+    // (rms norms, 16384 x 4096 139 us, not 147).
+    constexpr bool HOLD = THREADS == NB_THREADS && G == 1 && !POST_LAYER && !PRE_LAYER;
     extern __shared__ __align__(128) uint8_t ring_all[];
     __shared__ Shared sm;
     const int rank = CL == 1 ? 0 : static_cast<int>(ptx::cluster_ctarank());
@@ -278,18 +284,37 @@ __global__ void __launch_bounds__(THREADS, 1)
         wait_on(ptx::smem_u32(&sm.ring_bar[group][stage]), ring_phase, waits);
         uint4 q_dout[R], q_dxn[R], q_out[R], q_z[R], q_gate[R];
         float m1[R], r1[R], m2[R], r2[R];
+        const uint8_t* src = ring + stage * (R * NB_ARRAYS * ROW) + tid * 16;
+        auto get = [&](int i, int a) {
+            return in && row + i < last
+                       ? *reinterpret_cast<const uint4*>(src + (i * NB_ARRAYS + a) * ROW)
+                       : zero4();
+        };
+        // every thread of the group has read this stage
+        auto release = [&] {
+            if (tid == 0 && row + NB_STAGES * R < last) copy_rows(row + NB_STAGES * R, stage);
+            if (++stage == NB_STAGES) {
+                stage = 0;
+                ring_phase ^= 1u;
+            }
+        };
+        auto group_sync = [&] {
+            if constexpr (CL > 1 || WG > 1)
+                asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(GT) : "memory");
+            else
+                __syncwarp();
+        };
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const bool ok = in && row + i < last;
-            const uint8_t* src = ring + (stage * R + i) * (NB_ARRAYS * ROW) + tid * 16;
-            auto get = [&](int a) { return ok ? *reinterpret_cast<const uint4*>(src + a * ROW) : zero4(); };
-            q_dout[i] = dout ? get(0) : zero4();
+            q_dout[i] = dout ? get(i, 0) : zero4();
             if (BEFORE) {
-                q_dxn[i] = get(1);
-                q_out[i] = get(2);
+                q_dxn[i] = get(i, 1);
+                q_out[i] = get(i, 2);
             }
-            if (Z) q_z[i] = get(3);
-            q_gate[i] = gate ? get(4) : zero4();
+            if (Z && HOLD) {
+                q_z[i] = get(i, 3);
+                q_gate[i] = gate ? get(i, 4) : zero4();
+            }
             // (a row that is not there has statistics 0: nothing comes of it)
             m1[i] = POST_LAYER ? __shfl_sync(0xffffffffu, stat, 4 * i) : 0.0f;
             r1[i] = POST_NORM ? __shfl_sync(0xffffffffu, stat, 4 * i + 1) : 0.0f;
@@ -345,16 +370,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
 #pragma unroll
             for (int i = 0; i < R; ++i) unpack(q_dout[i], g[i]);
-            if constexpr (CL > 1 || WG > 1)
-                asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(GT) : "memory");
-            else
-                __syncwarp();
         }
-        // every thread of the group has read this stage
-        if (tid == 0 && row + NB_STAGES * R < last) copy_rows(row + NB_STAGES * R, stage);
-        if (++stage == NB_STAGES) {
-            stage = 0;
-            ring_phase ^= 1u;
+        if constexpr (!Z || HOLD) {
+            if constexpr (!BEFORE) group_sync();  // (else its sums met in between)
+            release();
         }
         uint32_t k[R];
         long long off[R];
@@ -379,6 +398,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 float2 z[4], t[4];
+                if (!HOLD) {
+                    q_z[i] = get(i, 3);
+                    q_gate[i] = gate ? get(i, 4) : zero4();
+                }
                 unpack(q_z[i], z);
                 unpack(q_gate[i], t);
                 const float2 m = both(-m1[i]), r = both(r1[i]);
@@ -423,6 +446,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if constexpr (POST_NORM) {
                 row_sums<CL, WG, N>(sums, sm, buf, phase, group, rank, waits);
+                if (!HOLD) release();
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     float2 z[4];
@@ -437,6 +461,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         g[i][e] = __fmul2_rn(r, __ffma2_rn(hat, mv, wd));
                     }
                 }
+            } else if constexpr (!HOLD) {
+                group_sync();
+                release();
             }
 #pragma unroll
             for (int i = 0; i < R; ++i)
