@@ -91,9 +91,12 @@ TPMLP_API tpmlp_status tpmlp_norm_forward(const tpmlp_norm_params* params, const
     const bool z = Z != nullptr, pre = d.pre != TPMLP_NORM_NONE;
     // without Z there is only the norm before
     if (!z && (d.post != TPMLP_NORM_NONE || !pre)) return TPMLP_ERR_INVALID_ARG;
-    if ((gate != nullptr) != (d.gate_rows > 0) || (gate && !z)) return TPMLP_ERR_INVALID_ARG;
-    if ((Xq != nullptr) != (Xs != nullptr)) return TPMLP_ERR_INVALID_ARG;
-    if (pre != (Xn != nullptr || Xq != nullptr)) return TPMLP_ERR_INVALID_ARG;
+    // (arrays of no tokens may be null: whether they are there is not looked at)
+    if (d.tokens > 0) {
+        if ((gate != nullptr) != (d.gate_rows > 0) || (gate && !z)) return TPMLP_ERR_INVALID_ARG;
+        if ((Xq != nullptr) != (Xs != nullptr)) return TPMLP_ERR_INVALID_ARG;
+        if (pre != (Xn != nullptr || Xq != nullptr)) return TPMLP_ERR_INVALID_ARG;
+    }
     if (Xq && d.q_format != TPMLP_FP8_E4M3 && d.q_format != TPMLP_FP8_E5M2) return TPMLP_ERR_INVALID_ARG;
     if (Xq && d.hidden % 16 != 0) return TPMLP_ERR_UNSUPPORTED;
     const int n = d.seq_chunks;
@@ -105,12 +108,14 @@ TPMLP_API tpmlp_status tpmlp_norm_forward(const tpmlp_norm_params* params, const
     TPMLP_TRY(check_weight(post_beta, d.post == TPMLP_NORM_LAYER));
     TPMLP_TRY(check_weight(pre_gamma, pre));
     TPMLP_TRY(check_weight(pre_beta, d.pre == TPMLP_NORM_LAYER));
-    if (gate) TPMLP_TRY(check_ptr(gate));
-    if (Xq) {
-        TPMLP_TRY(check_ptr(Xq));
-        TPMLP_TRY(check_scale(Xs));
+    if (d.tokens > 0) {
+        if (gate) TPMLP_TRY(check_ptr(gate));
+        if (Xq) {
+            TPMLP_TRY(check_ptr(Xq));
+            TPMLP_TRY(check_scale(Xs));
+        }
+        if (stats) TPMLP_TRY(check_scale(stats));
     }
-    if (stats) TPMLP_TRY(check_scale(stats));
     DeviceInfo* dev = nullptr;
     TPMLP_TRY(device_info(&dev));
     if (d.tokens == 0) return TPMLP_OK;
@@ -157,7 +162,8 @@ TPMLP_API tpmlp_status tpmlp_norm_backward(const tpmlp_norm_params* params, cons
     const bool z = Z != nullptr, pre = d.pre != TPMLP_NORM_NONE;
     const bool post = d.post != TPMLP_NORM_NONE;
     if (!z && (post || !pre)) return TPMLP_ERR_INVALID_ARG;
-    if ((gate != nullptr) != (d.gate_rows > 0) || (gate && !z)) return TPMLP_ERR_INVALID_ARG;
+    if (d.tokens > 0 && ((gate != nullptr) != (d.gate_rows > 0) || (gate && !z)))
+        return TPMLP_ERR_INVALID_ARG;
     if (!pre && !dOut) return TPMLP_ERR_INVALID_ARG;
     const int n = d.seq_chunks;
     TPMLP_TRY(check_chunks(dOut, dOut != nullptr, d.tokens, n));
