@@ -329,8 +329,9 @@ tpmlp_status tpmlp_sp_backward(const tpmlp_dims* dims, const tpmlp_sp_params* sp
  *   columns   groups of 128 along a column: s fp32 [ceil(R/128), C]
  *   weight    blocks of 128 x 128:          s fp32 [ceil(R/128), ceil(C/128)]
  * Conventions, chunking, errors and workspace rules as for the bf16 linear
- * layers, with features and shards multiples of 16 (else
- * TPMLP_ERR_UNSUPPORTED); scales (s) may start at any multiple of 4 bytes. */
+ * layers, with features and shards multiples of 16 and no more than 2^31 - 256
+ * tokens or features (else TPMLP_ERR_UNSUPPORTED); scales (s) may start at any
+ * multiple of 4 bytes. */
 typedef enum {
     TPMLP_FP8_E4M3 = 0, /* 4 exponent bits, 3 mantissa bits, no infinities */
     TPMLP_FP8_E5M2 = 1  /* 5 exponent bits, 2 mantissa bits */

@@ -263,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             int m0, n0;
             decode(p, f.tile, f.g, m0, n0);
             f.m = m0 + rank * 128 + lane + 32 * q;
-            f.n = F32 ? n0 + lane + 64 * q : n0 + 128 * lane;
+            f.n = F32 ? n0 + lane + 64 * q : n0 + 128 * (lane & 1);
             f.seg = f.kb = 0;
             start_segment();
         };

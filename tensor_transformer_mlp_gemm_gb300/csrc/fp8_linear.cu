@@ -54,7 +54,8 @@ tpmlp_status check_fp8_dims(const tpmlp_linear_dims* d, Split k) {
     if (split % d->t != 0 || d->tokens % d->seq_chunks != 0) return TPMLP_ERR_INVALID_ARG;
     if (d->t > kMaxShards || d->seq_chunks > kMaxShards) return TPMLP_ERR_UNSUPPORTED;
     if ((split / d->t) % 16 != 0 || other % 16 != 0) return TPMLP_ERR_UNSUPPORTED;
-    const int64_t lim = (int64_t(1) << 31) - 1;
+    // the products round each up to tiles of 256 in 32 bits
+    const int64_t lim = (int64_t(1) << 31) - 256;
     if (d->tokens > lim || d->in_features > lim || d->out_features > lim)
         return TPMLP_ERR_UNSUPPORTED;
     if (d->seq_chunks > 1 && (d->tokens / d->seq_chunks) % FP8_GROUP != 0)
