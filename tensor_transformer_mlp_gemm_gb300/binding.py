@@ -46,6 +46,7 @@ EXPORTED = (
     "tpmlp_fp8_column_linear_forward", "tpmlp_fp8_column_linear_backward",
     "tpmlp_fp8_row_linear_forward", "tpmlp_fp8_row_linear_backward",
     "tpmlp_norm_workspace_bytes", "tpmlp_norm_forward", "tpmlp_norm_backward",
+    "tpmlp_selftest_stall_loads",
 )
 
 
@@ -130,6 +131,8 @@ _lib.tpmlp_set_head_prefetch.restype = ctypes.c_int
 _lib.tpmlp_set_head_prefetch.argtypes = [ctypes.c_int]
 _lib.tpmlp_set_wait_timeout_ns.restype = ctypes.c_int
 _lib.tpmlp_set_wait_timeout_ns.argtypes = [ctypes.c_uint64]
+_lib.tpmlp_selftest_stall_loads.restype = ctypes.c_int
+_lib.tpmlp_selftest_stall_loads.argtypes = [ctypes.c_int]
 _lib.tpmlp_selftest_stalled_gemm.restype = ctypes.c_int
 _lib.tpmlp_selftest_stalled_gemm.argtypes = [_vp, _vp, _vp, ctypes.c_uint64, _vp]
 _lib.tpmlp_profile_begin.restype = ctypes.c_int
@@ -385,6 +388,10 @@ def tpmlp_selftest_map_cache() -> dict:
 
 def tpmlp_set_wait_timeout_ns(ns: int) -> None:
     _check(_lib.tpmlp_set_wait_timeout_ns(int(ns)), "tpmlp_set_wait_timeout_ns")
+
+
+def tpmlp_selftest_stall_loads(copies: int) -> None:
+    _check(_lib.tpmlp_selftest_stall_loads(int(copies)), "tpmlp_selftest_stall_loads")
 
 
 def tpmlp_selftest_stalled_gemm(a, b, c, timeout_ns: int, stream=None) -> int:

@@ -47,6 +47,8 @@ struct Fp8GemmParams {
     uint32_t ab_format;                // instruction descriptor bits of the operands' 8-bit formats
     unsigned int* err;                 // the device error word and the limit of any one wait
     unsigned long long timeout_ns;
+    int stall;                         // failure-detection self-test: the loader of a cluster's last
+                                       // CTA issues this many of its copies; < 0: all
 };
 
 // The whole product on CTA pairs with 256 x 256 output tiles; A's maps have boxes of

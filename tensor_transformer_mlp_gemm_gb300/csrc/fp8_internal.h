@@ -21,6 +21,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 extern EncodeTiledFn g_encode;
 extern MapCache g_maps;
 extern unsigned long long g_timeout_ns;
+extern thread_local int g_stall;  // failure-detection self-test (tpmlp_selftest_stall_loads)
 
 // Scales are read and written one at a time: a part of a larger array may start anywhere.
 inline tpmlp_status check_scale(const void* p) {

@@ -172,6 +172,7 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int kind, cuda
     p.ab_format = (static_cast<uint32_t>(fa) << 7) | (static_cast<uint32_t>(fb) << 10);
     p.err = dev->err;
     p.timeout_ns = g_timeout_ns;
+    p.stall = g_stall;
     TPMLP_CUDA(timed(kind, 1, st, [&] {
         return few ? launch_fp8_small(p, few, st) : launch_fp8_gemm(p, d.out_kind, st);
     }));

@@ -129,12 +129,14 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
     }
 }
 
-// Teardown wait: ignores the abort flag, still bounded.
+// Teardown wait for what this CTA has under way itself: ignores the abort flag.  Copies and
+// MMAs end by themselves, so its limit is not the caller's where that is short.
+constexpr unsigned long long DRAIN_NS = 1000000000ULL;
 __device__ __forceinline__ bool drain(uint32_t bar, uint32_t parity, unsigned long long timeout_ns,
                                       unsigned* err) {
     const uint64_t t0 = ptx::globaltimer_ns();
     while (!ptx::mbar_try_wait(bar, parity)) {
-        if (ptx::globaltimer_ns() - t0 > timeout_ns) {
+        if (ptx::globaltimer_ns() - t0 > max(timeout_ns, DRAIN_NS)) {
             atomicOr(err, ERR_DRAIN);
             return false;
         }

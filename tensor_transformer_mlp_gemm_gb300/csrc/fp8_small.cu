@@ -89,6 +89,9 @@ __global__ void __launch_bounds__(S_THREADS, Small<TN, PER_SM>::kPerSm)
     const uint32_t bar_done = bar0 + 16 * NST; // all MMAs
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 16 * NST + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_area + 16 * NST + 12);
+    // K blocks copied, and those with each warp's scales (a role that has given up says so)
+    volatile int* copied = abort_flag + 1;
+    volatile int* scaled = abort_flag + 2;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(blockIdx.x % splits);
@@ -104,6 +107,7 @@ __global__ void __launch_bounds__(S_THREADS, Small<TN, PER_SM>::kPerSm)
         }
         ptx::mbar_init(bar_done, 1);
         *abort_flag = 0;
+        scaled[0] = scaled[1] = scaled[2] = scaled[3] = 0x7FFFFFFF;
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
@@ -128,13 +132,11 @@ __global__ void __launch_bounds__(S_THREADS, Small<TN, PER_SM>::kPerSm)
             int stage = 0;
             uint32_t phase = 0;
             int s = first / kblocks, kb = first - s * kblocks, fills = 0;
-            bool ok = true;
-            for (int k = first; k < last; ++k) {
+            const int stop = p.stall >= 0 && rank == splits - 1 ? min(last, first + p.stall) : last;
+            for (int k = first; k < stop; ++k) {
                 if (!wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.timeout_ns, p.err,
-                          ERR_PRODUCER)) {
-                    ok = false;
+                          ERR_PRODUCER))
                     break;
-                }
                 const uint32_t sw = base + stage * C::kStageBytes, full = bar_full + 8 * stage;
                 const int k0 = kb * F8_BK;
                 ptx::mbar_arrive_expect_tx(full, C::kStageBytes);
@@ -151,13 +153,7 @@ __global__ void __launch_bounds__(S_THREADS, Small<TN, PER_SM>::kPerSm)
                     phase ^= 1u;
                 }
             }
-            if (!ok) {
-                // copies still in flight land before this CTA goes on
-                for (int f = (fills > NST ? fills - NST : 0); f < fills; ++f)
-                    if (!drain(bar_full + 8 * (f % NST), static_cast<uint32_t>((f / NST) & 1),
-                               p.timeout_ns, p.err))
-                        break;
-            }
+            *copied = fills;
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -225,7 +221,10 @@ __global__ void __launch_bounds__(S_THREADS, Small<TN, PER_SM>::kPerSm)
                     if (k0 + u + S_AHEAD < last) fetch(v[u]);
                     ok = __all_sync(0xffffffffu, wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag,
                                                       p.timeout_ns, p.err, ERR_PRODUCER));
-                    if (!ok) break;
+                    if (!ok) {
+                        if (lane == 0) scaled[q] = k0 + u - first;
+                        break;
+                    }
                     ptx::tc_fence_after();
                     const uint32_t t = lanes + C::kSums + stage * C::kSlot;
                     store_cols4(t, w);
@@ -249,27 +248,41 @@ __global__ void __launch_bounds__(S_THREADS, Small<TN, PER_SM>::kPerSm)
             }
         }
         // this CTA's sums, feature by feature of each token, where the operands were
-        __all_sync(0xffffffffu, wait(bar_done, 0, abort_flag, p.timeout_ns, p.err, ERR_EPILOGUE));
-        ptx::tc_fence_after();
-        float* sums = reinterpret_cast<float*>(gbase);
-        const int f = q * 32 + lane;
+        // (not of a CTA that has given up: copies and MMAs may still be under way there)
+        if (__all_sync(0xffffffffu, wait(bar_done, 0, abort_flag, p.timeout_ns, p.err, ERR_EPILOGUE))) {
+            ptx::tc_fence_after();
+            float* sums = reinterpret_cast<float*>(gbase);
+            const int f = q * 32 + lane;
 #pragma unroll
-        for (int c = 0; c < TN / 16; ++c) {
-            float x[16];
-            load_cols16(lanes + c * 16, x);
-            ptx::tmem_ld_wait();
+            for (int c = 0; c < TN / 16; ++c) {
+                float x[16];
+                load_cols16(lanes + c * 16, x);
+                ptx::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                asm volatile("" : "+f"(x[i]));  // used after the wait
-                sums[(c * 16 + i) * 128 + f] = x[i];
+                for (int i = 0; i < 16; ++i) {
+                    asm volatile("" : "+f"(x[i]));  // used after the wait
+                    sums[(c * 16 + i) * 128 + f] = x[i];
+                }
             }
+            ptx::tc_fence_before();
         }
-        ptx::tc_fence_before();
     }
 
     // every CTA's sums are in place
     __syncwarp();
     ptx::cluster_sync();
+    if (threadIdx.x == 0 && *abort_flag) {
+        // What this CTA has under way ends before it does.  A stage counts the scale warps
+        // too: those that gave up before they came to it are stood in for.
+        const int n = *copied;
+        for (int k = max(0, n - NST); k < n; ++k) {
+            const uint32_t full = bar_full + 8 * (k % NST);
+            for (int w = 0; w < S_WARPS; ++w)
+                if (scaled[w] <= k) arrive_relaxed(full);
+            drain(full, static_cast<uint32_t>((k / NST) & 1), p.timeout_ns, p.err);
+        }
+        drain(bar_done, 0, p.timeout_ns, p.err);
+    }
     {
         // tokens rank, rank + splits, ... of the tile: a warp a token, four features a lane
         const int col = f0 + lane * 4;

@@ -53,6 +53,7 @@ constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
 unsigned long long g_timeout_ns = 2000000000ULL;
+thread_local int g_stall = -1;
 int g_split_min_kblocks = DEFAULT_SPLIT_MIN_KBLOCKS;
 int g_head_prefetch = 0;
 int g_wide_tiles = WIDE_TILES_DEEP_K;
@@ -838,6 +839,12 @@ TPMLP_API tpmlp_status tpmlp_sync_check(void* stream) {
         if (cudaMemset(dev->err, 0, sizeof(word)) != cudaSuccess) return TPMLP_ERR_CUDA;
         return TPMLP_ERR_TIMEOUT;
     }
+    return TPMLP_OK;
+}
+
+TPMLP_API tpmlp_status tpmlp_selftest_stall_loads(int copies) {
+    if (copies < -1) return TPMLP_ERR_INVALID_ARG;
+    g_stall = copies;
     return TPMLP_OK;
 }
 

@@ -1,0 +1,63 @@
+"""Waits that run out: a loader that stops (on purpose, some copies into its work) ends the
+kernel at the limit with a status, nothing of it is left under way, and the next call is
+right.  A teardown that waited for what never comes would take its own limit of a second."""
+import contextlib
+import time
+
+import pytest
+import torch
+
+import test_gpu_fp8 as f8
+from tensor_transformer_mlp_gemm_gb300.inputs import custom_linear
+
+pytestmark = pytest.mark.gpu
+
+LIMIT_S = 0.03
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup(gpu):
+    from tensor_transformer_mlp_gemm_gb300.build import build
+    build()
+    yield
+
+
+@contextlib.contextmanager
+def stalled(copies):
+    from tensor_transformer_mlp_gemm_gb300 import binding
+    binding.tpmlp_set_wait_timeout_ns(int(LIMIT_S * 1e9))
+    binding.tpmlp_selftest_stall_loads(copies)
+    try:
+        yield
+    finally:
+        binding.tpmlp_selftest_stall_loads(-1)
+        binding.tpmlp_set_wait_timeout_ns(2_000_000_000)
+
+
+def gives_up(call, kernels=1):
+    """call runs into the limit in `kernels` launches, each ending soon after."""
+    from tensor_transformer_mlp_gemm_gb300 import binding
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    call()
+    status = binding.tpmlp_sync_check()
+    took = time.perf_counter() - t0
+    assert status == binding.TPMLP_ERR_TIMEOUT
+    # each wait of a kernel at most twice, one after the other
+    assert LIMIT_S * 0.9 < took < kernels * LIMIT_S * 4 + 0.3, took
+
+
+@pytest.mark.parametrize("copies", [0, 1, 3, 7])
+@pytest.mark.parametrize("split,T,din,dout,t", [
+    # (8 K blocks at least for each CTA)
+    ("column", 1, 16384, 1040, 1), ("row", 20, 8192, 512, 2), ("column", 48, 8192, 4096, 2),
+    ("column", 100, 8192, 4096, 1), ("column", 100, 8192, 12288, 1), ("column", 256, 8192, 512, 1)])
+def test_few_tokens(split, T, din, dout, t, copies):
+    w = custom_linear(T, din, dout, t, split)
+    lay, X, dY = f8._layer(w, 5)
+    x = lay.quantize(X)
+    with stalled(copies):
+        gives_up(lambda: lay.forward(x))
+    lay.forward(x)
+    f8._sync()
+    f8._check_forward(lay, x)
