@@ -34,9 +34,11 @@
 // x 4096 in 163 us; fp32 outputs of 512 x 4096 each, K = 16384, in 180 us (256 tiles for
 // 76 pairs: the fourth wave is a third full), of 1536 x 12288, K = 2048, in 227 us.
 //
-// Every wait is bounded as in the bf16 GEMM: a wait that expires sets a flag
-// that ends the CTA's roles, copies and MMAs in flight are drained (bounded),
-// tensor memory is freed, and the error word tells the host.
+// Every wait is bounded as in the bf16 GEMM: a wait that expires sets a flag that ends
+// the roles of both CTAs, copies and MMAs in flight are drained (bounded), tensor memory
+// is freed, and the error word tells the host.  For that each role leaves behind how far
+// it came: what counts on a stage's barrier is stood in for where a role stopped before
+// it, so that the barrier's phase says when the copies have landed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -85,6 +87,43 @@ __device__ __forceinline__ int pick(int part, int g, int s) {
     return part == F8_GROUP ? g : part == F8_KSEG ? s : 0;
 }
 
+// How many K blocks a role that gave up has done (one that did not: all), 64-bit counts in
+// shared memory: in the even CTA those copied and those with scales, by it and by the odd
+// one; in both those issued.
+constexpr int F_BLOCKS_DONE = 16 * F_STAGES + 32;  // from the barriers on
+constexpr int F_COPIED = 0, F_SCALED = 2, F_ISSUED = 4, F_COUNTS = 5;
+
+// After a wait has expired and every role has left its loop: what a CTA has under way ends.
+// (Not inlined: its values would take registers from the roles.)
+__device__ __noinline__ void settle(uint32_t bar0, int nk, int tiles, unsigned long long timeout_ns,
+                                    unsigned* err) {
+    constexpr int NST = F_STAGES;
+    const uint32_t bar_full = bar0, bar_empty = bar0 + 8 * NST, bar_done = bar0 + 16 * NST;
+    const long long* counts = static_cast<const long long*>(__cvta_shared_to_generic(bar0 + F_BLOCKS_DONE));
+    auto blocks = [&](int i) { return min(counts[i], static_cast<long long>(tiles) * nk); };
+    if (ptx::cluster_ctarank() == 0) {
+        // the copies of both CTAs
+        const long long even = blocks(F_COPIED), odd = blocks(F_COPIED + 1), n = max(even, odd);
+        for (long long k = max(0LL, n - NST); k < n; ++k) {
+            const uint32_t full = bar_full + 8 * static_cast<uint32_t>(k % NST);
+            if (k >= even)
+                ptx::mbar_arrive_expect_tx(full, F_STAGE_BYTES);  // the odd CTA's only
+            else if (k >= odd)
+                complete_tx(full, F_STAGE_BYTES);  // which will not come
+            for (int r = 0; r < 2; ++r)
+                for (int w = 0; w < F_SCALE_WARPS; ++w)
+                    if (k >= blocks(F_SCALED + r)) arrive_relaxed(full);
+            drain(full, static_cast<uint32_t>((k / NST) & 1), timeout_ns, err);
+        }
+    }
+    // the MMAs' arrivals on this CTA (the MMAs themselves have ended)
+    const long long n = blocks(F_ISSUED), whole = n / nk;
+    for (long long k = max(0LL, n - NST); k < n; ++k)
+        drain(bar_empty + 8 * static_cast<uint32_t>(k % NST), static_cast<uint32_t>((k / NST) & 1),
+              timeout_ns, err);
+    if (whole > 0) drain(bar_done, static_cast<uint32_t>((whole - 1) & 1), timeout_ns, err);
+}
+
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
@@ -108,6 +147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     const uint32_t bar_drain = bar_free + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 16 * NST + 24);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_area + 16 * NST + 28);
+    const uint32_t blocks_done = bar0 + F_BLOCKS_DONE;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(ptx::cluster_ctarank());
@@ -122,6 +162,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         ptx::mbar_init(bar_free, 2 * F_OUT_WARPS);
         ptx::mbar_init(bar_drain, 1);
         *abort_flag = 0;
+        for (int i = 0; i < F_COUNTS; ++i)
+            reinterpret_cast<long long*>(bar_area + F_BLOCKS_DONE)[i] = 0x7FFFFFFFFFFFFFFFLL;
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
@@ -138,6 +180,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
 
     const int kblocks = (p.K + F8_BK - 1) / F8_BK;
     const int nk = kblocks * p.ksegs;
+    // a wait of this kernel; who gives up takes the other CTA along
+    auto wait_for = [&](uint32_t bar, uint32_t parity, unsigned code) {
+        if (wait(bar, parity, abort_flag, p.timeout_ns, p.err, code)) return true;
+        store_cluster(ptx::mapa_shared(bar0 + 16 * NST + 28, static_cast<uint32_t>(rank ^ 1)), 1);
+        return false;
+    };
 
     if (warp < 4) {
         reg_dec<F_FEW_REGS>();
@@ -157,8 +205,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     const CUtensorMap* am = p.a_map + pick(p.a_part, g, s);
                     const CUtensorMap* bm = p.b_map + pick(p.b_part, g, s);
                     for (int kb = 0; kb < kblocks; ++kb) {
-                        if (!wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.timeout_ns, p.err,
-                                  ERR_PRODUCER)) {
+                        if ((fills == p.stall && rank == 1) ||
+                            !wait_for(bar_empty + 8 * stage, phase ^ 1u, ERR_PRODUCER)) {
                             ok = false;
                             break;
                         }
@@ -177,23 +225,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     }
                 }
             }
-            if (ok) {
-                // no release of a stage may arrive after this CTA has left
-                for (int i = 0; i < NST; ++i) {
-                    if (!drain(bar_empty + 8 * stage, phase ^ 1u, p.timeout_ns, p.err)) break;
-                    if (++stage == NST) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            } else if (rank == 0) {
-                for (long long f = (fills > NST ? fills - NST : 0); f < fills; ++f) {
-                    const int st = static_cast<int>(f % NST);
-                    if (!drain(bar_full + 8 * st, static_cast<uint32_t>((f / NST) & 1), p.timeout_ns,
-                               p.err))
-                        break;
+            // no release of a stage may arrive after this CTA has left
+            for (int i = 0; ok && i < NST; ++i) {
+                ok = wait_for(bar_empty + 8 * stage, phase ^ 1u, ERR_PRODUCER);
+                if (++stage == NST) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
+            if (!ok) store_cluster64(ptx::mapa_shared(blocks_done + 8 * (F_COPIED + rank), 0), fills);
         } else if (warp == 1 && rank == 0) {
             // ---------------- MMA issuer ----------------
             // The whole warp walks the loop and one lane issues, so the descriptors
@@ -204,14 +244,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             const uint32_t ka = (p.a_mn ? 4096 : 32) >> 4, kb = (p.b_mn ? 4096 : 32) >> 4;
             int stage = 0;
             uint32_t phase = 0, tiles = 0;
+            long long issued = 0;
             bool ok = true;
             for (int tile = cluster; ok && tile < p.total_tiles; tile += nclusters, ++tiles) {
-                ok = __all_sync(0xffffffffu, wait(bar_free, (tiles & 1) ^ 1u, abort_flag, p.timeout_ns,
-                                                  p.err, ERR_MMA));
+                ok = __all_sync(0xffffffffu, wait_for(bar_free, (tiles & 1) ^ 1u, ERR_MMA));
                 if (!ok) break;
                 for (int kk = 0; kk < nk; ++kk) {
-                    ok = __all_sync(0xffffffffu, wait(bar_full + 8 * stage, phase, abort_flag,
-                                                      p.timeout_ns, p.err, ERR_MMA));
+                    ok = __all_sync(0xffffffffu, wait_for(bar_full + 8 * stage, phase, ERR_MMA));
                     if (!ok) break;
                     ptx::tc_fence_after();
                     const uint32_t step = stage * (F_STAGE_BYTES >> 4);
@@ -225,6 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                         if (kk + 1 == nk) ptx::mma_commit_pair_multicast(bar_done, 0x3);
                     }
                     __syncwarp();
+                    ++issued;
                     if (++stage == NST) {
                         stage = 0;
                         phase ^= 1u;
@@ -235,7 +275,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 ptx::mma_commit_pair(bar_drain);
                 drain(bar_drain, 0, p.timeout_ns, p.err);
                 // the last release of the accumulator arrives on this CTA
-                if (ok && tiles > 0) drain(bar_free, (tiles - 1) & 1, p.timeout_ns, p.err);
+                if (ok && tiles > 0) wait_for(bar_free, (tiles - 1) & 1, ERR_MMA);
+                for (uint32_t r = 0; !ok && r < 2; ++r)
+                    store_cluster64(ptx::mapa_shared(blocks_done + 8 * F_ISSUED, r), issued);
             }
             __syncwarp();
         }
@@ -305,11 +347,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         int stage = 0;
         uint32_t phase = 0;
         uint32_t slot = 0, batch = 0;
-        for (long long done = 0; done < blocks; done += F_BATCH, ++batch) {
+        long long done = 0;
+        for (; done < blocks; done += F_BATCH, ++batch) {
             const int here = blocks - done < F_BATCH ? static_cast<int>(blocks - done) : F_BATCH;
             // the stages' last MMAs have read their scales (they end in order)
-            const bool ok = wait(bar_empty + 8 * (stage + here - 1), phase ^ 1u, abort_flag,
-                                 p.timeout_ns, p.err, ERR_PRODUCER);
+            const bool ok = wait_for(bar_empty + 8 * (stage + here - 1), phase ^ 1u, ERR_PRODUCER);
             copy_wait<F_RING - 2>();
             // what this thread copied, as exponents
             uint32_t* words = reinterpret_cast<uint32_t*>(ring + slot * (F_BATCH * F_SLOT)) + lane;
@@ -367,6 +409,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             }
         }
         copy_wait<0>();
+        // (the four warps go on and give up together)
+        if (done < blocks && warp == 4 && lane == 0)
+            store_cluster64(ptx::mapa_shared(blocks_done + 8 * (F_SCALED + rank), 0), done);
     } else {
         // ---------------- output ----------------
         reg_inc<F_MANY_REGS>();
@@ -395,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                                 __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
                 __syncwarp();
             }
-            bool ok = wait(bar_done, tiles & 1, abort_flag, p.timeout_ns, p.err, ERR_EPILOGUE);
+            bool ok = wait_for(bar_done, tiles & 1, ERR_EPILOGUE);
             ok = __all_sync(0xffffffffu, ok);  // the warp gives up together
             if (!ok) break;
             ptx::tc_fence_after();
@@ -475,6 +520,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     __syncwarp();
     ptx::cluster_sync();
     ptx::tc_fence_after();
+    if (*abort_flag) {  // (both CTAs' flag, or neither's)
+        // (a warp with registers enough)
+        if (warp == 8 && lane == 0)
+            settle(bar0, nk, (p.total_tiles - cluster - 1) / nclusters + 1, p.timeout_ns, p.err);
+        __syncwarp();
+        ptx::cluster_sync();
+    }
     if (warp == 1) {
         __syncwarp();
         ptx::tmem_dealloc_pair(tmem, F_TMEM_COLS);

@@ -153,6 +153,22 @@ __device__ __forceinline__ void arrive_relaxed_cluster(uint32_t cluster_addr) {
                  : "memory");
 }
 
+// A word or two into shared memory of either CTA of the pair.
+__device__ __forceinline__ void store_cluster(uint32_t cluster_addr, int v) {
+    asm volatile("st.relaxed.cluster.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v)
+                 : "memory");
+}
+__device__ __forceinline__ void store_cluster64(uint32_t cluster_addr, long long v) {
+    asm volatile("st.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(cluster_addr), "l"(v)
+                 : "memory");
+}
+
+// Takes bytes that no copy will bring off what the mbarrier's phase waits for.
+__device__ __forceinline__ void complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+
 // Barrier 1 of `threads` threads of the CTA; whether any of them came with `fail`.
 template <int THREADS>
 __device__ __forceinline__ bool barrier_any(bool fail) {

@@ -61,3 +61,33 @@ def test_few_tokens(split, T, din, dout, t, copies):
     lay.forward(x)
     f8._sync()
     f8._check_forward(lay, x)
+
+
+@pytest.mark.parametrize("copies", [0, 1, 3, 6, 8])
+@pytest.mark.parametrize("split,T,din,dout,t", [
+    # (at least 9 K blocks a tile, of tokens too)
+    ("column", 1100, 2048, 2064, 1), ("row", 1300, 2560, 1296, 2)])
+def test_pairs(split, T, din, dout, t, copies):
+    w = custom_linear(T, din, dout, t, split)
+    lay, X, dY = f8._layer(w, 6)
+    x = lay.quantize(X, cols=True)
+    with stalled(copies):
+        gives_up(lambda: lay.forward(x))
+        gives_up(lambda: lay.backward(dY, x), 2)
+    lay.forward(x)
+    lay.backward(dY, x)
+    f8._sync()
+    f8._check_forward(lay, x)
+    f8._check_backward(lay, x, dY, "e4m3")
+
+
+@pytest.mark.parametrize("copies", [17, 31, 40])
+def test_pairs_in_a_later_tile(copies):
+    w = custom_linear(2560, 2048, 8192, 1, "column")      # 320 tiles of 16 K blocks
+    lay, X, _ = f8._layer(w, 7)
+    x = lay.quantize(X)
+    with stalled(copies):
+        gives_up(lambda: lay.forward(x))
+    lay.forward(x)
+    f8._sync()
+    f8._check_forward(lay, x)
