@@ -142,6 +142,7 @@ TPMLP_API tpmlp_status tpmlp_norm_forward(const tpmlp_norm_params* params, const
     p.alpha = d.residual_scale;
     p.err = dev->err;
     p.timeout_ns = g_timeout_ns;
+    p.stall = g_stall;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     TPMLP_CUDA(timed(TPMLP_KERNEL_LAYERNORM_FWD, 1, st, [&] {
         return launch_nr_forward(p, post_of(d, z), pre_of(d), dev->sm_count, st);

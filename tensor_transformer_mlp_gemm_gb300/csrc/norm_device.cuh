@@ -5,6 +5,9 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "gemm_params.h"
+#include "ptx.cuh"
+
 namespace tpmlp {
 namespace nr {
 
@@ -49,6 +52,27 @@ struct Stepper {
         }
     }
 };
+
+// Waits for phase `parity` of `bar`; after the limit, false, and the error word says so.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, unsigned long long timeout_ns,
+                                        unsigned* err, unsigned code = ERR_EPILOGUE) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (ptx::globaltimer_ns() - t0 > timeout_ns) {
+            atomicOr(err, code);
+            return false;
+        }
+    }
+    return true;
+}
+
+// The same for copies of its own, before a CTA goes on without them.  They end by
+// themselves: the limit is not the caller's where that is short.
+__device__ __forceinline__ void drain_on(uint32_t bar, uint32_t parity, unsigned long long timeout_ns,
+                                         unsigned* err) {
+    wait_on(bar, parity, max(timeout_ns, 1000000000ULL), err, ERR_DRAIN);
+}
 
 // The sum of v over the warp, the same in every lane and every run.
 __device__ __forceinline__ float warp_sum(float v) {

@@ -51,6 +51,7 @@ struct NrForwardParams {
     float eps, alpha;
     unsigned int* err;           // the device error word and the limit of any one wait
     unsigned long long timeout_ns;
+    int stall;                   // failure-detection self-test: rows that a CTA copies; < 0: all
 };
 
 struct NrBackwardParams {

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import test_gpu_fp8 as f8
+import test_gpu_norm as nm
 from tensor_transformer_mlp_gemm_gb300.inputs import custom_linear
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +92,20 @@ def test_pairs_in_a_later_tile(copies):
     lay.forward(x)
     f8._sync()
     f8._check_forward(lay, x)
+
+
+@pytest.mark.parametrize("copies", [0, 1, 2, 5])
+@pytest.mark.parametrize("h,gate_rows,post,pre,quantize", [
+    (4096, 512, "rms", "rms", "e4m3"), (4096, 0, None, "layer", None), (1040, 0, "layer", "none", None),
+    (64, 0, "none", "none", None), (16384, 8192, "layer", "layer", None)])
+def test_norm_forward(h, gate_rows, post, pre, quantize, copies):
+    T = 8192                              # (at least 6 rows for each CTA)
+    d = nm._inputs(T, h, gate_rows, 8)
+    lay = nm._layer(d, T, h, post or "none", pre, gate_rows, 0.75, quantize=quantize)
+    z = post is not None
+    call = lambda: lay.forward(d["X"], d["Z"] if z else None, d["gate"])  # noqa: E731
+    with stalled(copies):
+        gives_up(call)
+    call()
+    nm._sync()
+    nm._check_forward(d, lay, lay.Out if z else None, lay.Xn, lay.stats, z=z)
