@@ -221,6 +221,7 @@ TPMLP_API tpmlp_status tpmlp_norm_backward(const tpmlp_norm_params* params, cons
     p.alpha = d.residual_scale;
     p.err = dev->err;
     p.timeout_ns = g_timeout_ns;
+    p.stall = g_stall;
     TPMLP_CUDA(nr_plan(p, dev->sm_count));
     TPMLP_CUDA(timed(TPMLP_KERNEL_LAYERNORM_BWD, 2, st, [&] {
         return launch_nr_backward(p, post_of(d, z), pre_of(d), st);

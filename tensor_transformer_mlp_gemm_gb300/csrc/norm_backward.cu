@@ -82,18 +82,30 @@ struct Shared {
     float part[2][NB_VALUES * NB_MAX_CLUSTER * NB_WARPS];  // groups side by side
     alignas(8) uint64_t sum_bar[2];
     uint64_t ring_bar[NB_MAX_GROUPS][NB_STAGES];
+    // What the end after an expired wait needs.  It is not in registers: the row loop has
+    // none left (there it spilled, layer norms of 16384 x 4096 168 -> 221 us).
+    volatile int gave_up;                       // a wait of the CTA has expired
+    volatile uint32_t copy_end[NB_MAX_GROUPS];  // rows of a group below this are copied,
+    volatile uint32_t row0[NB_MAX_GROUPS];      // from this one on
+    // copies not waited for: two pairs of rows from this one on, below that one
+    volatile uint32_t under_way[NB_MAX_GROUPS], under_way_end[NB_MAX_GROUPS];
 };
+// A CTA with a wait that has expired waits no more, sends no more and copies no more, but
+// goes through the rows that are left, so that no barrier misses a thread.
 struct Waits {
     unsigned long long timeout_ns;
     unsigned* err;
 };
 
-__device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, const Waits& w) {
+template <typename F>
+__device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, const Waits& w, Shared& sm,
+                                        F&& expired) {
     if (ptx::mbar_try_wait(bar, parity)) return;
     const uint64_t t0 = ptx::globaltimer_ns();
     while (!ptx::mbar_try_wait(bar, parity)) {
-        if (ptx::globaltimer_ns() - t0 > w.timeout_ns) {
+        if (sm.gave_up || ptx::globaltimer_ns() - t0 > w.timeout_ns) {
             atomicOr(w.err, ERR_EPILOGUE);
+            expired();
             return;
         }
     }
@@ -129,9 +141,9 @@ __device__ __forceinline__ float warp_sums(const float (&v)[N], int lane) {
 // Sums of N values over a row: the group's warps, and the cluster's CTAs.  The buffers
 // alternate: a part of the next but one sum can only come once every warp has given its
 // part of the next, and so has read this one.
-template <int CL, int WG, int N>
+template <int CL, int WG, int N, typename F>
 __device__ __forceinline__ void row_sums(float (&v)[N], Shared& sm, int& buf, uint32_t (&phase)[2],
-                                         int group, int rank, const Waits& w) {
+                                         int group, int rank, const Waits& w, F&& expired) {
     constexpr int SLOTS = CL * WG, LP = 32 / N;
     const int warp = (threadIdx.x >> 5) % WG, lane = threadIdx.x & 31;
     float* part = sm.part[buf] + group * (NB_VALUES * WG);
@@ -145,15 +157,16 @@ __device__ __forceinline__ void row_sums(float (&v)[N], Shared& sm, int& buf, ui
             __syncwarp();
     } else {
         const uint32_t bar = ptx::smem_u32(&sm.sum_bar[buf]);
-        if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bar, SLOTS * N * 4);
+        const bool alive = !sm.gave_up;
+        if (threadIdx.x == 0 && alive) ptx::mbar_arrive_expect_tx(bar, SLOTS * N * 4);
         // lane n * LP + i sends value n to CTA i
-        if (lane % LP < CL) {
+        if (lane % LP < CL && alive) {
             const uint32_t to = static_cast<uint32_t>(lane % LP);
             send(ptx::mapa_shared(ptx::smem_u32(part + n * SLOTS + slot), to), x,
                  ptx::mapa_shared(bar, to));
         }
         __syncwarp();
-        wait_on(bar, phase[buf], w);
+        wait_on(bar, phase[buf], w, sm, expired);
         phase[buf] ^= 1u;
     }
     float t = 0.0f;
@@ -196,6 +209,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         ptx::mbar_init(ptx::smem_u32(&sm.sum_bar[0]), 1);
         ptx::mbar_init(ptx::smem_u32(&sm.sum_bar[1]), 1);
+        sm.gave_up = 0;
         for (int g = 0; g < G; ++g)
             for (int s = 0; s < NB_STAGES; ++s) ptx::mbar_init(ptx::smem_u32(&sm.ring_bar[g][s]), 1);
         ptx::fence_mbar_init();
@@ -265,7 +279,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (tid == 0) {
 #pragma unroll
         for (int s = 0; s < NB_STAGES; ++s)
-            if (row + s * R < last) copy_rows(row + s * R, s);
+            if (row + s * R < last && (p.stall < 0 || rank + 1 < CL || s < p.stall))
+                copy_rows(row + s * R, s);
+        sm.row0[group] = static_cast<uint32_t>(row);
+        sm.copy_end[group] = static_cast<uint32_t>(
+            p.stall < 0 || rank + 1 < CL ? last : min(last, row + static_cast<long long>(p.stall) * R));
+        sm.under_way_end[group] = 0;
     }
     // lane 4 i + k has statistic k of the pair's row i
     auto load_stats = [&](long long r0) {
@@ -280,8 +299,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     int stage = 0;
     uint32_t ring_phase = 0;
     Stepper chunk(row, 1, p.rows_per_chunk), seq(row, 1, p.gate_rows);
+    // a wait has expired: under way may be the pair from row r on and the next one
+    auto expired = [&](long long r) {
+        sm.gave_up = 1;
+        if (tid == 0 && sm.copy_end[group] > 0) {
+            sm.under_way[group] = static_cast<uint32_t>(r);
+            sm.under_way_end[group] = sm.copy_end[group];
+            sm.copy_end[group] = 0;
+        }
+    };
     for (; row < last; row += R) {
-        wait_on(ptx::smem_u32(&sm.ring_bar[group][stage]), ring_phase, waits);
+        wait_on(ptx::smem_u32(&sm.ring_bar[group][stage]), ring_phase, waits, sm, [&] { expired(row); });
         uint4 q_dout[R], q_dxn[R], q_out[R], q_z[R], q_gate[R];
         float m1[R], r1[R], m2[R], r2[R];
         const uint8_t* src = ring + stage * (R * NB_ARRAYS * ROW) + tid * 16;
@@ -290,9 +318,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                        ? *reinterpret_cast<const uint4*>(src + (i * NB_ARRAYS + a) * ROW)
                        : zero4();
         };
+        // (one CTA's sums wait on no mbarrier, so what follows the pair is known here, if
+        // there are registers to keep it in)
+        constexpr bool EARLY = CL == 1 && THREADS == NB_FEWER;
+        const bool more = EARLY && tid == 0 && row + NB_STAGES * R < sm.copy_end[group];
         // every thread of the group has read this stage
         auto release = [&] {
-            if (tid == 0 && row + NB_STAGES * R < last) copy_rows(row + NB_STAGES * R, stage);
+            if (EARLY ? more : tid == 0 && row + NB_STAGES * R < sm.copy_end[group])
+                copy_rows(row + NB_STAGES * R, stage);
             if (++stage == NB_STAGES) {
                 stage = 0;
                 ring_phase ^= 1u;
@@ -350,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 sums[i] = sv.x + sv.y;
                 if (PRE_LAYER) sums[R + i] = sw.x + sw.y;
             }
-            row_sums<CL, WG, N>(sums, sm, buf, phase, group, rank, waits);
+            row_sums<CL, WG, N>(sums, sm, buf, phase, group, rank, waits, [&] { expired(row); });
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 float2 d[4], v[4], w[4];
@@ -445,7 +478,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             if constexpr (POST_NORM) {
-                row_sums<CL, WG, N>(sums, sm, buf, phase, group, rank, waits);
+                row_sums<CL, WG, N>(sums, sm, buf, phase, group, rank, waits,
+                                    [&] { expired(HOLD ? row + R : row); });  // (the stage is free)
                 if (!HOLD) release();
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
@@ -471,6 +505,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dz[k[i]]) + off[i]) = pack(g[i]);
         }
     }
+
+    if (tid == 0) {
+        // copies that were not waited for land before the CTA leaves
+        const uint32_t end = sm.under_way_end[group];
+        for (uint32_t i = 0; i < NB_STAGES && end > 0; ++i) {
+            const uint32_t r = sm.under_way[group] + i * R, pair = (r - sm.row0[group]) / R;
+            if (r < end)
+                drain_on(ptx::smem_u32(&sm.ring_bar[group][pair % NB_STAGES]), pair / NB_STAGES & 1u,
+                     p.timeout_ns, p.err);
+        }
+    }
+    __syncwarp();
+    if constexpr (CL > 1) ptx::cluster_arrive_relaxed();
 
     // the block's column sums, the groups' added in order: one partial row for each vector
     ptx::griddep_launch_dependents();
@@ -508,8 +555,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     if constexpr (Z) {
         if (gate && cut) put(s_gate);
     }
-    // a CTA that has left cannot take a part that is still on its way to it: the last
-    // sums have all been waited for, so none is
+    // No part may be on its way to a CTA that has left.  The last sums have all been waited
+    // for, so none is; but a CTA that gave up is done before the others, which send until
+    // their own wait for the same sum has run out.
+    __syncwarp();
+    if constexpr (CL > 1) ptx::cluster_wait();
 }
 
 // out[c] = sum over the blocks of a vector's partial rows, in block order within

@@ -70,6 +70,8 @@ struct NrBackwardParams {
     int blocks_per_seq;
     unsigned int* err;           // the device error word and the limit of any one wait
     unsigned long long timeout_ns;
+    int stall;                   // failure-detection self-test: row pairs that each group of a cluster's
+                                 // last CTA copies; < 0: all
 };
 
 cudaError_t launch_nr_forward(const NrForwardParams& p, int post, int pre, int sm_count,

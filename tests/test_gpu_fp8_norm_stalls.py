@@ -109,3 +109,27 @@ def test_norm_forward(h, gate_rows, post, pre, quantize, copies):
     call()
     nm._sync()
     nm._check_forward(d, lay, lay.Out if z else None, lay.Xn, lay.stats, z=z)
+
+
+@pytest.mark.parametrize("copies", [0, 1, 2, 5])
+@pytest.mark.parametrize("T,h,gate_rows,post,pre", [
+    # (6 pairs of rows at least for each group of threads); post None: no block before
+    (16384, 512, 2048, "rms", "rms"), (8192, 1024, 0, "none", "none"), (4096, 4096, 512, "layer", "layer"),
+    (4096, 4096, 0, None, "rms"), (4096, 4096, 4096, "rms", "none"),
+    # clusters: the CTAs that load go on until their sums do not come
+    (2048, 6144, 512, "layer", "rms"), (2048, 8192, 512, "rms", "rms"), (2048, 9000, 0, None, "layer"),
+    (2048, 12288, 512, "rms", "rms"), (2048, 12288, 0, "none", "none"), (1024, 12288, 0, "rms", "none"),
+    (1024, 16384, 512, "layer", "layer")])
+def test_norm_backward(T, h, gate_rows, post, pre, copies):
+    d = nm._inputs(T, h, gate_rows, 9)
+    lay = nm._layer(d, T, h, post or "none", pre, gate_rows, 0.75)
+    z, dXn = post is not None, d["dXn"] if pre != "none" else None
+    lay.forward(d["X"], d["Z"] if z else None, d["gate"])
+    Out = lay.Out if z else d["X"]
+    call = lambda: lay.backward(d["dOut"], dXn, d["Z"] if z else None, Out, gate=d["gate"])  # noqa: E731
+    lay._gradients()
+    with stalled(copies):
+        gives_up(call)
+    call()
+    nm._sync()
+    nm._check_backward(d, lay, Out, lay.stats, d["dOut"], dXn, z=z)
