@@ -630,7 +630,7 @@ enum {
     TPMLP_KERNEL_LINEAR_DGRAD = 8,  /* linear layers (bf16, 8-bit): dX = sum_i dY_i.W_i^T, dX_i = dZ.W_i^T */
     TPMLP_KERNEL_LINEAR_WGRAD = 9,  /* linear layers (bf16, 8-bit): dW_i */
     TPMLP_KERNEL_LAYERNORM_FWD = 10,  /* sequence-parallel sublayer: LN(X) and row statistics; tpmlp_norm_forward */
-    TPMLP_KERNEL_LAYERNORM_BWD = 11,  /* sequence-parallel sublayer: dX, dgamma, dbeta (2 launches; 3 for h > 4096); tpmlp_norm_backward (2) */
+    TPMLP_KERNEL_LAYERNORM_BWD = 11,  /* sequence-parallel sublayer: dX, dgamma, dbeta (2 launches; 3 for h > 4096); tpmlp_norm_backward (2; 1 with no norm and no gate to add up) */
     TPMLP_KERNEL_DROPOUT_BWD = 12,    /* sequence-parallel sublayer: dZ from dOut and the mask, db2 (2 launches) */
     TPMLP_KERNEL_SP_COPY = 13,        /* tpmlp_sp_gather / tpmlp_sp_scatter, 8-bit quantisation */
     TPMLP_KERNEL_KINDS = 14

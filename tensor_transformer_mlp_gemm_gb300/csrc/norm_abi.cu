@@ -223,7 +223,9 @@ TPMLP_API tpmlp_status tpmlp_norm_backward(const tpmlp_norm_params* params, cons
     p.timeout_ns = g_timeout_ns;
     p.stall = g_stall;
     TPMLP_CUDA(nr_plan(p, dev->sm_count));
-    TPMLP_CUDA(timed(TPMLP_KERNEL_LAYERNORM_BWD, 2, st, [&] {
+    // the second launch adds up what the row blocks left, if anything
+    const bool sums = post || pre || (gate && p.blocks_per_seq > 0);
+    TPMLP_CUDA(timed(TPMLP_KERNEL_LAYERNORM_BWD, sums ? 2 : 1, st, [&] {
         return launch_nr_backward(p, post_of(d, z), pre_of(d), st);
     }));
     return TPMLP_OK;

@@ -76,7 +76,7 @@ struct NrBackwardParams {
 
 cudaError_t launch_nr_forward(const NrForwardParams& p, int post, int pre, int sm_count,
                               cudaStream_t st);
-// Two launches: the rows, and the sums over the row blocks.
+// The rows, and, if there are any, the sums over the row blocks: up to two launches.
 cudaError_t launch_nr_backward(const NrBackwardParams& p, int post, int pre, cudaStream_t st);
 
 // Row blocks of the backward pass.  A block never holds part of one gate's rows

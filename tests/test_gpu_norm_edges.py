@@ -1,4 +1,5 @@
-"""The norms around a block at the edges of what they take: no tokens with a gate or 8-bit rows."""
+"""The norms around a block at the edges of what they take: no tokens with a gate or 8-bit
+rows, wide rows with no norm before, and how many kernels a backward pass launches."""
 import pytest
 import torch
 
@@ -33,3 +34,30 @@ def test_empty(gate_rows, quantize, chunks):
         assert torch.count_nonzero(getattr(lay, k)) == 0
     if gate_rows:
         assert lay.dgate.shape == (0, 64)
+
+
+@pytest.mark.parametrize("T,h,gate_rows", [(701, 4096, 0), (701, 3080, 701), (305, 8192, 61), (151, 9000, 0),
+                                           (305, 12288, 0), (151, 16384, 151)])
+@pytest.mark.parametrize("post", ["rms", "layer", "none"])
+def test_no_norm_before(T, h, gate_rows, post):
+    """Wide rows, an odd number of them, several pairs for each group: a stage of the ring is
+    freed by a barrier of its own where there are no sums of a norm before."""
+    nm.test_norm(T, h, gate_rows, post, "none")
+
+
+@pytest.mark.parametrize("post,pre,gate_rows,launches", [
+    ("none", "none", 0, 1), ("none", "none", 1, 1), ("none", "none", 512, 2), ("rms", "none", 0, 2),
+    ("none", "rms", 0, 2)])
+def test_launches_of_the_backward_pass(post, pre, gate_rows, launches):
+    """The profile counts the kernels that were launched: the second one only where there
+    are sums over rows for it."""
+    from tensor_transformer_mlp_gemm_gb300 import binding
+    d = nm._inputs(2048, 256, gate_rows, 3)
+    lay = nm._layer(d, 2048, 256, post, pre, gate_rows, 1.0)
+    lay.forward(d["X"], d["Z"], d["gate"])
+    lay._gradients()
+    binding.tpmlp_profile_begin(8)
+    lay.backward(d["dOut"], d["dXn"] if pre != "none" else None, d["Z"], lay.Out, gate=d["gate"])
+    torch.cuda.synchronize()
+    counts = binding.tpmlp_profile_end()[1]
+    assert counts["layernorm_bwd"] == launches
