@@ -531,7 +531,9 @@ tpmlp_status tpmlp_set_wide_tiles(int mode);
  * encoded maps in a cache keyed by every argument of the encoding (base
  * address, element type, extents, strides, box, swizzle), so a repeated call
  * on the same buffers encodes nothing.  A buffer at a new address is a new key
- * (a stale entry is never used for another address).  At most 4096 maps are
+ * (a stale entry is never used for another address); the operands of the 8-bit
+ * layers share one map for each shape, and each call sets the address in its own
+ * copy.  At most 4096 maps are
  * kept; when the cache is full it is emptied.  Thread-safe (one mutex).
  * tpmlp_map_cache_stats reports the hits, misses (encodings) and entries so
  * far; any pointer may be NULL.  Always TPMLP_OK. */

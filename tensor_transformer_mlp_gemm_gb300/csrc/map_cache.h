@@ -8,7 +8,9 @@
 // strides, box, swizzle, L2 promotion), so it is cached under exactly those:
 // a buffer at a new address (or of another shape) is a new key, and a cached
 // map is never wrong for its key, even after the memory behind it was freed
-// and reallocated.  The cache holds at most `capacity` maps; when it is full
+// and reallocated.  8-bit operands, which come at new addresses all the time, are
+// kept by the rest (the key's address is null), and the caller's copy gets its
+// address.  The cache holds at most `capacity` maps; when it is full
 // it is emptied and refills from the next calls.  A mutex guards it.
 #pragma once
 

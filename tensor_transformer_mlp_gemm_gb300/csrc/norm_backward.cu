@@ -52,7 +52,8 @@ constexpr int NB_RING = NB_STAGES * NB_ROWS * NB_ARRAYS * NB_COLS * 2;
 static_assert(NB_COLS * NB_MAX_CLUSTER >= NR_MAX_H, "a cluster holds the widest row");
 
 // CTAs side by side for a row, groups of a CTA's threads that take rows of their own, and
-// the CTA's threads: 384 unless only 512 hold one or two rows.
+// the CTA's threads: 384 unless only 512 hold one or two rows.  Every CTA of a cluster has
+// columns of the row.
 int cluster_of(long long h) {
     return h <= NB_COLS ? 1 : h <= 2 * NB_COLS ? 2 : h <= 3 * NB_FEWER * 8 ? 3 : 4;
 }
@@ -151,10 +152,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], Shared& sm, int& buf, ui
     const int n = lane / LP, slot = rank * WG + warp;
     if constexpr (CL == 1) {
         if (lane % LP == 0) part[n * SLOTS + slot] = x;
-        if constexpr (WG > 1)
-            asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(WG * 32) : "memory");
-        else
-            __syncwarp();
+        asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(WG * 32) : "memory");
     } else {
         const uint32_t bar = ptx::smem_u32(&sm.sum_bar[buf]);
         const bool alive = !sm.gave_up;
@@ -187,6 +185,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr bool POST_LAYER = POST == NR_POST_LAYER, PRE_LAYER = PRE == NR_PRE_LAYER;
     constexpr int R = NB_ROWS, GT = THREADS / G, WG = GT / 32, ROW = GT * 16;  // a row's bytes in the ring
     static_assert(CL == 1 || G == 1, "wide rows take whole CTAs");
+    static_assert(WG > 1, "a group's warps meet at a barrier");
     // Z and the gate are read from the ring when they are needed, not held from the start:
     // that spilled (layer norms, 16384 x 4096 182 us instead of 168; rms norms, 16384 x
     // 2048 94 instead of 85).  Where they fit they are held, and the stage is free sooner
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     // the ring: one thread of the group has the copies of a row pair under way
     const int cols = min(GT * 8, p.h - c0);
-    const uint32_t bytes = cols > 0 ? static_cast<uint32_t>(cols) * 2 : 0;
+    const uint32_t bytes = static_cast<uint32_t>(cols) * 2;
     // (a row's token chunk and gate are stepped, not divided out: the divisions were
     // half of all instructions)
     Stepper copy_chunk(row, 1, p.rows_per_chunk), copy_gate(row, 1, p.gate_rows);
@@ -253,7 +252,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int n = r0 + 1 < last ? 2 : 1;
         const int arrays = (dout ? 1 : 0) + (BEFORE ? 2 : 0) + (Z ? 1 : 0) + (gate ? 1 : 0);
         ptx::mbar_arrive_expect_tx(bar, bytes * static_cast<uint32_t>(n * arrays));
-        if (bytes == 0) return;
         for (int i = 0; i < n; ++i) {
             const uint32_t k = copy_chunk.q;
             const long long off = static_cast<long long>(copy_chunk.r) * p.h + c0;
@@ -332,10 +330,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         };
         auto group_sync = [&] {
-            if constexpr (CL > 1 || WG > 1)
-                asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(GT) : "memory");
-            else
-                __syncwarp();
+            asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(GT) : "memory");
         };
 #pragma unroll
         for (int i = 0; i < R; ++i) {

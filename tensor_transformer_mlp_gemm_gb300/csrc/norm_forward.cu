@@ -18,7 +18,7 @@
 // rows that are left with the others, so that no barrier misses it; what it has under way
 // lands first.
 // Measured, rms norms and a gate, cold caches, launch included: 16384 x 4096 in 88 us
-// (6.1 TB/s), with 8-bit Xn 96; 8192 x 8192 88; 2048 x 12288 43; 16384 x 1024 29.
+// (6.1 TB/s), with 8-bit Xn 96; 8192 x 8192 88; 2048 x 12288 43; 16384 x 1024 29.  Back to back 16384 x 4096 84 (8-bit 86), 2048 x 12288 36, 16384 x 1024 24.
 #include "fp8_cvt.cuh"
 #include "norm_device.cuh"
 #include "norm_residual.cuh"

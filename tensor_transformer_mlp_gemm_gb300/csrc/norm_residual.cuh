@@ -27,7 +27,7 @@ namespace tpmlp {
 
 constexpr int NR_MAX_CHUNKS = 8;
 constexpr int NR_MAX_H = 16384;
-constexpr int NR_MAX_UNITS = 192;  // CTAs of the backward pass, at most one per SM
+constexpr int NR_MAX_UNITS = 192;  // most CTAs of the backward pass that run at once: one on an SM
 
 // N_post: no Z at all (Out is X, not written), identity, rms, layer;  N_pre: none, rms, layer
 enum NrPost : int { NR_ABSENT = 0, NR_IDENTITY = 1, NR_POST_RMS = 2, NR_POST_LAYER = 3 };
