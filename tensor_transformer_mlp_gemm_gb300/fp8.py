@@ -279,8 +279,7 @@ class DeviceFp8Linear:
         self._y = ((T, s), t) if self.column else ((T // n, dout), n)
         self._dx = ((T // n, din), n) if self.column else ((T, s), t)
         self.Y = [torch.empty(self._y[0], dtype=bf, device=dev) for _ in range(self._y[1])]
-        self.dX = [torch.empty(self._dx[0], dtype=bf, device=dev) for _ in range(self._dx[1])]
-        self._grads = None
+        self._dX = self._dx_ptrs = self._grads = None
         if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()
                                       or workspace.numel() * workspace.element_size() < need):
             raise ValueError(f"the workspace needs {need} contiguous bytes on {dev}")
@@ -301,8 +300,18 @@ class DeviceFp8Linear:
         self._Y = tuple(self._list(xs, self._y, "Y"))
         self._y_ptrs = _pointers(self._Y)
 
+    # Gradients are made by the first backward call, so that a layer that only goes forward
+    # does not hold them.
+    def _input_grads(self, stream=None):
+        if self._dX is None:
+            with binding.allocate_on(self.device, stream):
+                self.dX = [torch.empty(self._dx[0], dtype=torch.bfloat16, device=self.device)
+                           for _ in range(self._dx[1])]
+        return self._dx_ptrs
+
     @property
     def dX(self):
+        self._input_grads()
         return list(self._dX)
 
     @dX.setter
@@ -311,7 +320,7 @@ class DeviceFp8Linear:
         self._dx_ptrs = _pointers(self._dX)
 
     def _weight_grads(self, stream=None):
-        # fp32 gradients, four times the weights' bytes: made by the first backward call
+        # fp32, four times the weights' bytes
         if self._grads is None:
             shape = self._Wq[0].shape
             with binding.allocate_on(self.device, stream):
@@ -385,7 +394,7 @@ class DeviceFp8Linear:
         ``quantize`` makes it."""
         q, s = self._tokens(x, cols=True)
         dY = _pointers(self._list(dY, self._y, "dY"))
-        dX = self._dx_ptrs if dX is None else _pointers(self._list(dX, self._dx, "dX"))
+        dX = self._input_grads(stream) if dX is None else _pointers(self._list(dX, self._dx, "dX"))
         dW, db = self._weight_grads(stream)
         with binding.on_device(self.device):
             stream = binding.stream_on(self.device, stream)
