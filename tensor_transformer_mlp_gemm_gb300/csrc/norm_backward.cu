@@ -24,9 +24,9 @@
 // 111 as 3 x 512, 105 as 4 x 384.
 // The column sums of a block of rows go to a partial row, and a second kernel adds the
 // blocks in order; a gate whose rows lie in one group is finished there.  No atomics.
-// Measured, rms norms and 8 gates, cold caches, launches included: 16384 x 4096 in 139 us
-// (5.8 TB/s), layer norms 168; 8192 x 8192 168 and 199; 2048 x 12288 82; 16384 x 2048 85;
-// 16384 x 1024 51.
+// Measured, rms norms and 8 gates, back to back, both launches: 16384 x 4096 in 137 us (5.9
+// TB/s), layer norms 159; 8192 x 8192 165 and 190; 2048 x 12288 76; 16384 x 2048 80; 16384 x
+// 1024 46; 917 x 9000 and 7 gates, layer, 37.  (Figures above: cold caches, up to 6 us more.)
 #include <algorithm>
 
 #include "gemm_params.h"
@@ -84,7 +84,7 @@ struct Shared {
     alignas(8) uint64_t sum_bar[2];
     uint64_t ring_bar[NB_MAX_GROUPS][NB_STAGES];
     // What the end after an expired wait needs.  It is not in registers: the row loop has
-    // none left (there it spilled, layer norms of 16384 x 4096 168 -> 221 us).
+    // none left (there it spilled: layer norms of 16384 x 4096 221 us, not 159).
     volatile int gave_up;                       // a wait of the CTA has expired
     volatile uint32_t copy_end[NB_MAX_GROUPS];  // rows of a group below this are copied,
     volatile uint32_t row0[NB_MAX_GROUPS];      // from this one on
