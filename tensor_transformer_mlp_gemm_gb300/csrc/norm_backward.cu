@@ -400,7 +400,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = 0; i < R; ++i) unpack(q_dout[i], g[i]);
         }
         if constexpr (!Z || HOLD) {
-            if constexpr (!BEFORE) group_sync();  // (else its sums met in between)
+            // (else the group met at its sums; over a cluster they meet at an mbarrier, which
+            // does not order what a thread has read and not yet used)
+            if constexpr (!BEFORE || CL > 1) group_sync();
             release();
         }
         uint32_t k[R];
