@@ -61,3 +61,38 @@ def test_launches_of_the_backward_pass(post, pre, gate_rows, launches):
     torch.cuda.synchronize()
     counts = binding.tpmlp_profile_end()[1]
     assert counts["layernorm_bwd"] == launches
+
+
+@pytest.mark.parametrize("T,chunks,gate_rows", [(96, 4, 32), (240, 8, 80), (240, 8, 20), (60, 2, 12)])
+def test_gates_across_chunks(T, chunks, gate_rows):
+    """Gates that begin and end inside token chunks, with 8-bit rows and bf16 ones: what whole
+    tensors give."""
+    from tensor_transformer_mlp_gemm_gb300 import binding
+    h = 528
+    d = nm._inputs(T, h, gate_rows, T)
+    whole = nm._layer(d, T, h, "rms", "layer", gate_rows, 0.9)
+    parts = nm._layer(d, T, h, "rms", "layer", gate_rows, 0.9, seq_chunks=chunks)
+    eight = nm._layer(d, T, h, "rms", "layer", gate_rows, 0.9, seq_chunks=chunks, quantize="e4m3")
+    one = nm._layer(d, T, h, "rms", "layer", gate_rows, 0.9, quantize="e4m3")
+    c = lambda x: [t.clone() for t in x.chunk(chunks)]  # noqa: E731
+    whole.forward(d["X"], d["Z"], d["gate"])
+    one.forward(d["X"], d["Z"], d["gate"])
+    X, Z = c(d["X"]), c(d["Z"])
+    parts.forward(X, Z, d["gate"])
+    eight.forward(X, Z, d["gate"])
+    # both forms of Xn, in chunks
+    Xn, q, s = c(torch.zeros_like(d["X"])), torch.zeros_like(eight.q), torch.zeros_like(eight.q_scale)
+    binding.tpmlp_norm_forward(eight.params, X, Z, eight.post_gamma, None, d["gate"], eight.pre_gamma,
+                               eight.pre_beta, [torch.empty_like(x) for x in X], Xn, q, s, None)
+    whole.backward(d["dOut"], d["dXn"], d["Z"], whole.Out, gate=d["gate"])
+    parts.backward(c(d["dOut"]), c(d["dXn"]), Z, parts.Out, gate=d["gate"])
+    nm._sync()
+    for k in ("Out", "Xn", "dX", "dZ"):
+        assert torch.equal(getattr(whole, k), torch.cat(getattr(parts, k)))
+    for k in ("dgate", "dpost_gamma", "dpre_gamma", "dpre_beta"):
+        assert torch.equal(getattr(whole, k), getattr(parts, k))
+    assert torch.equal(torch.cat(Xn), whole.Xn)
+    for got, scale in ((eight.q, eight.q_scale), (q, s)):
+        assert torch.equal(got.view(torch.uint8), one.q.view(torch.uint8)) and torch.equal(scale, one.q_scale)
+    nm._check_forward(d, whole, whole.Out, whole.Xn, whole.stats)
+    nm._check_backward(d, whole, whole.Out, whole.stats, d["dOut"], d["dXn"])
