@@ -414,6 +414,118 @@ tpmlp_status tpmlp_fp8_row_linear_backward(const tpmlp_linear_dims* dims,
                                            void* const* dW_shards, void* db, void* workspace,
                                            void* stream);
 
+/* ---- Linear layers on 4-bit operands ------------------------------------------------
+ * The same layers with X, W and dY in 4-bit floating point (a sign, two exponent bits, one
+ * mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and a scale for each group along the axis that
+ * a product sums over, on the tensor cores' 4-bit instructions:
+ *
+ *   mx   groups of 32; s = the smallest power of two with max |x| <= 6 s, at least 2^-126,
+ *        stored as an 8-bit exponent (biased by 127)
+ *   nv   groups of 16 and a scale g (fp32, on the device) for the tensor, which all its
+ *        shards share: s = max |x| / (6 g) rounded to e4m3, at most 448, at least 2^-9;
+ *        tpmlp_fp4_tensor_scale makes g the smallest power of two, at least 2^-110, with
+ *        which the largest finite magnitude is at most 6 * 448 g.  A given g has to be a
+ *        power of two of 2^-110 .. 2^117 (else every result is NaN); what it leaves out of
+ *        range becomes the largest value
+ *   q  = round-to-nearest-even(x / s), of nv x / (s g)
+ *
+ * The same on every machine: powers of two leave every comparison exact.  A group with an
+ * infinity or a NaN has the scale NaN, and so have the results that take part of it.
+ *
+ * A 4-bit matrix [R, K] is summed over K: R rows of (K rounded up to 32) / 2 bytes, element
+ * 2i in the low half of byte i.  Its scales: for each 128 rows and each 256 of K 1024 bytes
+ * (mx) or 2048 (nv) of one byte a scale, in blocks of 128 rows by 4 groups, row r's group j
+ * at byte 16 (r % 32) + 4 (r / 32) + j of its block.  Quantising "by rows" makes [T, C] of a
+ * bf16 [T, C], "by columns" the transposed [C, T].  tpmlp_fp4_packed_bytes and
+ * tpmlp_fp4_scale_bytes are the sizes of the two arrays, which start on 16 bytes.
+ * Conventions, chunking, errors and workspace rules as for the bf16 linear layers, with
+ * features and shards multiples of 32 and no more than 2^31 - 256 tokens or features (else
+ * TPMLP_ERR_UNSUPPORTED). */
+typedef enum {
+    TPMLP_FP4_MX = 0,
+    TPMLP_FP4_NV = 1
+} tpmlp_fp4_format;
+
+/* `parts` bf16 matrices [rows, cols] of the same shape, quantised in one launch: each with
+ * outputs of its own (gather = 0), or row chunks of one matrix [parts * rows, cols] with one
+ * output (gather = 1; rows then a multiple of 128 unless parts = 1). */
+typedef struct {
+    int64_t rows, cols; /* of each part; cols a multiple of 32 */
+    int32_t parts;      /* 1..8 */
+    int32_t gather;
+    int32_t format;     /* tpmlp_fp4_format */
+} tpmlp_fp4_quant;
+
+size_t tpmlp_fp4_packed_bytes(int64_t rows, int64_t k);
+size_t tpmlp_fp4_scale_bytes(int64_t rows, int64_t k, int format);
+
+/* g of all parts together (nv) into scale[0], fp32 on the device. */
+tpmlp_status tpmlp_fp4_tensor_scale(const tpmlp_fp4_quant* quant, const void* const* src, void* scale,
+                                    void* stream);
+
+/* Quantise by rows, by columns, or both in one read of src.  scale: g (nv), NULL (mx).
+ * q_rows, s_rows, q_cols, s_cols: host arrays of `parts` device pointers (one with gather);
+ * the row pair or the column pair may be NULL, not both. */
+tpmlp_status tpmlp_fp4_quantize(const tpmlp_fp4_quant* quant, const void* const* src, const void* scale,
+                                void* const* q_rows, void* const* s_rows, void* const* q_cols,
+                                void* const* s_cols, void* stream);
+
+/* The values of a 4-bit matrix [rows, k] in bf16, which holds them exactly (but those that
+ * rounding took past its largest value, which become infinite). */
+tpmlp_status tpmlp_fp4_dequantize(int64_t rows, int64_t k, int format, const void* q, const void* s,
+                                  const void* scale, void* out, void* stream);
+
+/* Bytes of scratch workspace a call with these dims needs: forward calls, or (backward != 0)
+ * forward and backward calls.  0 for unsupported dims. */
+size_t tpmlp_fp4_linear_workspace_bytes(const tpmlp_linear_dims* dims, int format, int backward);
+
+/* Column parallel.  Forward:  Y_i = X.W_i + b[i*oi:(i+1)*oi], X quantised here by rows
+ *   X          seq_chunks chunks of [Tc, in] bf16
+ *   x_scale    g of X (nv; NULL for mx): read if x_calibrated, else computed and written
+ *   Xq, Xs     X by columns (output, for the backward pass), or both NULL
+ *   Wq, Ws     [t] shards W_i by columns ([oi, in]);  w_scale their g
+ *   b          [out] bf16;  Y_shards [t] of [T, oi] bf16 (output)
+ * Backward for upstream dY_i (bf16, quantised here both ways, g computed):
+ *   dX = sum_i dY_i.W_i^T (bf16, seq_chunks chunks), dW_i = X^T.dY_i (fp32),
+ *   db = column sums of the bf16 dY (fp32)
+ *   Xq, Xs, x_scale  as the forward call left them
+ *   Wq, Ws     [t] shards W_i by rows ([in, oi])
+ * With T = 0 the forward does nothing and the backward zeroes dW and db. */
+tpmlp_status tpmlp_fp4_column_linear_forward(const tpmlp_linear_dims* dims, int format,
+                                             const void* const* X, void* x_scale, int x_calibrated,
+                                             void* Xq, void* Xs, const void* const* Wq_shards,
+                                             const void* const* Ws_shards, const void* w_scale,
+                                             const void* b, void* const* Y_shards, void* workspace,
+                                             void* stream);
+tpmlp_status tpmlp_fp4_column_linear_backward(const tpmlp_linear_dims* dims, int format,
+                                              const void* const* dY_shards, const void* Xq,
+                                              const void* Xs, const void* x_scale,
+                                              const void* const* Wq_shards, const void* const* Ws_shards,
+                                              const void* w_scale, void* const* dX,
+                                              void* const* dW_shards, void* db, void* workspace,
+                                              void* stream);
+
+/* Row parallel.  Forward:  Z = (sum_i X_i.W_i) + b
+ *   X          [t] shards X_i [T, ii] bf16, with one x_scale
+ *   Xq, Xs     [t] shards by columns (output), or both NULL
+ *   Wq, Ws     [t] shards W_i by columns ([out, ii]);  Z seq_chunks chunks of [Tc, out] bf16
+ * Backward for upstream dZ (seq_chunks chunks, bf16):
+ *   dX_i = dZ.W_i^T (bf16 [T, ii]), dW_i = X_i^T.dZ (fp32 [ii, out]), db (fp32)
+ *   Wq, Ws     [t] shards W_i by rows ([ii, out]) */
+tpmlp_status tpmlp_fp4_row_linear_forward(const tpmlp_linear_dims* dims, int format,
+                                          const void* const* X_shards, void* x_scale, int x_calibrated,
+                                          void* const* Xq_shards, void* const* Xs_shards,
+                                          const void* const* Wq_shards, const void* const* Ws_shards,
+                                          const void* w_scale, const void* b, void* const* Z,
+                                          void* workspace, void* stream);
+tpmlp_status tpmlp_fp4_row_linear_backward(const tpmlp_linear_dims* dims, int format,
+                                           const void* const* dZ, const void* const* Xq_shards,
+                                           const void* const* Xs_shards, const void* x_scale,
+                                           const void* const* Wq_shards, const void* const* Ws_shards,
+                                           const void* w_scale, void* const* dX_shards,
+                                           void* const* dW_shards, void* db, void* workspace,
+                                           void* stream);
+
 /* ---- Norms before and after a block, with its gate and residual scale ------------
  * What surrounds a block f in a residual stream X with a norm on both sides of it:
  *

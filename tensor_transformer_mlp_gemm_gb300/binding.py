@@ -45,6 +45,10 @@ EXPORTED = (
     "tpmlp_fp8_quantize", "tpmlp_fp8_quantize_weight", "tpmlp_fp8_linear_workspace_bytes",
     "tpmlp_fp8_column_linear_forward", "tpmlp_fp8_column_linear_backward",
     "tpmlp_fp8_row_linear_forward", "tpmlp_fp8_row_linear_backward",
+    "tpmlp_fp4_packed_bytes", "tpmlp_fp4_scale_bytes", "tpmlp_fp4_tensor_scale", "tpmlp_fp4_quantize",
+    "tpmlp_fp4_dequantize", "tpmlp_fp4_linear_workspace_bytes",
+    "tpmlp_fp4_column_linear_forward", "tpmlp_fp4_column_linear_backward",
+    "tpmlp_fp4_row_linear_forward", "tpmlp_fp4_row_linear_backward",
     "tpmlp_norm_workspace_bytes", "tpmlp_norm_forward", "tpmlp_norm_backward",
     "tpmlp_selftest_stall_loads",
 )
@@ -74,6 +78,11 @@ class tpmlp_fp8_quant(ctypes.Structure):
 
 class tpmlp_fp8_formats(ctypes.Structure):
     _fields_ = [("x", ctypes.c_int32), ("w", ctypes.c_int32), ("dy", ctypes.c_int32)]
+
+
+class tpmlp_fp4_quant(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("parts", ctypes.c_int32),
+                ("gather", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
 class tpmlp_norm_params(ctypes.Structure):
@@ -186,6 +195,33 @@ _lib.tpmlp_fp8_column_linear_backward.argtypes = [_ldims_p, _fmt_p, _vpp, _vp, _
 _lib.tpmlp_fp8_row_linear_backward.restype = ctypes.c_int
 _lib.tpmlp_fp8_row_linear_backward.argtypes = [_ldims_p, _fmt_p, _vpp, _vpp, _vpp, _vpp, _vpp,
                                                _vpp, _vpp, _vp, _vp, _vp]
+
+_quant4_p = ctypes.POINTER(tpmlp_fp4_quant)
+_lib.tpmlp_fp4_packed_bytes.restype = ctypes.c_size_t
+_lib.tpmlp_fp4_packed_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64]
+_lib.tpmlp_fp4_scale_bytes.restype = ctypes.c_size_t
+_lib.tpmlp_fp4_scale_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
+_lib.tpmlp_fp4_tensor_scale.restype = ctypes.c_int
+_lib.tpmlp_fp4_tensor_scale.argtypes = [_quant4_p, _vpp, _vp, _vp]
+_lib.tpmlp_fp4_quantize.restype = ctypes.c_int
+_lib.tpmlp_fp4_quantize.argtypes = [_quant4_p, _vpp, _vp, _vpp, _vpp, _vpp, _vpp, _vp]
+_lib.tpmlp_fp4_dequantize.restype = ctypes.c_int
+_lib.tpmlp_fp4_dequantize.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, _vp, _vp, _vp, _vp,
+                                      _vp]
+_lib.tpmlp_fp4_linear_workspace_bytes.restype = ctypes.c_size_t
+_lib.tpmlp_fp4_linear_workspace_bytes.argtypes = [_ldims_p, ctypes.c_int, ctypes.c_int]
+_lib.tpmlp_fp4_column_linear_forward.restype = ctypes.c_int
+_lib.tpmlp_fp4_column_linear_forward.argtypes = [_ldims_p, ctypes.c_int, _vpp, _vp, ctypes.c_int, _vp, _vp,
+                                                 _vpp, _vpp, _vp, _vp, _vpp, _vp, _vp]
+_lib.tpmlp_fp4_row_linear_forward.restype = ctypes.c_int
+_lib.tpmlp_fp4_row_linear_forward.argtypes = [_ldims_p, ctypes.c_int, _vpp, _vp, ctypes.c_int, _vpp, _vpp,
+                                              _vpp, _vpp, _vp, _vp, _vpp, _vp, _vp]
+_lib.tpmlp_fp4_column_linear_backward.restype = ctypes.c_int
+_lib.tpmlp_fp4_column_linear_backward.argtypes = [_ldims_p, ctypes.c_int, _vpp, _vp, _vp, _vp, _vpp, _vpp,
+                                                  _vp, _vpp, _vpp, _vp, _vp, _vp]
+_lib.tpmlp_fp4_row_linear_backward.restype = ctypes.c_int
+_lib.tpmlp_fp4_row_linear_backward.argtypes = [_ldims_p, ctypes.c_int, _vpp, _vpp, _vpp, _vp, _vpp, _vpp,
+                                               _vp, _vpp, _vpp, _vp, _vp, _vp]
 
 _norm_p = ctypes.POINTER(tpmlp_norm_params)
 _lib.tpmlp_norm_workspace_bytes.restype = ctypes.c_size_t
@@ -542,6 +578,76 @@ def tpmlp_fp8_row_linear_backward(dims, formats, dZ, Xq_shards, Xs_shards, Wq_sh
         ctypes.byref(dims), ctypes.byref(formats), _arr(dZ), _arr(Xq_shards), _arr(Xs_shards),
         _arr(Wq_shards), _arr(Ws_shards), _arr(dX_shards), _arr(dW_shards), _ptr(db),
         _ptr(workspace), _stream(stream)), "tpmlp_fp8_row_linear_backward")
+
+
+FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
+
+
+def make_fp4_quant(rows: int, cols: int, parts: int = 1, gather: bool = False,
+                   fmt: int = 0) -> tpmlp_fp4_quant:
+    return tpmlp_fp4_quant(int(rows), int(cols), int(parts), int(gather), int(fmt))
+
+
+def tpmlp_fp4_packed_bytes(rows: int, k: int) -> int:
+    return int(_lib.tpmlp_fp4_packed_bytes(int(rows), int(k)))
+
+
+def tpmlp_fp4_scale_bytes(rows: int, k: int, fmt: int) -> int:
+    return int(_lib.tpmlp_fp4_scale_bytes(int(rows), int(k), int(fmt)))
+
+
+def tpmlp_fp4_tensor_scale(quant, src, scale, stream=None) -> None:
+    _check(_lib.tpmlp_fp4_tensor_scale(ctypes.byref(quant), _arr(src), _ptr(scale), _stream(stream)),
+           "tpmlp_fp4_tensor_scale")
+
+
+def tpmlp_fp4_quantize(quant, src, scale, q_rows, s_rows, q_cols, s_cols, stream=None) -> None:
+    """src: quant.parts tensors; the outputs: as many, or one with quant.gather; the row pair
+    or the column pair may be None."""
+    _check(_lib.tpmlp_fp4_quantize(ctypes.byref(quant), _arr(src), _ptr(scale), _opt(q_rows), _opt(s_rows),
+                                   _opt(q_cols), _opt(s_cols), _stream(stream)), "tpmlp_fp4_quantize")
+
+
+def tpmlp_fp4_dequantize(rows: int, k: int, fmt: int, q, s, scale, out, stream=None) -> None:
+    _check(_lib.tpmlp_fp4_dequantize(int(rows), int(k), int(fmt), _ptr(q), _ptr(s), _ptr(scale), _ptr(out),
+                                     _stream(stream)), "tpmlp_fp4_dequantize")
+
+
+def tpmlp_fp4_linear_workspace_bytes(dims: tpmlp_linear_dims, fmt: int, backward: bool) -> int:
+    """Scratch bytes of the 4-bit linear calls with these dims (0 if invalid)."""
+    return int(_lib.tpmlp_fp4_linear_workspace_bytes(ctypes.byref(dims), int(fmt), int(backward)))
+
+
+def tpmlp_fp4_column_linear_forward(dims, fmt: int, X, x_scale, x_calibrated, Xq, Xs, Wq_shards, Ws_shards,
+                                    w_scale, b, Y_shards, workspace, stream=None) -> None:
+    _check(_lib.tpmlp_fp4_column_linear_forward(
+        ctypes.byref(dims), fmt, _arr(X), _ptr(x_scale), int(x_calibrated), _ptr(Xq), _ptr(Xs),
+        _arr(Wq_shards), _arr(Ws_shards), _ptr(w_scale), _ptr(b), _arr(Y_shards), _ptr(workspace),
+        _stream(stream)), "tpmlp_fp4_column_linear_forward")
+
+
+def tpmlp_fp4_row_linear_forward(dims, fmt: int, X_shards, x_scale, x_calibrated, Xq_shards, Xs_shards,
+                                 Wq_shards, Ws_shards, w_scale, b, Z, workspace, stream=None) -> None:
+    _check(_lib.tpmlp_fp4_row_linear_forward(
+        ctypes.byref(dims), fmt, _arr(X_shards), _ptr(x_scale), int(x_calibrated), _opt(Xq_shards),
+        _opt(Xs_shards), _arr(Wq_shards), _arr(Ws_shards), _ptr(w_scale), _ptr(b), _arr(Z),
+        _ptr(workspace), _stream(stream)), "tpmlp_fp4_row_linear_forward")
+
+
+def tpmlp_fp4_column_linear_backward(dims, fmt: int, dY_shards, Xq, Xs, x_scale, Wq_shards, Ws_shards,
+                                     w_scale, dX, dW_shards, db, workspace, stream=None) -> None:
+    _check(_lib.tpmlp_fp4_column_linear_backward(
+        ctypes.byref(dims), fmt, _arr(dY_shards), _ptr(Xq), _ptr(Xs), _ptr(x_scale), _arr(Wq_shards),
+        _arr(Ws_shards), _ptr(w_scale), _arr(dX), _arr(dW_shards), _ptr(db), _ptr(workspace),
+        _stream(stream)), "tpmlp_fp4_column_linear_backward")
+
+
+def tpmlp_fp4_row_linear_backward(dims, fmt: int, dZ, Xq_shards, Xs_shards, x_scale, Wq_shards, Ws_shards,
+                                  w_scale, dX_shards, dW_shards, db, workspace, stream=None) -> None:
+    _check(_lib.tpmlp_fp4_row_linear_backward(
+        ctypes.byref(dims), fmt, _arr(dZ), _arr(Xq_shards), _arr(Xs_shards), _ptr(x_scale),
+        _arr(Wq_shards), _arr(Ws_shards), _ptr(w_scale), _arr(dX_shards), _arr(dW_shards), _ptr(db),
+        _ptr(workspace), _stream(stream)), "tpmlp_fp4_row_linear_backward")
 
 
 NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
