@@ -594,6 +594,43 @@ tpmlp_status tpmlp_norm_backward(const tpmlp_norm_params* params, const void* co
                                  void* dpre_gamma, void* dpre_beta, void* workspace,
                                  void* stream);
 
+/* ---- Norm of all gradients, and clipping by it -------------------------------------
+ * Before an optimiser's step: the Euclidean norm of a list of gradients together, and
+ *
+ *   out = grad * min(1, max_norm / (norm + 1e-6))
+ *
+ * for each of them, in the gradient's own type (the product in fp32, rounded once).  out may
+ * be grad itself; it may not lie over any other tensor of the list, nor may a tensor be in
+ * the list twice.  Tensors are contiguous, of any size (0 too, and then any pointer), and start
+ * on a multiple of their element's size.  Squares are summed in fp32 over at most 64 elements
+ * and in 64 bits from there (in 64 bits at once where fp32 would overflow or lose them), in an
+ * order that depends on sizes and alignment alone.  A NaN makes the norm and everything clipped
+ * NaN; an infinity makes the norm infinite and what is clipped 0 (infinities NaN).  In place,
+ * gradients whose factor is 1 are not written.
+ *   norm       fp32 [1] on the device (output; infinite where the norm is past fp32's range,
+ *              which clipping is not bound to)
+ *   max_norm   finite, >= 0
+ *   workspace  tpmlp_grad_workspace_bytes(n) bytes of scratch of one call
+ * At most 65536 tensors of at most 2^40 elements (else TPMLP_ERR_UNSUPPORTED). */
+typedef enum {
+    TPMLP_GRAD_F32 = 0,
+    TPMLP_GRAD_BF16 = 1,
+    TPMLP_GRAD_F16 = 2
+} tpmlp_grad_type;
+
+typedef struct {
+    const void* grad;
+    void* out;      /* read by tpmlp_grad_clip only */
+    int64_t count;  /* elements */
+    int32_t type;   /* tpmlp_grad_type */
+} tpmlp_grad_tensor;
+
+size_t tpmlp_grad_workspace_bytes(int64_t tensors);
+tpmlp_status tpmlp_grad_norm(const tpmlp_grad_tensor* tensors, int64_t n, void* norm, void* workspace,
+                             void* stream);
+tpmlp_status tpmlp_grad_clip(const tpmlp_grad_tensor* tensors, int64_t n, float max_norm, void* norm,
+                             void* workspace, void* stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* tpmlp_status_string(tpmlp_status s);
 
@@ -644,7 +681,7 @@ tpmlp_status tpmlp_set_wide_tiles(int mode);
  * address, element type, extents, strides, box, swizzle), so a repeated call
  * on the same buffers encodes nothing.  A buffer at a new address is a new key
  * (a stale entry is never used for another address); the operands of the 8-bit
- * layers share one map for each shape, and each call sets the address in its own
+ * and 4-bit layers share one map for each shape, and each call sets the address in its own
  * copy.  At most 4096 maps are
  * kept; when the cache is full it is emptied.  Thread-safe (one mutex).
  * tpmlp_map_cache_stats reports the hits, misses (encodings) and entries so
@@ -674,7 +711,7 @@ tpmlp_status tpmlp_set_wait_timeout_ns(uint64_t ns);
 tpmlp_status tpmlp_selftest_stalled_gemm(const void* a, const void* b, void* c,
                                          uint64_t timeout_ns, void* stream);
 
-/* The same for the products of the 8-bit linear layers and the norms around a block:
+/* The same for the products of the 8-bit and 4-bit linear layers and the norms around a block:
  * after this call, those that the calling thread launches stop loading in the last
  * CTA of each cluster after `copies` (>= 0) steps (K blocks, or rows), so that what
  * waits for the rest gives up at the limit
@@ -739,14 +776,14 @@ enum {
     TPMLP_KERNEL_DGRAD_X = 3,     /* dX = sum_i dY_i.A_i^T */
     TPMLP_KERNEL_WGRAD_B = 4,     /* dB_i = H_i^T.dZ */
     TPMLP_KERNEL_WGRAD_A = 5,     /* dA_i = X^T.dY_i */
-    TPMLP_KERNEL_BIAS_GRAD = 6,   /* db1, db2, linear db column sums (all launches) */
-    TPMLP_KERNEL_LINEAR_FWD = 7,  /* linear layers (bf16, 8-bit): Y_i = X.W_i + b, Z = sum_i X_i.W_i + b */
-    TPMLP_KERNEL_LINEAR_DGRAD = 8,  /* linear layers (bf16, 8-bit): dX = sum_i dY_i.W_i^T, dX_i = dZ.W_i^T */
-    TPMLP_KERNEL_LINEAR_WGRAD = 9,  /* linear layers (bf16, 8-bit): dW_i */
+    TPMLP_KERNEL_BIAS_GRAD = 6,   /* db1, db2, linear db column sums; gradient norm and clipping (all launches) */
+    TPMLP_KERNEL_LINEAR_FWD = 7,  /* linear layers (bf16, 8-bit, 4-bit): Y_i = X.W_i + b, Z = sum_i X_i.W_i + b */
+    TPMLP_KERNEL_LINEAR_DGRAD = 8,  /* linear layers (bf16, 8-bit, 4-bit): dX = sum_i dY_i.W_i^T, dX_i = dZ.W_i^T */
+    TPMLP_KERNEL_LINEAR_WGRAD = 9,  /* linear layers (bf16, 8-bit, 4-bit): dW_i */
     TPMLP_KERNEL_LAYERNORM_FWD = 10,  /* sequence-parallel sublayer: LN(X) and row statistics; tpmlp_norm_forward */
     TPMLP_KERNEL_LAYERNORM_BWD = 11,  /* sequence-parallel sublayer: dX, dgamma, dbeta (2 launches; 3 for h > 4096); tpmlp_norm_backward (2; 1 with no norm and no gate to add up) */
     TPMLP_KERNEL_DROPOUT_BWD = 12,    /* sequence-parallel sublayer: dZ from dOut and the mask, db2 (2 launches) */
-    TPMLP_KERNEL_SP_COPY = 13,        /* tpmlp_sp_gather / tpmlp_sp_scatter, 8-bit quantisation */
+    TPMLP_KERNEL_SP_COPY = 13,        /* tpmlp_sp_gather / tpmlp_sp_scatter, 8-bit and 4-bit quantisation and back */
     TPMLP_KERNEL_KINDS = 14
 };
 tpmlp_status tpmlp_profile_begin(int capacity);

@@ -49,6 +49,7 @@ EXPORTED = (
     "tpmlp_fp4_dequantize", "tpmlp_fp4_linear_workspace_bytes",
     "tpmlp_fp4_column_linear_forward", "tpmlp_fp4_column_linear_backward",
     "tpmlp_fp4_row_linear_forward", "tpmlp_fp4_row_linear_backward",
+    "tpmlp_grad_workspace_bytes", "tpmlp_grad_norm", "tpmlp_grad_clip",
     "tpmlp_norm_workspace_bytes", "tpmlp_norm_forward", "tpmlp_norm_backward",
     "tpmlp_selftest_stall_loads",
 )
@@ -83,6 +84,11 @@ class tpmlp_fp8_formats(ctypes.Structure):
 class tpmlp_fp4_quant(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("parts", ctypes.c_int32),
                 ("gather", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class tpmlp_grad_tensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("type", ctypes.c_int32)]
 
 
 class tpmlp_norm_params(ctypes.Structure):
@@ -222,6 +228,14 @@ _lib.tpmlp_fp4_column_linear_backward.argtypes = [_ldims_p, ctypes.c_int, _vpp, 
 _lib.tpmlp_fp4_row_linear_backward.restype = ctypes.c_int
 _lib.tpmlp_fp4_row_linear_backward.argtypes = [_ldims_p, ctypes.c_int, _vpp, _vpp, _vpp, _vp, _vpp, _vpp,
                                                _vp, _vpp, _vpp, _vp, _vp, _vp]
+
+_grad_p = ctypes.POINTER(tpmlp_grad_tensor)
+_lib.tpmlp_grad_workspace_bytes.restype = ctypes.c_size_t
+_lib.tpmlp_grad_workspace_bytes.argtypes = [ctypes.c_int64]
+_lib.tpmlp_grad_norm.restype = ctypes.c_int
+_lib.tpmlp_grad_norm.argtypes = [_grad_p, ctypes.c_int64, _vp, _vp, _vp]
+_lib.tpmlp_grad_clip.restype = ctypes.c_int
+_lib.tpmlp_grad_clip.argtypes = [_grad_p, ctypes.c_int64, ctypes.c_float, _vp, _vp, _vp]
 
 _norm_p = ctypes.POINTER(tpmlp_norm_params)
 _lib.tpmlp_norm_workspace_bytes.restype = ctypes.c_size_t
@@ -648,6 +662,29 @@ def tpmlp_fp4_row_linear_backward(dims, fmt: int, dZ, Xq_shards, Xs_shards, x_sc
         ctypes.byref(dims), fmt, _arr(dZ), _arr(Xq_shards), _arr(Xs_shards), _ptr(x_scale),
         _arr(Wq_shards), _arr(Ws_shards), _ptr(w_scale), _arr(dX_shards), _arr(dW_shards), _ptr(db),
         _ptr(workspace), _stream(stream)), "tpmlp_fp4_row_linear_backward")
+
+
+GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def make_grad_tensors(tensors):
+    """An array of (grad, out, count, type): pointers or tensors, a number, a code."""
+    return (tpmlp_grad_tensor * max(len(tensors), 1))(
+        *[tpmlp_grad_tensor(_ptr(g), _ptr(o), int(n), int(code)) for g, o, n, code in tensors])
+
+
+def tpmlp_grad_workspace_bytes(tensors: int) -> int:
+    return int(_lib.tpmlp_grad_workspace_bytes(int(tensors)))
+
+
+def tpmlp_grad_norm(tensors, n: int, norm, workspace, stream=None) -> None:
+    _check(_lib.tpmlp_grad_norm(tensors, n, _ptr(norm), _ptr(workspace), _stream(stream)),
+           "tpmlp_grad_norm")
+
+
+def tpmlp_grad_clip(tensors, n: int, max_norm: float, norm, workspace, stream=None) -> None:
+    _check(_lib.tpmlp_grad_clip(tensors, n, max_norm, _ptr(norm), _ptr(workspace), _stream(stream)),
+           "tpmlp_grad_clip")
 
 
 NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}

@@ -1,0 +1,82 @@
+"""The norm of a list of gradients together, and clipping by it, before an optimiser's step.
+
+PyTorch is used for device memory and streams only; both run in libtpmlp through
+:mod:`binding` (include/tpmlp.h):
+
+  norm = sqrt(sum over all tensors of grad^2)
+  out  = grad * min(1, max_norm / (norm + 1e-6))
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding
+
+
+def _flat(x: torch.Tensor, what: str):
+    if x.dtype not in binding.GRAD_TYPES or not x.is_contiguous() or not x.is_cuda:
+        raise ValueError(f"{what} must be contiguous fp32, bf16 or fp16 CUDA tensors, got {x.dtype} "
+                         f"{tuple(x.shape)} {'' if x.is_contiguous() else 'not contiguous '}on {x.device}")
+
+
+def _check_apart(grads, outs) -> None:
+    """Nothing is written over what another entry reads or writes."""
+    spans = []
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if g.numel():
+            n = g.numel() * g.element_size()
+            spans.append((g.data_ptr(), g.data_ptr() + n, i))
+            if o.data_ptr() != g.data_ptr():
+                spans.append((o.data_ptr(), o.data_ptr() + n, i))
+    spans.sort()
+    for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError(f"gradients and outputs lie over each other (numbers {i} and {j} of the list)")
+
+
+class DeviceGradients:
+    """A list of gradients (fp32, bf16, fp16; any sizes) that are clipped together.
+
+    out: where the clipped ones go, tensors of the same shapes and types, or None: in place.
+    ``norm``: fp32 [1] on the device, written by both calls."""
+
+    def __init__(self, grads, out=None):
+        self.grads = tuple(grads)
+        self.out = self.grads if out is None else tuple(out)
+        if not self.grads:
+            raise ValueError("at least one gradient is needed")
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} outputs are needed, got {len(self.out)}")
+        self.device = dev = self.grads[0].device
+        for g, o in zip(self.grads, self.out):
+            _flat(g, "gradients")
+            if o is not g:
+                _flat(o, "outputs")
+            if g.device != dev or o.device != dev or o.dtype != g.dtype or o.shape != g.shape:
+                raise ValueError(f"gradients lie on one device, outputs have their shape and type: got "
+                                 f"{g.dtype} {tuple(g.shape)} on {g.device}, {o.dtype} {tuple(o.shape)} on "
+                                 f"{o.device}")
+        _check_apart(self.grads, self.out)
+        n = len(self.grads)
+        need = binding.tpmlp_grad_workspace_bytes(n)
+        if need == 0:
+            raise ValueError(f"too many gradients for a call: {n}")
+        # (marshalled once, so the object keeps the tensors)
+        self._tensors = binding.make_grad_tensors(
+            [(g, o, g.numel(), binding.GRAD_TYPES[g.dtype]) for g, o in zip(self.grads, self.out)])
+        self.norm = torch.empty(1, dtype=torch.float32, device=dev)
+        self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
+
+    def measure(self, stream=None) -> torch.Tensor:
+        """The norm, without clipping."""
+        with binding.on_device(self.device):
+            binding.tpmlp_grad_norm(self._tensors, len(self.grads), self.norm, self.ws,
+                                    binding.stream_on(self.device, stream))
+        return self.norm
+
+    def clip(self, max_norm: float, stream=None) -> torch.Tensor:
+        """Writes the clipped gradients; returns the norm before clipping."""
+        with binding.on_device(self.device):
+            binding.tpmlp_grad_clip(self._tensors, len(self.grads), max_norm, self.norm, self.ws,
+                                    binding.stream_on(self.device, stream))
+        return self.norm
