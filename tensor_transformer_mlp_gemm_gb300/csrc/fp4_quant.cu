@@ -9,18 +9,17 @@
 // the rows a thread holds 8 rows x 8 columns as eight 16-byte loads, all in flight before
 // the first use.  For the columns the tile goes through shared memory, and a thread takes
 // 32 rows of two columns, which is 16 bytes of each column's output.
-#include "fp4_quant.cuh"
+#include <cuda_fp16.h>
 
+#include "fp4_quant.cuh"
 #include "fp8_cvt.cuh"
 #include "ptx.cuh"
 
 namespace tpmlp {
 namespace {
 
-using q8::fold;
 using q8::hi_f;
 using q8::kMagnitudes;
-using q8::largest;
 using q8::lo_f;
 
 constexpr int QT = 256;  // threads
@@ -28,6 +27,18 @@ constexpr int TILE = 128;
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// The larger magnitude of two pairs of bf16, with some sign; NaN (0x7FFF) where either is.
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// the largest magnitude's bits among a pair, among 8 values
+__device__ __forceinline__ uint32_t fold(uint32_t w) { return larger(w, w >> 16) & 0x7FFFu; }
+__device__ __forceinline__ uint32_t largest(const uint4& v) {
+    return fold(larger(larger(v.x, v.y), larger(v.z, v.w)));
 }
 
 // A group's scale: its byte, and what its values are multiplied by (0: not finite).
@@ -57,12 +68,17 @@ __device__ __forceinline__ Scale4 scale_of(uint32_t amax, float inv_g) {
             r.inv = 0.0f;
         }
     } else {
-        // the quotient's rounding leaves ties where they are: a border has 5 significant bits
-        const float v = __fdiv_rn(__uint_as_float(amax << 16) * inv_g, 6.0f);
+        // amax / 6 as a product with a rounded 1 / 6, then rounded to 12 significant bits
+        // (Veltkamp's splitting): a border between two e4m3 values has 5, and a quotient that
+        // is not on it is 2^-9 of it away.  (4096 / 6 is past the largest scale.)
+        const float v = fminf(__uint_as_float(amax << 16) * inv_g, 4096.0f) * (1.0f / 6.0f);
+        const float t = __fmul_rn(v, 4097.0f), w = __fsub_rn(t, __fsub_rn(t, v));
         uint16_t b;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.0f), "f"(v));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.0f), "f"(w));
         r.byte = max(static_cast<uint32_t>(b), 1u);
-        r.inv = __frcp_rn(e4m3_f(r.byte)) * inv_g;
+        float inv_s;  // (off by 2^-23 at most)
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv_s) : "f"(e4m3_f(r.byte)));
+        r.inv = inv_s * inv_g;
         if (amax >= 0x7F80u || inv_g == 0.0f) {
             r.byte = 0x7Fu;
             r.inv = 0.0f;
@@ -78,7 +94,7 @@ __device__ __forceinline__ float inverse_of(const float* g) {
 }
 
 // x * inv in both halves.  Of nv, inv is a rounded reciprocal, so the product of an x on a
-// border may miss it by a few 2^-24: it is rounded to multiples of 2^-16, which borders are,
+// border may miss it by a few 2^-22: it is rounded to multiples of 2^-16, which borders are,
 // and which no other quotient (2^-9 of a border away) reaches a border by.
 template <int FMT>
 __device__ __forceinline__ float2 scaled(float2 x, float inv) {
@@ -165,13 +181,13 @@ __global__ void __launch_bounds__(QT, per_sm(MODE))
 #pragma unroll
         for (int o = 1; o < 4 / PER; o <<= 1)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) rm[i] = __vmaxu2(rm[i], __shfl_xor_sync(0xffffffffu, rm[i], o));
+            for (int i = 0; i < 4; ++i) rm[i] = larger(rm[i], __shfl_xor_sync(0xffffffffu, rm[i], o));
         const uint32_t group = PER == 2 ? cv >> 1 : cv >> 2;
         uint8_t* q = p.q_rows[part];
         const long long ld = fp4_ld(p.cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const Scale4 sc = scale_of<FMT>(i & 1 ? rm[i / 2] >> 16 : rm[i / 2] & 0xFFFFu, inv_g);
+            const Scale4 sc = scale_of<FMT>((i & 1 ? rm[i / 2] >> 16 : rm[i / 2]) & 0x7FFFu, inv_g);
             const int r = slot + 16 * i;
             if (cv % (4 / PER) == 0) s_rows[scale_at(r, group)] = static_cast<uint8_t>(sc.byte);
             if (col_in && r0 + r < total) {
@@ -214,9 +230,9 @@ __global__ void __launch_bounds__(QT, per_sm(MODE))
         uint32_t m[PER];
 #pragma unroll
         for (int h = 0; h < PER; ++h) {
-            m[h] = 0;
+            m[h] = w[h * (32 / PER)];
 #pragma unroll
-            for (int k = 0; k < 32 / PER; ++k) m[h] = __vmaxu2(m[h], w[h * (32 / PER) + k] & kMagnitudes);
+            for (int k = 1; k < 32 / PER; ++k) m[h] = larger(m[h], w[h * (32 / PER) + k]);
         }
 #pragma unroll
         for (int side = 0; side < 2; ++side) {  // the even column, the odd one
@@ -224,7 +240,7 @@ __global__ void __launch_bounds__(QT, per_sm(MODE))
             Scale4 sc[PER];
 #pragma unroll
             for (int h = 0; h < PER; ++h) {
-                sc[h] = scale_of<FMT>(side ? m[h] >> 16 : m[h] & 0xFFFFu, inv_g);
+                sc[h] = scale_of<FMT>((side ? m[h] >> 16 : m[h]) & 0x7FFFu, inv_g);
                 s_cols[scale_at(2 * cp + side, g * PER + h)] = static_cast<uint8_t>(sc[h].byte);
             }
 #pragma unroll
@@ -339,51 +355,71 @@ __global__ void __launch_bounds__(MT, M_PER_SM)
 
 // ---- back ----------------------------------------------------------------------------
 
-// A thread takes 16 values of a row: 8 bytes, one group of nv or half of one of mx.
+// A CTA takes 128 rows by 256 of K, whose scales lie next to each other; a warp a row at a
+// time, 8 values a lane, sixteen rows' values under way before the first use.
+constexpr int DT = 256, D_ROWS = 128 / (DT / 32);
+
 template <int FMT>
-__global__ void __launch_bounds__(QT)
-    fp4_dequant_kernel(long long R, long long K, const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
-                       const float* __restrict__ scale, uint16_t* __restrict__ out) {
+__global__ void __launch_bounds__(DT, 4)
+    fp4_dequant_kernel(long long R, long long K, int kblocks, const uint8_t* __restrict__ q,
+                       const uint8_t* __restrict__ s, const float* __restrict__ scale,
+                       uint16_t* __restrict__ out) {
+    __shared__ uint4 s_scales[fp4_scale_step(FMT) / 16];
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const long long per_row = (K + 15) / 16;
-    const long long i = static_cast<long long>(blockIdx.x) * QT + threadIdx.x;
-    if (i >= R * per_row) return;
-    const long long r = i / per_row, k0 = (i - r * per_row) * 16;
-    const long long group = k0 / fp4_group(FMT);
-    const uint32_t byte = __ldg(s + (r >> 7) * ((K + 255) / 256) * fp4_scale_step(FMT) + (group >> 2) * 512 +
-                                (r & 31) * 16 + ((r >> 5) & 3) * 4 + (group & 3));
-    float f;
-    if constexpr (FMT == FP4_MX) {
-        f = __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);
-    } else {
-        const float inv = inverse_of(scale);
-        f = byte >= 0x7F || inv == 0.0f ? __uint_as_float(0x7FC00000u) : e4m3_f(byte) * __ldg(scale);
-    }
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(q + r * fp4_ld(K) + k0 / 2));
-    uint32_t o[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long rt = blockIdx.x / kblocks;
+    const int kb = static_cast<int>(blockIdx.x % kblocks);
+    const long long r0 = rt * 128 + warp, k = kb * 256LL + lane * 8;
+    const long long ld = fp4_ld(K);
+    const bool in = k < K;
+    const uint8_t* from = q + r0 * ld + k / 2;
+    uint32_t u[D_ROWS];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t b = (j < 4 ? u.x >> (8 * j) : u.y >> (8 * (j - 4))) & 0xFFu;
-        // value = (-1)^sign * (exponent ? 2^(exponent - 1) (1 + m / 2) : m / 2)
-        float x[2];
+    for (int i = 0; i < D_ROWS; ++i)
+        u[i] = in && r0 + 8 * i < R ? __ldg(reinterpret_cast<const uint32_t*>(from + 8 * i * ld)) : 0u;
+    if (threadIdx.x < fp4_scale_step(FMT) / 16)
+        s_scales[threadIdx.x] = __ldg(reinterpret_cast<const uint4*>(s) +
+                                      static_cast<long long>(blockIdx.x) * (fp4_scale_step(FMT) / 16) + threadIdx.x);
+    float g = 1.0f;
+    if constexpr (FMT == FP4_NV) g = inverse_of(scale) == 0.0f ? __uint_as_float(0x7FC00000u) : __ldg(scale);
+    __syncthreads();
+    if (!in) return;
+    const uint8_t* scales = reinterpret_cast<const uint8_t*>(s_scales);
+    const uint32_t group = lane * 8 / fp4_group(FMT);
+    const bool whole = k + 8 <= K && K % 8 == 0;
+    uint16_t* to = out + r0 * K + k;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t n = h ? b >> 4 : b & 15u, mag = n & 7u;
-            const float a = mag < 2 ? 0.5f * static_cast<float>(mag) : __uint_as_float((mag << 22) + (126u << 23));
-            x[h] = (n & 8u ? -a : a) * f;
+    for (int i = 0; i < D_ROWS; ++i) {
+        if (r0 + 8 * i >= R) break;
+        const uint32_t byte = scales[scale_at(warp + 8 * i, group)];
+        float f;
+        if constexpr (FMT == FP4_MX)
+            f = __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);
+        else
+            f = byte >= 0x7F ? __uint_as_float(0x7FC00000u) : e4m3_f(byte) * g;
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t h;
+            asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+                "mov.b32 {a, b, c, d}, %1;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
+                : "=r"(h)
+                : "r"(u[i] >> (8 * j)));
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            const float2 y = __fmul2_rn(x, make_float2(f, f));
+            // (exact: 6 significant bits)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(y.y), "f"(y.x));
         }
-        // (exact: 6 significant bits)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(x[1]), "f"(x[0]));
-    }
-    uint16_t* to = out + r * K + k0;
-    if (K % 16 == 0) {
-        reinterpret_cast<uint4*>(to)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        reinterpret_cast<uint4*>(to)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    } else {
+        uint16_t* row = to + 8 * i * K;
+        if (whole) {
+            *reinterpret_cast<uint4*>(row) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (k0 + j < K) to[j] = static_cast<uint16_t>(j & 1 ? o[j / 2] >> 16 : o[j / 2]);
+            for (int j = 0; j < 8; ++j)
+                if (k + j < K) row[j] = static_cast<uint16_t>(j & 1 ? o[j / 2] >> 16 : o[j / 2]);
+        }
     }
 }
 
@@ -411,11 +447,11 @@ cudaError_t launch_fp4_tensor_scale(const Fp4QuantParams& p, float* scale, cudaS
 
 cudaError_t launch_fp4_dequant(long long R, long long K, int fmt, const void* q, const void* s,
                                const float* scale, void* out, cudaStream_t st) {
-    const long long ctas = (R * ((K + 15) / 16) + QT - 1) / QT;
-    if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    const long long kb = (K + 255) / 256, rt = (R + 127) / 128;
+    if (rt > 0x7FFFFFFFLL / kb) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-    cfg.blockDim = dim3(QT, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(rt * kb), 1, 1);
+    cfg.blockDim = dim3(DT, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -423,7 +459,7 @@ cudaError_t launch_fp4_dequant(long long R, long long K, int fmt, const void* q,
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     auto kern = fmt == FP4_NV ? fp4_dequant_kernel<FP4_NV> : fp4_dequant_kernel<FP4_MX>;
-    return cudaLaunchKernelEx(&cfg, kern, R, K, static_cast<const uint8_t*>(q),
+    return cudaLaunchKernelEx(&cfg, kern, R, K, static_cast<int>(kb), static_cast<const uint8_t*>(q),
                               static_cast<const uint8_t*>(s), scale, static_cast<uint16_t*>(out));
 }
 

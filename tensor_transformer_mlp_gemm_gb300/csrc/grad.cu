@@ -39,6 +39,9 @@ constexpr int G_VECS = 8;        // vectors of a thread in the largest chunk
 constexpr int G_CTAS = 1024;     // at most (partial sums of a launch)
 constexpr int G_FEW = 32, G_MANY = 512;  // tensors in a launch's arguments
 constexpr int64_t G_TENSORS = 65536;     // in a call
+// Bytes at the end that the first pass leaves in L2 like any others; what lies before them is
+// marked as the first to go.  (4096 x 16384 block in fp32: 87 us, all alike 93.)
+constexpr unsigned G_KEEP = 50u << 20;
 constexpr double G_EPS = 1e-6;
 
 // The tensors of one launch.
@@ -101,6 +104,39 @@ __device__ __forceinline__ uint4 load_vector(const Chunk& k, uintptr_t a) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A load whose line is the first to leave L2.
+__device__ __forceinline__ uint4 load_once(const uint4* a) {
+    uint64_t policy;
+    uint4 v;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(a), "l"(policy));
+    return v;
+}
+
+// This thread's vectors of a chunk.  In one that its tensor fills they are loaded without a
+// test between them, all in flight before the first use.
+template <int N>
+__device__ __forceinline__ void load_chunk(const Tensors<N>& p, const Chunk& k, uint4 (&v)[G_VECS], bool keep) {
+    const uintptr_t a = k.base + threadIdx.x * 16;
+    const bool whole = k.base >= k.begin && k.base + static_cast<uintptr_t>(p.vecs) * (GT * 16) <= k.end;
+    if (whole && p.vecs == G_VECS) {
+        const uint4* src = reinterpret_cast<const uint4*>(a);
+        if (keep) {
+#pragma unroll
+            for (int u = 0; u < G_VECS; ++u) v[u] = __ldg(src + u * GT);
+        } else {
+#pragma unroll
+            for (int u = 0; u < G_VECS; ++u) v[u] = load_once(src + u * GT);
+        }
+        return;
+    }
+#pragma unroll
+    for (int u = 0; u < G_VECS; ++u)
+        v[u] = u < p.vecs ? load_vector(k, a + u * (GT * 16)) : make_uint4(0, 0, 0, 0);
+}
+
 // the two values of a word of bf16 or fp16
 __device__ __forceinline__ float2 halves(uint32_t w, int type) {
     if (type == TPMLP_GRAD_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -124,7 +160,7 @@ __device__ __forceinline__ float squares(const uint4& v, int type) {
     return s;
 }
 
-__device__ __noinline__ double squares64(const uint4& v, int type) {
+__device__ __noinline__ double squares64(uint4 v, int type) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     double s = 0.0;
     for (int j = 0; j < 4; ++j) {
@@ -136,109 +172,175 @@ __device__ __noinline__ double squares64(const uint4& v, int type) {
     return s;
 }
 
-// The sum over the CTA, in thread 0 (and nowhere else).
-__device__ __forceinline__ double block_sum(double x, double* s_sum) {
+// Each value of a vector times f e.
+__device__ __forceinline__ void scale(uint32_t (&w)[4], int type, float f, float e) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.0;
-    if (threadIdx.x == 0)
-        for (int w = 0; w < GT / 32; ++w) x += s_sum[w];
-    return x;
+    for (int j = 0; j < 4; ++j) {
+        if (type == TPMLP_GRAD_F32) {
+            w[j] = __float_as_uint(__uint_as_float(w[j]) * f * e);
+            continue;
+        }
+        const float2 y = halves(w[j], type);
+        if (type == TPMLP_GRAD_BF16) {
+            const __nv_bfloat162 z = __floats2bfloat162_rn(y.x * f * e, y.y * f * e);
+            w[j] = *reinterpret_cast<const uint32_t*>(&z);
+        } else {
+            const __half2 z = __floats2half2_rn(y.x * f * e, y.y * f * e);
+            w[j] = *reinterpret_cast<const uint32_t*>(&z);
+        }
+    }
 }
+
+// A sum in two fp32 parts (Knuth's two-sum), which hold it as well as 64 bits would: those run
+// at 1/64 of the rate here, and with 64-bit sums of the threads the smallest calls took twice
+// as long.
+struct Sum {
+    float hi, lo;
+    __device__ __forceinline__ void add(float x) {
+        const float t = __fadd_rn(hi, x), z = __fsub_rn(t, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, z)), __fsub_rn(x, z)));
+        hi = t;
+    }
+    template <int FIRST>
+    __device__ __forceinline__ void over_lanes() {
+#pragma unroll
+        for (int o = FIRST; o > 0; o >>= 1) {
+            const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
+            add(h);
+            lo = __fadd_rn(lo, l);
+        }
+    }
+};
 
 template <int N>
 __global__ void __launch_bounds__(GT, G_PER_SM)
-    grad_squares_kernel(const __grid_constant__ Tensors<N> p, double* __restrict__ partial) {
-    __shared__ double s_sum[GT / 32];
-    ptx::griddep_launch_dependents();
+    grad_squares_kernel(const __grid_constant__ Tensors<N> p, unsigned keep, double* __restrict__ partial) {
+    __shared__ Sum s_sum[GT / 32];
+    __shared__ double s_wide[GT / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     ptx::griddep_wait();
-    double acc = 0.0;
+    // (after the wait: the kernel that clips may then read the gradients before its own)
+    ptx::griddep_launch_dependents();
+    Sum acc = {0.0f, 0.0f};
+    double wide = 0.0;
     for (unsigned c = blockIdx.x; c < p.chunks; c += gridDim.x) {
         const Chunk k = chunk_of(p, c);
         uint4 v[G_VECS];
-#pragma unroll
-        for (int u = 0; u < G_VECS; ++u)
-            v[u] = u < p.vecs ? load_vector(k, k.base + (u * GT + threadIdx.x) * 16) : make_uint4(0, 0, 0, 0);
+        load_chunk(p, k, v, c + keep >= p.chunks);
         float s = 0.0f;
+        if (k.type == TPMLP_GRAD_F32) {
 #pragma unroll
-        for (int u = 0; u < G_VECS; ++u) s += squares(v[u], k.type);
-        // At most 64 squares: below 2^-126 each is off by at most 2^-150, 2^-34 of a sum of 2^-110.
-        if (s >= 7.7037197775489434e-34f && s <= 3.4028234663852886e38f) {
-            acc += static_cast<double>(s);
+            for (int u = 0; u < G_VECS; ++u) s += squares(v[u], TPMLP_GRAD_F32);
+        } else {
+#pragma unroll
+            for (int u = 0; u < G_VECS; ++u) s += squares(v[u], k.type);
+        }
+        // At most 64 squares: below 2^-126 each is off by at most 2^-150, 2^-34 of a sum of
+        // 2^-110; and no number of sums up to 2^90 overflows.
+        if (s >= 0x1p-110f && s <= 0x1p90f) {
+            acc.add(s);
         } else {
             uint32_t any = 0;
 #pragma unroll
             for (int u = 0; u < G_VECS; ++u) any |= v[u].x | v[u].y | v[u].z | v[u].w;
             if (any)
 #pragma unroll
-                for (int u = 0; u < G_VECS; ++u) acc += squares64(v[u], k.type);
+                for (int u = 0; u < G_VECS; ++u) wide += squares64(v[u], k.type);
         }
     }
-    const double sum = block_sum(acc, s_sum);
-    if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+    acc.over_lanes<16>();
+    if (lane == 0) s_sum[warp] = acc;
+    const bool any_wide = __syncthreads_or(wide != 0.0);  // (NaN too)
+    if (any_wide) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) wide += __shfl_xor_sync(0xffffffffu, wide, o);
+        if (lane == 0) s_wide[warp] = wide;
+        __syncthreads();
+    }
+    if (warp == 0) {
+        acc = s_sum[lane % (GT / 32)];
+        acc.over_lanes<GT / 64>();
+        if (lane == 0) {
+            double sum = static_cast<double>(acc.hi) + static_cast<double>(acc.lo);
+            if (any_wide)
+                for (int w = 0; w < GT / 32; ++w) sum += s_wide[w];
+            partial[blockIdx.x] = sum;
+        }
+    }
 }
 
-// The norm of all partial sums, in every thread.
-__device__ __forceinline__ double norm_of(const double* partial, int n, double* s_sum) {
-    double x = 0.0;
-    for (int i = threadIdx.x; i < n; i += GT) x += partial[i];
-    const double sum = block_sum(x, s_sum);
-    if (threadIdx.x == 0) s_sum[0] = sqrt(sum);
+// The norm of all partial sums, and max_norm / (norm + 1e-6), in every thread.
+struct Norm {
+    float norm;
+    double factor;
+};
+__device__ __forceinline__ Norm norm_of(const double* partial, int n, double max_norm, Norm* s_norm) {
+    if (threadIdx.x < 32) {
+        double x = 0.0;
+        for (int i = threadIdx.x; i < n; i += 32) x += partial[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (threadIdx.x == 0) {
+            if (x >= 1e-30 && x <= 1e30) {
+                // (roots and quotients in 64 bits take a microsecond)
+                s_norm->norm = sqrtf(static_cast<float>(x));
+                s_norm->factor = static_cast<float>(max_norm) / (s_norm->norm + static_cast<float>(G_EPS));
+            } else {
+                const double r = sqrt(x);
+                s_norm->norm = static_cast<float>(r);
+                s_norm->factor = max_norm / (r + G_EPS);
+            }
+        }
+    }
     __syncthreads();
-    return s_sum[0];
+    return *s_norm;
 }
 
 __global__ void __launch_bounds__(GT) grad_norm_kernel(const double* partial, int n, float* norm) {
-    __shared__ double s_sum[GT / 32];
+    __shared__ Norm s_norm;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const double x = norm_of(partial, n, s_sum);
-    if (threadIdx.x == 0) *norm = static_cast<float>(x);
+    const Norm x = norm_of(partial, n, 0.0, &s_norm);
+    if (threadIdx.x == 0) *norm = x.norm;
 }
 
 template <int N>
 __global__ void __launch_bounds__(GT, G_PER_SM)
     grad_scale_kernel(const __grid_constant__ Tensors<N> p, const double* __restrict__ partial, int n,
                       double max_norm, float* norm) {
-    __shared__ double s_sum[GT / 32];
+    __shared__ Norm s_norm;
     ptx::griddep_launch_dependents();
+    // the first chunk is on its way while the sums of squares end
+    Chunk k = chunk_of(p, p.chunks - 1 - blockIdx.x);
+    uint4 v[G_VECS];
+    load_chunk(p, k, v, true);
     ptx::griddep_wait();
-    const double x = norm_of(partial, n, s_sum);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(x);
-    const double q = max_norm / (x + G_EPS);
+    const Norm x = norm_of(partial, n, max_norm, &s_norm);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = x.norm;
+    const double q = x.factor;
     // in two factors: one below fp32's normal numbers would lose digits  (NaN stays)
     const bool tiny = q < 0x1p-100;
     const float f = q >= 1.0 ? 1.0f : static_cast<float>(tiny ? q * 0x1p64 : q), e = tiny ? 0x1p-64f : 1.0f;
     for (unsigned r = blockIdx.x; r < p.chunks; r += gridDim.x) {
-        const Chunk k = chunk_of(p, p.chunks - 1 - r);
+        if (r != blockIdx.x) {
+            k = chunk_of(p, p.chunks - 1 - r);
+            load_chunk(p, k, v, true);
+        }
         const uintptr_t to = reinterpret_cast<uintptr_t>(p.out[k.i]) - k.begin;  // (wraps)
         if (to == 0 && f == 1.0f) continue;  // in place, and nothing changes
-        uint4 v[G_VECS];
-#pragma unroll
-        for (int u = 0; u < G_VECS; ++u)
-            v[u] = u < p.vecs ? load_vector(k, k.base + (u * GT + threadIdx.x) * 16) : make_uint4(0, 0, 0, 0);
+        const bool plain = to % 16 == 0 && k.base >= k.begin &&
+                           k.base + static_cast<uintptr_t>(p.vecs) * (GT * 16) <= k.end;
 #pragma unroll
         for (int u = 0; u < G_VECS; ++u) {
             const uintptr_t a = k.base + (u * GT + threadIdx.x) * 16;
             uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (k.type == TPMLP_GRAD_F32) {
-                    w[j] = __float_as_uint(__uint_as_float(w[j]) * f * e);
-                } else {
-                    const float2 y = halves(w[j], k.type);
-                    if (k.type == TPMLP_GRAD_BF16) {
-                        const __nv_bfloat162 z = __floats2bfloat162_rn(y.x * f * e, y.y * f * e);
-                        w[j] = *reinterpret_cast<const uint32_t*>(&z);
-                    } else {
-                        const __half2 z = __floats2half2_rn(y.x * f * e, y.y * f * e);
-                        w[j] = *reinterpret_cast<const uint32_t*>(&z);
-                    }
-                }
+            scale(w, k.type, f, e);
+            if (u >= p.vecs) break;
+            if (plain) {
+                __stcs(reinterpret_cast<uint4*>(a + to), make_uint4(w[0], w[1], w[2], w[3]));
+                continue;
             }
-            if (u >= p.vecs || a + 16 <= k.begin || a >= k.end) continue;
+            if (a + 16 <= k.begin || a >= k.end) continue;
             if (a >= k.begin && a + 16 <= k.end && to % 16 == 0) {
                 __stcs(reinterpret_cast<uint4*>(a + to), make_uint4(w[0], w[1], w[2], w[3]));
             } else if (k.type == TPMLP_GRAD_F32) {
@@ -351,13 +453,14 @@ tpmlp_status run(const Plan& plan, const tpmlp_grad_tensor* t, int64_t n, bool c
         if (launches == kMost) return TPMLP_ERR_UNSUPPORTED;
         start[launches++] = from;
     }
+    const unsigned keep = clip ? G_KEEP / (static_cast<unsigned>(plan.vecs) * GT * 16) : 0;
     int sums = 0;
     for (int l = 0; l < launches; ++l) {
         int64_t at = start[l];
         if (launches > 1) fill(p, t, n, &at, plan.vecs);
         const unsigned grid = p.chunks < static_cast<unsigned>(plan.ctas) ? p.chunks : plan.ctas;
         TPMLP_CUDA(timed(TPMLP_KERNEL_BIAS_GRAD, 1, st,
-                         [&] { return launch(grad_squares_kernel<N>, grid, st, p, partial + sums); }));
+                         [&] { return launch(grad_squares_kernel<N>, grid, st, p, keep, partial + sums); }));
         sums += static_cast<int>(grid);
     }
     const double* all = partial;
