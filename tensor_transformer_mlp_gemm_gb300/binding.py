@@ -338,6 +338,18 @@ def _check(status: int, where: str) -> None:
         raise TpmlpError(status, where)
 
 
+def prepared(name: str):
+    """The library's call `name` for arguments that are marshalled already (integers as
+    pointers, arrays, None)."""
+    f = getattr(_lib, name)
+
+    def call(*args):
+        status = f(*args)
+        if status != TPMLP_OK:
+            raise TpmlpError(status, name)
+    return call
+
+
 def tpmlp_status_string(status: int) -> str:
     return _lib.tpmlp_status_string(int(status)).decode()
 

@@ -33,8 +33,10 @@ struct Fp4GemmParams {
     const uint8_t* sa[F4_MAX_MAPS];      // the same scales, for the few-rows kernel
     const uint8_t* sb[F4_MAX_MAPS];
     void* out[F4_MAX_MAPS];              // [M, N] per group, or [chunk_rows, N] per token chunk
+    const void* x[F4_MAX_MAPS];          // few rows only: A in bf16 [M, K], quantised on the way
     const float* ga;                     // the tensors' scales (nv)
     const float* gb;
+    int early;                           // B is there before the grids ahead have ended
     int M, N, K;                         // per group; K per segment
     int groups, ksegs;
     int a_part, b_part;
@@ -53,7 +55,9 @@ cudaError_t launch_fp4_gemm(const Fp4GemmParams& p, int fmt, bool f32, cudaStrea
 
 // The same (bf16 output) for few rows of A: tiles of 128 columns by `rows` rows of A, which
 // is also the box of A's maps, with K cut over up to 8 CTAs of a cluster.
-cudaError_t launch_fp4_small(const Fp4GemmParams& p, int fmt, int rows, cudaStream_t st);
+// A comes in 4 bits, or up to FP4_QUANT_ROWS rows of it in bf16 (quantise).
+constexpr int FP4_QUANT_ROWS = 16;
+cudaError_t launch_fp4_small(const Fp4GemmParams& p, int fmt, int rows, bool quantise, cudaStream_t st);
 // Those rows for a product of this shape on the current device; 0: it has rows and
 // columns enough for the pairs.
 cudaError_t fp4_small_rows(int M, int N, int groups, int fmt, int& rows);

@@ -154,6 +154,7 @@ struct Product {
     void* const* out;
     int nout;          // outputs: one per group, or one per token chunk
     int chunk_rows;    // > 0: rows per token chunk
+    const void* const* x;  // A in bf16, for the few-rows kernel to quantise, or null
 };
 
 bool encode_operand(CUtensorMap* m, CUtensorMap* sm, const Operand& o, int K, int rows, int box,
@@ -177,10 +178,17 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int format, in
     std::memset(&p, 0, sizeof(p));
     int few = 0;  // rows of a tile of the few-rows kernel
     if (!d.f32) TPMLP_CUDA(fp4_small_rows(d.M, d.N, d.groups, format, few));
-    if (!encode_operand(p.a_map, p.as_map, d.a, d.K, d.M, few ? few : 128, format, few ? 0 : 1) ||
+    if ((!d.x && !encode_operand(p.a_map, p.as_map, d.a, d.K, d.M, few ? few : 128, format, few ? 0 : 1)) ||
         !encode_operand(p.b_map, p.bs_map, d.b, d.K, d.N, 128, format, few ? 0 : 2))
         return TPMLP_ERR_UNSUPPORTED;
-    for (int i = 0; i < d.a.n; ++i) p.sa[i] = static_cast<const uint8_t*>(d.a.s[i]);
+    for (int i = 0; i < d.a.n; ++i) {
+        if (d.x)
+            p.x[i] = d.x[i];
+        else
+            p.sa[i] = static_cast<const uint8_t*>(d.a.s[i]);
+    }
+    // A was quantised by this call, after what came before had ended: B may be read already
+    p.early = !d.x;
     for (int i = 0; i < d.b.n; ++i) p.sb[i] = static_cast<const uint8_t*>(d.b.s[i]);
     for (int i = 0; i < d.nout; ++i) p.out[i] = d.out[i];
     p.ga = static_cast<const float*>(d.a.scale);
@@ -205,13 +213,14 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int format, in
     p.timeout_ns = g_timeout_ns;
     p.stall = g_stall;
     TPMLP_CUDA(timed(kind, 1, st, [&] {
-        return few ? launch_fp4_small(p, format, few, st) : launch_fp4_gemm(p, format, d.f32, st);
+        return few ? launch_fp4_small(p, format, few, d.x != nullptr, st) : launch_fp4_gemm(p, format, d.f32, st);
     }));
     return TPMLP_OK;
 }
 
 // Quantises an activation or gradient: token chunks of one matrix [T, cols], or `parts`
-// matrices.  calibrated: *scale is given; else (nv) it is computed here.
+// matrices.  calibrated: *scale is given; else (nv) it is computed here.  Neither by rows nor by
+// columns: only that.
 tpmlp_status quantize(const void* const* src, int parts, bool gather, long long rows, long long cols,
                       int format, void* scale, bool calibrated, const Packed* by_rows,
                       const Packed* by_cols, float* sums, long long sums_ld, cudaStream_t st) {
@@ -233,6 +242,7 @@ tpmlp_status quantize(const void* const* src, int parts, bool gather, long long 
     if (format == FP4_NV && !calibrated)
         TPMLP_CUDA(timed(TPMLP_KERNEL_SP_COPY, 1, st,
                          [&] { return launch_fp4_tensor_scale(p, static_cast<float*>(scale), st); }));
+    if (!by_rows && !by_cols) return TPMLP_OK;
     const int mode = (by_rows ? FP4_Q_ROWS : 0) | (by_cols ? FP4_Q_COLS : 0) | (sums ? FP4_Q_SUMS : 0);
     TPMLP_CUDA(timed(TPMLP_KERNEL_SP_COPY, 1, st, [&] { return launch_fp4_quant(p, format, mode, st); }));
     return TPMLP_OK;
@@ -283,14 +293,17 @@ tpmlp_status forward(Split k, const tpmlp_linear_dims* dims, int format, const v
         cols.q[i] = static_cast<uint8_t*>(Xq[i]);
         cols.s[i] = static_cast<uint8_t*>(Xs[i]);
     }
-    TPMLP_TRY(quantize(X, nx, col, col ? s.Tc : s.T, K, format, x_scale, x_calibrated != 0, &rows,
-                       save ? &cols : nullptr, nullptr, 0, st));
     Product p;
     p.M = s.T;
     p.N = col ? s.shard : s.out;
     p.K = K;
     p.groups = col ? s.t : 1;
     p.ksegs = col ? 1 : s.t;
+    // up to 16 tokens the product quantises them itself, for one launch less (one token, 4096 ->
+    // 12288 features)
+    p.x = s.T <= FP4_QUANT_ROWS && !save ? X : nullptr;
+    TPMLP_TRY(quantize(X, nx, col, col ? s.Tc : s.T, K, format, x_scale, x_calibrated != 0,
+                       p.x ? nullptr : &rows, save ? &cols : nullptr, nullptr, 0, st));
     p.a = Operand{reinterpret_cast<const void* const*>(rows.q), reinterpret_cast<const void* const*>(rows.s),
                   nq, col ? F4_SINGLE : F4_KSEG, x_scale};
     p.b = Operand{Wq, Ws, s.t, col ? F4_GROUP : F4_KSEG, w_scale};
@@ -355,6 +368,7 @@ tpmlp_status backward(Split k, const tpmlp_linear_dims* dims, int format, const 
         p.out = dX;
         p.nout = ndx;
         p.chunk_rows = col ? s.Tc : 0;
+        p.x = nullptr;
         TPMLP_TRY(run_product(dev, p, format, TPMLP_KERNEL_LINEAR_DGRAD, st));
     }
     {
@@ -373,6 +387,7 @@ tpmlp_status backward(Split k, const tpmlp_linear_dims* dims, int format, const 
         p.out = dW;
         p.nout = s.t;
         p.chunk_rows = 0;
+        p.x = nullptr;
         TPMLP_TRY(run_product(dev, p, format, TPMLP_KERNEL_LINEAR_WGRAD, st));
     }
     return TPMLP_OK;

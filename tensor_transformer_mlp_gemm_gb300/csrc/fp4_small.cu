@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "fp4_cvt.cuh"
 #include "fp4_gemm.cuh"
 #include "fp4_mma.cuh"
 
@@ -25,6 +26,7 @@ namespace {
 using namespace f8;
 
 constexpr int S_THREADS = 256;
+constexpr int S_WARPS = 4;       // of the output, and of quantising
 constexpr int S_MAX_SPLIT = 8;   // the portable cluster size
 
 // Up to 64 tokens two CTAs take an SM, at 256 one.  At 128 either: one with a ring as
@@ -73,7 +75,7 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-template <int FMT, int TN, int PER_SM>
+template <int FMT, int TN, int PER_SM, bool QUANT>
 __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
     fp4_small_kernel(const __grid_constant__ Fp4GemmParams p, int splits) {
     using C = Small<FMT, TN, PER_SM>;
@@ -89,7 +91,9 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
     const uint32_t bar_done = bar0 + 16 * NST; // all MMAs
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_area + 16 * NST + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bar_area + 16 * NST + 12);
-    volatile int* copied = abort_flag + 1;  // stages
+    // stages copied, and those with each warp's values (a role that has given up says so)
+    volatile int* copied = abort_flag + 1;
+    volatile int* quantised = abort_flag + 2;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(blockIdx.x % splits);
@@ -100,11 +104,12 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_full + 8 * s, QUANT ? 1 + S_WARPS : 1);
             ptx::mbar_init(bar_empty + 8 * s, 1);
         }
         ptx::mbar_init(bar_done, 1);
         *abort_flag = 0;
+        for (int w = 0; w < S_WARPS; ++w) quantised[w] = 0x7FFFFFFF;
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
@@ -117,7 +122,6 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
 
     const int kblocks = (p.K + F4_BK - 1) / F4_BK;
     const int nk = kblocks * p.ksegs;
@@ -130,26 +134,46 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
             uint32_t phase = 0;
             int s = first / kblocks, kb = first - s * kblocks, fills = 0;
             const int stop = p.stall >= 0 && rank == splits - 1 ? min(last, first + p.stall) : last;
-            for (int k = first; k < stop; ++k) {
-                if (!wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.timeout_ns, p.err,
-                          ERR_PRODUCER))
-                    break;
-                const uint32_t sw = base + stage * C::kStageBytes, full = bar_full + 8 * stage;
-                const int wi = f4::pick(p.b_part, g, s), xi = f4::pick(p.a_part, g, s);
-                ptx::mbar_arrive_expect_tx(full, C::kStageBytes);
+            // B's part of stage `stage`; scales of 128 rows lie next to each other along K
+            constexpr uint32_t X_BYTES = QUANT ? TN * 128 + C::kScales : 0;  // written here, not copied
+            const long long along = static_cast<long long>(kblocks) * C::kScales;
+            auto load_b = [&](int st, int seg, int block) {
+                const uint32_t sw = base + st * C::kStageBytes, full = bar_full + 8 * st;
+                const int wi = f4::pick(p.b_part, g, seg);
+                ptx::mbar_arrive_expect_tx(full, C::kStageBytes - X_BYTES);
                 // (a byte holds two of K)
-                ptx::tma_load_2d(sw, p.b_map + wi, kb * 128, f0, full);
-                ptx::tma_load_2d(sw + F4_BOX_BYTES, p.a_map + xi, kb * 128, t0, full);
-                // scales of 128 rows lie next to each other along K
-                const long long along = static_cast<long long>(kblocks) * C::kScales;
-                const uint32_t ss = sw + F4_BOX_BYTES + TN * 128;
-                bulk_load(ss, p.sb[wi] + (f0 >> 7) * along + kb * C::kScales, C::kScales, full);
+                ptx::tma_load_2d(sw, p.b_map + wi, block * 128, f0, full);
+                bulk_load(sw + F4_BOX_BYTES + TN * 128, p.sb[wi] + (f0 >> 7) * along + block * C::kScales,
+                          C::kScales, full);
+            };
+            // what the ring takes of B, if that may be read already
+            int ahead = 0;
+            for (int es = s, eb = kb; p.early && ahead < NST && first + ahead < stop; ++ahead) {
+                load_b(ahead, es, eb);
+                if (++eb == kblocks) {
+                    eb = 0;
+                    ++es;
+                }
+            }
+            ptx::griddep_wait();
+            for (int k = first; k < stop; ++k) {
+                if (k - first >= ahead) {
+                    if (!wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag, p.timeout_ns, p.err,
+                              ERR_PRODUCER))
+                        break;
+                    load_b(stage, s, kb);
+                }
+                if constexpr (!QUANT) {
+                    const uint32_t sw = base + stage * C::kStageBytes, full = bar_full + 8 * stage;
+                    const int xi = f4::pick(p.a_part, g, s);
+                    ptx::tma_load_2d(sw + F4_BOX_BYTES, p.a_map + xi, kb * 128, t0, full);
 #pragma unroll
-                for (int i = 0; i < C::kTiles; ++i) {
-                    // (behind the last row any: nobody reads those columns of sums)
-                    const int at = t0 + 128 * i < p.M ? (t0 >> 7) + i : 0;
-                    bulk_load(ss + (1 + i) * C::kScales, p.sa[xi] + at * along + kb * C::kScales,
-                              C::kScales, full);
+                    for (int i = 0; i < C::kTiles; ++i) {
+                        // (behind the last token any: nobody reads those sums)
+                        const int at = t0 + 128 * i < p.M ? (t0 >> 7) + i : 0;
+                        bulk_load(sw + F4_BOX_BYTES + TN * 128 + (1 + i) * C::kScales,
+                                  p.sa[xi] + at * along + kb * C::kScales, C::kScales, full);
+                    }
                 }
                 ++fills;
                 if (++kb == kblocks) {
@@ -206,6 +230,79 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
     } else if (warp >= 4) {
         const int q = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        ptx::griddep_wait();
+        if constexpr (QUANT) {
+            // A: a thread takes 32 of a row of each stage, 16 bytes of its 128-byte swizzle row
+            static_assert(TN == 16 && C::kTiles == 1, "eight threads a row");
+            constexpr int PER = FMT == FP4_NV ? 2 : 1;  // groups of 32
+            const int i = q * 32 + lane, row = i >> 3, run = i & 7;
+            float inv_g = 0.0f;
+            if constexpr (FMT == FP4_NV) inv_g = q4::inverse_of(p.ga);
+            int s = first / kblocks, kb = first - s * kblocks;
+            auto fetch = [&](uint4 (&v)[4]) {
+                const int k = kb * F4_BK + run * 32;
+                const bool in = row < p.M && k < p.K;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(p.x[f4::pick(p.a_part, g, s)]) +
+                    (in ? static_cast<long long>(row) * p.K + k : 0));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = in ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+                if (++kb == kblocks) {
+                    kb = 0;
+                    ++s;
+                }
+            };
+            uint8_t* to = gbase + F4_BOX_BYTES + row * 128 + ((run ^ (row & 7)) << 4);
+            uint8_t* scales = gbase + F4_BOX_BYTES + TN * 128 + C::kScales + row * 16;
+            uint4 next[4];
+            if (first < last) fetch(next);
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int k = first; k < last; ++k) {
+                uint4 v[4] = {next[0], next[1], next[2], next[3]};
+                if (k + 1 < last) fetch(next);
+                uint32_t o[4];
+                uint32_t byte[PER];
+#pragma unroll
+                for (int h = 0; h < PER; ++h) {
+                    uint32_t m = q4::larger(q4::largest(v[2 * h]), q4::largest(v[2 * h + 1]));
+                    if constexpr (PER == 1)
+                        m = q4::larger(m, q4::larger(q4::largest(v[2]), q4::largest(v[3])));
+                    const q4::Scale4 sc = q4::scale_of<FMT>(m & 0x7FFFu, inv_g);
+                    byte[h] = sc.byte;
+#pragma unroll
+                    for (int j = h * (4 / PER); j < (h + 1) * (4 / PER); ++j) {
+                        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                        float2 f[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            f[e] = q4::scaled<FMT>(make_float2(q8::lo_f(w[e]), q8::hi_f(w[e])), sc.inv);
+                        o[j] = sc.inv > 0.0f ? q4::cvt8(f[0], f[1], f[2], f[3]) : 0u;
+                    }
+                }
+                const bool ok = __all_sync(0xffffffffu, wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag,
+                                                             p.timeout_ns, p.err, ERR_PRODUCER));
+                if (!ok) {
+                    if (lane == 0) quantised[q] = k - first;
+                    break;
+                }
+                const int at = stage * C::kStageBytes;
+                *reinterpret_cast<uint4*>(to + at) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+                for (int h = 0; h < PER; ++h) {
+                    const int j = run * PER + h;  // the stage's group
+                    scales[at + (j >> 2) * 512 + (j & 3)] = static_cast<uint8_t>(byte[h]);
+                }
+                // for the tensor cores, which read shared memory another way
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar_full + 8 * stage);
+                if (++stage == NST) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
         // this CTA's sums, feature by feature of each token, where the operands were
         // (not of a CTA that has given up: copies and MMAs may still be under way there)
         if (__all_sync(0xffffffffu, wait(bar_done, 0, abort_flag, p.timeout_ns, p.err, ERR_EPILOGUE))) {
@@ -228,13 +325,19 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
     }
 
     // every CTA's sums are in place
+    ptx::griddep_wait();
     __syncwarp();
     ptx::cluster_sync();
     if (threadIdx.x == 0 && *abort_flag) {
-        // what this CTA has under way ends before it does
+        // What this CTA has under way ends before it does.  A stage counts the quantising warps
+        // too: those that gave up before they came to it are stood in for.
         const int n = *copied;
-        for (int k = max(0, n - NST); k < n; ++k)
-            drain(bar_full + 8 * (k % NST), static_cast<uint32_t>((k / NST) & 1), p.timeout_ns, p.err);
+        for (int k = max(0, n - NST); k < n; ++k) {
+            const uint32_t full = bar_full + 8 * (k % NST);
+            for (int w = 0; QUANT && w < S_WARPS; ++w)
+                if (quantised[w] <= k) arrive_relaxed(full);
+            drain(full, static_cast<uint32_t>((k / NST) & 1), p.timeout_ns, p.err);
+        }
         drain(bar_done, 0, p.timeout_ns, p.err);
     }
     {
@@ -289,7 +392,7 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
 }
 
 // attr: two of them, the cluster's first
-template <int FMT, int TN, int PER_SM>
+template <int FMT, int TN, int PER_SM, bool QUANT>
 void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int splits) {
     cfg.gridDim = dim3(static_cast<unsigned>(splits), 1, 1);
     cfg.blockDim = dim3(S_THREADS, 1, 1);
@@ -307,12 +410,12 @@ void configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int splits) {
 // Stands in for the kernel where the runtime is asked how many of its clusters run at
 // once: of a kernel that allocates tensor memory it counts one CTA on an SM, whatever it
 // allocates.  (Never launched; as many registers as two CTAs may have.)
-template <int FMT, int TN, int PER_SM>
+template <int FMT, int TN, int PER_SM, bool QUANT>
 __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm) fp4_small_stand_in() {}
 
 // Clusters of each size that a device runs at once (a cluster lies in one group of SMs:
 // with two CTAs on an SM 97 of 3, 74 of 4 and 36 of 8 on 152 SMs).
-template <int FMT, int TN, int PER_SM>
+template <int FMT, int TN, int PER_SM, bool QUANT>
 cudaError_t resident(const int*& clusters) {
     constexpr int kDevices = 64;
     static int known[kDevices][S_MAX_SPLIT + 1] = {};
@@ -322,19 +425,19 @@ cudaError_t resident(const int*& clusters) {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
     if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
-        e = cudaFuncSetAttribute(fp4_small_kernel<FMT, TN, PER_SM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(fp4_small_kernel<FMT, TN, PER_SM, QUANT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Small<FMT, TN, PER_SM>::kSmem);
         if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(fp4_small_stand_in<FMT, TN, PER_SM>,
+        e = cudaFuncSetAttribute(fp4_small_stand_in<FMT, TN, PER_SM, QUANT>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, Small<FMT, TN, PER_SM>::kSmem);
         if (e != cudaSuccess) return e;
         for (int c = 1; c <= S_MAX_SPLIT; ++c) {
             cudaLaunchConfig_t cfg = {};
             cudaLaunchAttribute attr[2];
-            configure<FMT, TN, PER_SM>(cfg, attr, c);
+            configure<FMT, TN, PER_SM, QUANT>(cfg, attr, c);
             cfg.numAttrs = 1;
             int n = 0;
-            e = cudaOccupancyMaxActiveClusters(&n, fp4_small_stand_in<FMT, TN, PER_SM>, &cfg);
+            e = cudaOccupancyMaxActiveClusters(&n, fp4_small_stand_in<FMT, TN, PER_SM, QUANT>, &cfg);
             if (e != cudaSuccess) return e;
             __atomic_store_n(&known[dev][c], n, __ATOMIC_RELAXED);
         }
@@ -344,10 +447,10 @@ cudaError_t resident(const int*& clusters) {
     return cudaSuccess;
 }
 
-template <int FMT, int TN, int PER_SM>
+template <int FMT, int TN, int PER_SM, bool QUANT>
 cudaError_t launch(const Fp4GemmParams& p, cudaStream_t st) {
     const int* clusters = nullptr;
-    const cudaError_t e = resident<FMT, TN, PER_SM>(clusters);
+    const cudaError_t e = resident<FMT, TN, PER_SM, QUANT>(clusters);
     if (e != cudaSuccess) return e;
     const long long tiles = static_cast<long long>((p.N + 127) / 128) * p.groups;
     const long long rows = (p.M + TN - 1) / TN;
@@ -359,10 +462,10 @@ cudaError_t launch(const Fp4GemmParams& p, cudaStream_t st) {
     while (splits > 1 && tiles * rows > clusters[splits]) --splits;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    configure<FMT, TN, PER_SM>(cfg, attr, splits);
+    configure<FMT, TN, PER_SM, QUANT>(cfg, attr, splits);
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), static_cast<unsigned>(rows), 1);
     cfg.stream = st;
-    return cudaLaunchKernelEx(&cfg, fp4_small_kernel<FMT, TN, PER_SM>, p, splits);
+    return cudaLaunchKernelEx(&cfg, fp4_small_kernel<FMT, TN, PER_SM, QUANT>, p, splits);
 }
 
 }  // namespace
@@ -371,7 +474,7 @@ cudaError_t fp4_small_rows(int M, int N, int groups, int fmt, int& rows) {
     rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     if (M <= 128) return cudaSuccess;
     const int* clusters = nullptr;
-    const cudaError_t e = fmt == FP4_NV ? resident<FP4_NV, 256, 1>(clusters) : resident<FP4_MX, 256, 1>(clusters);
+    const cudaError_t e = fmt == FP4_NV ? resident<FP4_NV, 256, 1, false>(clusters) : resident<FP4_MX, 256, 1, false>(clusters);
     if (e != cudaSuccess) return e;
     // Pairs on 256 x 256 tiles are faster unless so few tiles that K can be cut in four here.
     const long long tiles = static_cast<long long>((N + 127) / 128) * groups;
@@ -380,25 +483,27 @@ cudaError_t fp4_small_rows(int M, int N, int groups, int fmt, int& rows) {
 }
 
 template <int FMT>
-static cudaError_t launch_rows(const Fp4GemmParams& p, int rows, cudaStream_t st) {
+static cudaError_t launch_rows(const Fp4GemmParams& p, int rows, bool quantise, cudaStream_t st) {
+    if (quantise && rows != FP4_QUANT_ROWS) return cudaErrorInvalidValue;
     switch (rows) {
-        case 16: return launch<FMT, 16, 2>(p, st);
-        case 32: return launch<FMT, 32, 2>(p, st);
-        case 64: return launch<FMT, 64, 2>(p, st);
+        case 16: return quantise ? launch<FMT, 16, 2, true>(p, st) : launch<FMT, 16, 2, false>(p, st);
+        case 32: return launch<FMT, 32, 2, false>(p, st);
+        case 64: return launch<FMT, 64, 2, false>(p, st);
         case 128: {
             const int* clusters = nullptr;
-            const cudaError_t e = resident<FMT, 128, 1>(clusters);
+            const cudaError_t e = resident<FMT, 128, 1, false>(clusters);
             if (e != cudaSuccess) return e;
             const long long tiles = static_cast<long long>((p.N + 127) / 128) * p.groups;
-            return tiles <= clusters[2] ? launch<FMT, 128, 1>(p, st) : launch<FMT, 128, 2>(p, st);
+            return tiles <= clusters[2] ? launch<FMT, 128, 1, false>(p, st) : launch<FMT, 128, 2, false>(p, st);
         }
-        case 256: return launch<FMT, 256, 1>(p, st);
+        case 256: return launch<FMT, 256, 1, false>(p, st);
     }
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_fp4_small(const Fp4GemmParams& p, int fmt, int rows, cudaStream_t st) {
-    return fmt == FP4_NV ? launch_rows<FP4_NV>(p, rows, st) : launch_rows<FP4_MX>(p, rows, st);
+cudaError_t launch_fp4_small(const Fp4GemmParams& p, int fmt, int rows, bool quantise, cudaStream_t st) {
+    return fmt == FP4_NV ? launch_rows<FP4_NV>(p, rows, quantise, st)
+                         : launch_rows<FP4_MX>(p, rows, quantise, st);
 }
 
 }  // namespace tpmlp

@@ -10,10 +10,12 @@ bit; groups along the axis that a product sums over share a scale (include/tpmlp
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import binding
-from .fp8 import _check_like, _check_parts, _pointers, _strided, _up256
+from .fp8 import _ARRAYS, _check_like, _check_parts, _pointers, _strided, _up256
 from .inputs import LinearWorkload
 
 
@@ -184,7 +186,7 @@ class DeviceFp4Linear:
                  x_scale: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
         if w.split not in ("column", "row"):
             raise ValueError("split must be 'column' or 'row'")
-        self.w, self.weights, self.fmt = w, weights, weights.fmt
+        self.w, self._weights, self.fmt = w, weights, weights.fmt
         self.column = w.split == "column"
         self._code = _format(self.fmt)
         T, din, dout, t, n = w.tokens, w.in_features, w.out_features, w.t, w.seq_chunks
@@ -205,28 +207,45 @@ class DeviceFp4Linear:
             if m.shape != shape or m.device != dev:
                 raise ValueError(f"a 4-bit weight shard of shape {shape} on {dev} is needed, got "
                                  f"{m.shape} on {m.device}")
-        _check_scale(x_scale, self.fmt, dev, "x_scale")
-        self.b, self.x_scale = b, x_scale
+        self._bias = b
+        self.x_scale = x_scale
         bf = torch.bfloat16
         # the shapes of X_i, Y_i (or Z) and their gradients, and how many of each
         self._x = ((T // n, din), n) if self.column else ((T, s), t)
         self._y = ((T, s), t) if self.column else ((T // n, dout), n)
         self.Y = [torch.empty(self._y[0], dtype=bf, device=dev) for _ in range(self._y[1])]
         self._dX = self._dx_ptrs = self._grads = self._saved = None
-        self._has_saved = False
+        self._has_saved, self._saved_scale = False, None
         if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()
                                       or workspace.numel() * workspace.element_size() < need):
             raise ValueError(f"the workspace needs {need} contiguous bytes on {dev}")
         self.ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8,
                                                                       device=dev)
-        # (pointers of the layer's own buffers are marshalled once)
+        # (what stays the same in every call is marshalled once, and kept)
+        split = "column" if self.column else "row"
+        self._call = binding.prepared(f"tpmlp_fp4_{split}_linear_forward")
+        self._call_back = binding.prepared(f"tpmlp_fp4_{split}_linear_backward")
+        self._dims = ctypes.byref(self.dims)
+        self._b = b.data_ptr()
+        self._w_scale = None if weights.scale is None else weights.scale.data_ptr()
         self._forward = (_pointers([m.q for m in weights.forward]), _pointers([m.s for m in weights.forward]))
         self._backward = weights.backward and (_pointers([m.q for m in weights.backward]),
                                                _pointers([m.s for m in weights.backward]))
         # where a forward call without a calibration writes the scale: one that keeps nothing, and
         # one that keeps X for the backward pass
         self._scales = torch.empty(2, 1, dtype=torch.float32, device=dev) if self.fmt == "nvfp4" else None
-        self._saved_scale = None
+
+    weights = property(lambda self: self._weights)
+    b = property(lambda self: self._bias)
+
+    @property
+    def x_scale(self):
+        return self._x_scale
+
+    @x_scale.setter
+    def x_scale(self, scale):
+        _check_scale(scale, self.fmt, self.device, "x_scale")
+        self._x_scale = scale
 
     @property
     def Y(self):
@@ -289,30 +308,45 @@ class DeviceFp4Linear:
             _check_like(x, spec[0], torch.bfloat16, self.device, what)
         return xs
 
+    def _ptrs(self, xs, spec, what):
+        """Pointers of the bf16 tensors xs, which are looked over."""
+        if isinstance(xs, torch.Tensor):
+            xs = (xs,)
+        shape, n = spec
+        dev, bf = self.device, torch.bfloat16
+        if len(xs) != n:
+            self._list(xs, spec, what)
+        got = []
+        for x in xs:
+            if x.dtype is not bf or x.shape != shape or not x.is_contiguous() or x.device != dev:
+                self._list(xs, spec, what)
+            got.append(x.data_ptr())
+        return _ARRAYS[n](*got)
+
     def forward(self, X, save: bool = False, Y=None, stream=None) -> None:
         """X: bf16 (column: its token chunks, row: t shards).  save: keep X in 4 bits for the
         next backward call."""
-        X = _pointers(self._list(X, self._x, "X"))
-        Y = self._y_ptrs if Y is None else _pointers(self._list(Y, self._y, "Y"))
-        if save and self._backward is None:
-            raise ValueError("the weights have no form for the backward pass")
-        kept = self._save(stream) if save else None
-        scale = self.x_scale
-        calibrated = scale is not None
-        if not calibrated and self._scales is not None:
-            scale = self._scales[int(save)]
-        with binding.on_device(self.device):
-            stream = binding.stream_on(self.device, stream)
-            if self.column:
-                binding.tpmlp_fp4_column_linear_forward(
-                    self.dims, self._code, X, scale, calibrated, kept and kept.q_ptrs[0],
-                    kept and kept.s_ptrs[0], *self._forward, self.weights.scale, self.b, Y, self.ws, stream)
-            else:
-                binding.tpmlp_fp4_row_linear_forward(
-                    self.dims, self._code, X, scale, calibrated, kept and kept.q_ptrs,
-                    kept and kept.s_ptrs, *self._forward, self.weights.scale, self.b, Y, self.ws, stream)
+        X = self._ptrs(X, self._x, "X")
+        Y = self._y_ptrs if Y is None else self._ptrs(Y, self._y, "Y")
+        q = s = scale = None
         if save:
-            self._saved_scale, self._has_saved = scale, True
+            if self._backward is None:
+                raise ValueError("the weights have no form for the backward pass")
+            kept = self._save(stream)
+            q, s = (kept.q_ptrs[0], kept.s_ptrs[0]) if self.column else (kept.q_ptrs, kept.s_ptrs)
+        calibrated = self._x_scale is not None
+        if calibrated:
+            scale = self._x_scale.data_ptr()
+        elif self._scales is not None:
+            scale = self._scales[int(save)].data_ptr()
+        dev = self.device
+        with binding.on_device(dev):
+            self._call(self._dims, self._code, X, scale, calibrated, q, s, *self._forward, self._w_scale,
+                       self._b, Y, self.ws.data_ptr(), binding.stream_on(dev, stream))
+        if save:
+            # (of a calibration the tensor, in case another one is set before the backward call)
+            self._saved_scale = (self._x_scale if calibrated else None, scale)
+            self._has_saved = True
 
     def backward(self, dY, dX=None, stream=None) -> None:
         """dY: bf16 (column: t shards, row: token chunks), for the X that the last forward call
@@ -321,17 +355,13 @@ class DeviceFp4Linear:
             raise ValueError("the weights have no form for the backward pass")
         if not self._has_saved:
             raise ValueError("there is no forward call with save=True to go back through")
-        dY = _pointers(self._list(dY, self._y, "dY"))
-        dX = self._input_grads(stream) if dX is None else _pointers(self._list(dX, self._x, "dX"))
+        dY = self._ptrs(dY, self._y, "dY")
+        dX = self._input_grads(stream) if dX is None else self._ptrs(dX, self._x, "dX")
         _, db, dW = self._weight_grads(stream)
-        kept, scale = self._saved, self._saved_scale
-        with binding.on_device(self.device):
-            stream = binding.stream_on(self.device, stream)
-            if self.column:
-                binding.tpmlp_fp4_column_linear_backward(
-                    self.dims, self._code, dY, kept.q_ptrs[0], kept.s_ptrs[0], scale, *self._backward,
-                    self.weights.scale, dX, dW, db, self.ws, stream)
-            else:
-                binding.tpmlp_fp4_row_linear_backward(
-                    self.dims, self._code, dY, kept.q_ptrs, kept.s_ptrs, scale, *self._backward,
-                    self.weights.scale, dX, dW, db, self.ws, stream)
+        kept = self._saved
+        q, s = (kept.q_ptrs[0], kept.s_ptrs[0]) if self.column else (kept.q_ptrs, kept.s_ptrs)
+        dev = self.device
+        with binding.on_device(dev):
+            self._call_back(self._dims, self._code, dY, q, s, self._saved_scale[1], *self._backward,
+                            self._w_scale, dX, dW, db.data_ptr(), self.ws.data_ptr(),
+                            binding.stream_on(dev, stream))

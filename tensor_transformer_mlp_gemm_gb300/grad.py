@@ -61,6 +61,8 @@ class DeviceGradients:
         need = binding.tpmlp_grad_workspace_bytes(n)
         if need == 0:
             raise ValueError(f"too many gradients for a call: {n}")
+        self._measure = binding.prepared("tpmlp_grad_norm")
+        self._clip = binding.prepared("tpmlp_grad_clip")
         # (marshalled once, so the object keeps the tensors)
         self._tensors = binding.make_grad_tensors(
             [(g, o, g.numel(), binding.GRAD_TYPES[g.dtype]) for g, o in zip(self.grads, self.out)])
@@ -70,13 +72,13 @@ class DeviceGradients:
     def measure(self, stream=None) -> torch.Tensor:
         """The norm, without clipping."""
         with binding.on_device(self.device):
-            binding.tpmlp_grad_norm(self._tensors, len(self.grads), self.norm, self.ws,
-                                    binding.stream_on(self.device, stream))
+            self._measure(self._tensors, len(self.grads), self.norm.data_ptr(), self.ws.data_ptr(),
+                          binding.stream_on(self.device, stream))
         return self.norm
 
     def clip(self, max_norm: float, stream=None) -> torch.Tensor:
         """Writes the clipped gradients; returns the norm before clipping."""
         with binding.on_device(self.device):
-            binding.tpmlp_grad_clip(self._tensors, len(self.grads), max_norm, self.norm, self.ws,
-                                    binding.stream_on(self.device, stream))
+            self._clip(self._tensors, len(self.grads), max_norm, self.norm.data_ptr(), self.ws.data_ptr(),
+                       binding.stream_on(self.device, stream))
         return self.norm
