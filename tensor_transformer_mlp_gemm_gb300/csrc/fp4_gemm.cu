@@ -3,8 +3,10 @@
 //
 // CTA layout (384 threads, persistent over tiles; both CTAs of a pair compute one
 // 256 x 256 tile, 128 rows each):
-//   warp 0       TMA producer: this CTA's 128 rows of A and of B for each 256 of K, the
-//                scales of its rows of A and of all 256 rows of B
+//   warps 0, 2   TMA producers for each 256 of K: of this CTA's 128 rows of A and their
+//                scales; of its 128 rows of B and the scales of all 256.  (One thread for
+//                all four copies took longer than the MMAs where a segment of K is two
+//                stages: forward of 16384 x 4096 x 4096 in eight segments 101 us, now 90.)
 //   warp 1       owns the tensor memory; in the even CTA copies the pair's scales into it and
 //                issues the MMAs, four K slices of 64 for each stage
 //   warps 4..11  output: warp w reads lanes 32 (w % 4) .. of the accumulator and columns
@@ -65,8 +67,9 @@ __device__ __forceinline__ void decode(const Fp4GemmParams& p, int tile, int& g,
 }
 
 // How many stages a role that gave up has done (one that did not: all), 64-bit counts in
-// shared memory: in the even CTA those copied, by it and by the odd one; in both those issued.
-constexpr int F_COPIED = 0, F_ISSUED = 2, F_COUNTS = 3;
+// shared memory: in the even CTA those copied, A's and B's by it and by the odd one; in both
+// those issued.
+constexpr int F_COPIED = 0, F_ISSUED = 4, F_COUNTS = 5;
 
 // After a wait has expired and every role has left its loop: what a CTA has under way ends.
 // (Not inlined: its values would take registers from the roles.)
@@ -80,14 +83,19 @@ __device__ __noinline__ void settle(uint32_t bar0, int nk, int tiles, unsigned l
         static_cast<const long long*>(__cvta_shared_to_generic(bar0 + 16 * NST + 32));
     auto stages = [&](int i) { return min(counts[i], static_cast<long long>(tiles) * nk); };
     if (ptx::cluster_ctarank() == 0) {
-        // the copies of both CTAs
-        const long long even = stages(F_COPIED), odd = stages(F_COPIED + 1), n = max(even, odd);
+        // The copies of both CTAs.  A stage's barrier counts the bytes of all four producers, as
+        // its first arms it; what will not come is taken off, or it is armed with what comes.
+        long long n = 0;
+        for (int i = 0; i < 4; ++i) n = max(n, stages(F_COPIED + i));
         for (long long k = max(0LL, n - NST); k < n; ++k) {
             const uint32_t full = bar_full + 8 * static_cast<uint32_t>(k % NST);
-            if (k >= even)
-                ptx::mbar_arrive_expect_tx(full, STAGE);  // the odd CTA's only
-            else if (k >= odd)
-                complete_tx(full, STAGE);  // which will not come
+            uint32_t coming = 0;
+            for (int i = 0; i < 4; ++i)
+                if (k < stages(F_COPIED + i)) coming += F4_BOX_BYTES + (1 + (i & 1)) * Shape<FMT>::kScales;
+            if (k >= stages(F_COPIED))
+                ptx::mbar_arrive_expect_tx(full, coming);
+            else if (coming < 2 * STAGE)
+                complete_tx(full, 2 * STAGE - coming);
             drain(full, static_cast<uint32_t>((k / NST) & 1), timeout_ns, err);
         }
     }
@@ -165,9 +173,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
 
     if (warp < 4) {
         reg_dec<F_FEW_REGS>();
-        if (warp == 0 && lane == 0) {
-            // ---------------- TMA producer ----------------
+        if ((warp == 0 || warp == 2) && lane == 0) {
+            // ---------------- TMA producers ----------------
+            const bool of_b = warp == 2;
+            const CUtensorMap *maps = of_b ? p.b_map : p.a_map, *smaps = of_b ? p.bs_map : p.as_map;
+            const int part = of_b ? p.b_part : p.a_part, has_z = of_b ? p.b_z : p.a_z;
+            const int seg = of_b ? 0 : p.a_seg;
             const uint32_t even_full = ptx::mapa_shared(bar_full, 0);
+            const uint32_t to = base + (of_b ? F4_BOX_BYTES : 0);
+            const uint32_t sto = base + 2 * F4_BOX_BYTES + (of_b ? S::kScales : 0);
             int stage = 0;
             uint32_t phase = 0;
             long long fills = 0;
@@ -176,25 +190,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 if (tile + nclusters >= p.total_tiles) ptx::griddep_launch_dependents();
                 int g, m0, n0;
                 decode(p, tile, g, m0, n0);
-                const int arow = m0 + rank * 128, brow = n0 + rank * 128;
+                const int row = (of_b ? n0 : m0) + rank * 128, srow = (of_b ? n0 : row) >> 7;
                 for (int s = 0; ok && s < p.ksegs; ++s) {
-                    const int ai = f4::pick(p.a_part, g, s), bi = f4::pick(p.b_part, g, s);
-                    for (int kb = 0; kb < kblocks; ++kb) {
+                    const int i = f4::pick(part, g, s), at = has_z ? 0 : i, z = i - at;
+                    const CUtensorMap *map = maps + at, *smap = smaps + at;
+                    for (int kb = s * seg, end = kb + kblocks; kb < end; ++kb) {
                         if ((fills == p.stall && rank == 1) ||
                             !wait_for(bar_empty + 8 * stage, phase ^ 1u, ERR_PRODUCER)) {
                             ok = false;
                             break;
                         }
-                        const uint32_t sa = base + stage * S::kStageBytes, full = even_full + 8 * stage;
-                        const uint32_t ss = sa + 2 * F4_BOX_BYTES;
-                        if (rank == 0)  // counts both CTAs' bytes
+                        const uint32_t off = stage * S::kStageBytes, full = even_full + 8 * stage;
+                        if (rank == 0 && !of_b)  // counts everybody's bytes
                             ptx::mbar_arrive_expect_tx(bar_full + 8 * stage, 2 * S::kStageBytes);
                         // (a byte holds two of K, an element of the scales' maps eight bytes)
-                        ptx::tma_load_2d_pair(sa, p.a_map + ai, kb * 128, arow, full);
-                        ptx::tma_load_2d_pair(sa + F4_BOX_BYTES, p.b_map + bi, kb * 128, brow, full);
-                        ptx::tma_load_2d_pair(ss, p.as_map + ai, kb * (S::kScales / 8), arow >> 7, full);
-                        ptx::tma_load_2d_pair(ss + S::kScales, p.bs_map + bi, kb * (S::kScales / 8),
-                                              n0 >> 7, full);
+                        ptx::tma_load_3d_pair(to + off, map, kb * 128, row, z, full);
+                        ptx::tma_load_3d_pair(sto + off, smap, kb * (S::kScales / 8), srow, z, full);
                         ++fills;
                         if (++stage == NST) {
                             stage = 0;
@@ -211,7 +222,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                     phase ^= 1u;
                 }
             }
-            if (!ok) store_cluster64(ptx::mapa_shared(stages_done + 8 * (F_COPIED + rank), 0), fills);
+            if (!ok)
+                store_cluster64(ptx::mapa_shared(stages_done + 8 * (F_COPIED + 2 * rank + of_b), 0), fills);
         } else if (warp == 1 && rank == 0) {
             // ---------------- MMA issuer ----------------
             // The whole warp walks the loop and one lane issues, so the descriptors

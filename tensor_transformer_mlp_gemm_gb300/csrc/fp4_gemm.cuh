@@ -26,6 +26,8 @@ constexpr int F4_BOX_BYTES = 128 * 128;  // 128 rows of an operand for it
 enum Fp4Part : int { F4_SINGLE = 0, F4_GROUP = 1, F4_KSEG = 2 };
 
 struct Fp4GemmParams {
+    // [bytes of K, rows, matrices]: one map for all of an operand's matrices where they lie at
+    // equal steps (a_z, b_z: the matrix is the third coordinate), else one for each
     CUtensorMap a_map[F4_MAX_MAPS];      // values, boxes of 128 bytes x 128 rows
     CUtensorMap b_map[F4_MAX_MAPS];
     CUtensorMap as_map[F4_MAX_MAPS];     // scales, 128 rows of one stage (of B, 256 rows)
@@ -40,6 +42,8 @@ struct Fp4GemmParams {
     int M, N, K;                         // per group; K per segment
     int groups, ksegs;
     int a_part, b_part;
+    int a_z, b_z;
+    int a_seg;                           // K blocks from a segment to the next in one matrix A, or 0
     int mtiles, ntiles, total_tiles, band;
     int chunk_rows;                      // > 0: output i holds rows [i * chunk_rows, ...), else output g
     const void* bias;                    // bf16 [groups * N] or null

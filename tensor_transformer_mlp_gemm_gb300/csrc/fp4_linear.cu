@@ -84,6 +84,7 @@ Lin lin_of(const tpmlp_linear_dims& d, Split k) {
 struct Packed {
     uint8_t* q[kMaxShards];
     uint8_t* s[kMaxShards];
+    long long k;  // of rows that the parts share (joined), else 0
 };
 
 inline size_t packed_bytes(int n, long long R, long long K, int format) {
@@ -103,6 +104,20 @@ Packed place(uint8_t*& at, int n, long long R, long long K, int format) {
     return o;
 }
 
+// The same for segments of K that a product sums: where each is whole stages of K, as one
+// matrix [R, n K] (one tensor map in the place of n, and rows that lie further apart: forward
+// of 16384 x 4096 x 4096 in eight segments JOINEDUS).
+Packed place_segments(uint8_t*& at, int n, long long R, long long K, int format) {
+    if (n == 1 || K % F4_BK != 0) return place(at, n, R, K, format);
+    Packed o = place(at, 1, R, n * K, format);
+    for (int i = 1; i < n; ++i) {
+        o.q[i] = o.q[0] + i * (K / 2);
+        o.s[i] = o.s[0] + i * (K / F4_BK) * fp4_scale_step(format);
+    }
+    o.k = n * K;
+    return o;
+}
+
 // Scratch of a forward call: X by rows; of a backward call: dY by rows and by columns, the
 // bias gradient's partial sums, and dY's scale.
 size_t forward_bytes(const tpmlp_linear_dims& d, Split k, int format) {
@@ -116,21 +131,31 @@ size_t backward_bytes(const tpmlp_linear_dims& d, Split k, int format) {
            align256(static_cast<size_t>(up128(d.tokens)) * d.out_features * sizeof(float)) + 256;
 }
 
-// Scales [tiles of 128 rows][inner bytes], fetched as boxes of a stage by `box` tiles; kept by
-// shape, as maps of 8-bit operands are.
-bool encode_scales(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t tiles, uint32_t stage,
-                   uint32_t box_tiles) {
-    const cuuint64_t dims[2] = {inner / 8, tiles};
-    const cuuint64_t strides[1] = {inner};
-    const cuuint32_t box[2] = {stage / 8, box_tiles};
+// The step between matrices that lie at equal, ascending ones (a multiple of 16 bytes that a
+// tensor map takes), else 0.
+uint64_t equal_steps(const void* const* p, int n) {
+    const uint64_t first = reinterpret_cast<uint64_t>(p[0]);
+    const uint64_t step = n > 1 ? reinterpret_cast<uint64_t>(p[1]) - first : 0;
+    for (int i = 2; i < n; ++i)
+        if (reinterpret_cast<uint64_t>(p[i]) - first != i * step) return 0;
+    return step < (uint64_t(1) << 40) && step % 16 == 0 ? step : 0;
+}
+
+// Matrices [outer, inner bytes], `n` of them `step` bytes apart, in elements of `elem` bytes and
+// boxes of box_inner elements x box_outer rows.  Kept by shape, as maps of 8-bit operands are.
+bool encode3(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t n, uint64_t step,
+             int elem, uint32_t box_inner, uint32_t box_outer) {
+    const CUtensorMapDataType type = elem == 8 ? CU_TENSOR_MAP_DATA_TYPE_INT64 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUtensorMapSwizzle swizzle = elem == 8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    const cuuint64_t dims[3] = {inner / elem, outer, n};
+    const cuuint64_t strides[2] = {inner, n > 1 ? step : inner};
+    const cuuint32_t box[3] = {box_inner, box_outer, 1};
     const MapKey key =
-        make_map_key(CU_TENSOR_MAP_DATA_TYPE_INT64, 2, nullptr, dims, strides, box,
-                     CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+        make_map_key(type, 3, nullptr, dims, strides, box, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     const bool ok = g_maps.get(key, m, [&](CUtensorMap* out) {
-        const cuuint32_t estr[2] = {1, 1};
-        return g_encode(out, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<void*>(ptr), dims, strides,
-                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        const cuuint32_t estr[3] = {1, 1, 1};
+        return g_encode(out, type, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     });
     return ok && set_address(m, ptr);
@@ -144,6 +169,7 @@ struct Operand {
     int n;
     int part;
     const void* scale;  // of the tensor (nv)
+    long long k;        // > 0: all segments are one matrix with this K
 };
 
 struct Product {
@@ -157,13 +183,18 @@ struct Product {
     const void* const* x;  // A in bf16, for the few-rows kernel to quantise, or null
 };
 
+// The maps of an operand's values, and (box_tiles > 0) of its scales, that many times 128 rows a
+// box; *z: one map for all its matrices.
 bool encode_operand(CUtensorMap* m, CUtensorMap* sm, const Operand& o, int K, int rows, int box,
-                    int format, int box_tiles) {
+                    int format, uint32_t box_tiles, int* z) {
     const uint64_t inner = static_cast<uint64_t>(fp4_scale_bytes(1, K, format));
-    if (!encode_bytes(m, o.q[0], fp4_ld(K), rows, box)) return false;
-    if (box_tiles && !encode_scales(sm, o.s[0], inner, up128(rows), fp4_scale_step(format), box_tiles))
-        return false;
-    for (int i = 1; i < o.n; ++i) {
+    const uint64_t step = equal_steps(o.q, o.n), sstep = equal_steps(o.s, o.n);
+    *z = o.n > 1 && step && sstep;
+    const uint64_t n = *z ? o.n : 1;
+    if (!encode3(m, o.q[0], fp4_ld(K), rows, n, step, 1, 128, box)) return false;
+    const uint32_t width = static_cast<uint32_t>(fp4_scale_step(format) / 8);
+    if (box_tiles && !encode3(sm, o.s[0], inner, up128(rows), n, sstep, 8, width, box_tiles)) return false;
+    for (int i = 1; !*z && i < o.n; ++i) {
         m[i] = m[0];
         if (!set_address(&m[i], o.q[i])) return false;
         if (!box_tiles) continue;
@@ -178,8 +209,9 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int format, in
     std::memset(&p, 0, sizeof(p));
     int few = 0;  // rows of a tile of the few-rows kernel
     if (!d.f32) TPMLP_CUDA(fp4_small_rows(d.M, d.N, d.groups, format, few));
-    if ((!d.x && !encode_operand(p.a_map, p.as_map, d.a, d.K, d.M, few ? few : 128, format, few ? 0 : 1)) ||
-        !encode_operand(p.b_map, p.bs_map, d.b, d.K, d.N, 128, format, few ? 0 : 2))
+    if ((!d.x && !encode_operand(p.a_map, p.as_map, d.a, d.a.k > 0 ? static_cast<int>(d.a.k) : d.K, d.M,
+                               few ? few : 128, format, few ? 0 : 1, &p.a_z)) ||
+        !encode_operand(p.b_map, p.bs_map, d.b, d.K, d.N, 128, format, few ? 0 : 2, &p.b_z))
         return TPMLP_ERR_UNSUPPORTED;
     for (int i = 0; i < d.a.n; ++i) {
         if (d.x)
@@ -199,6 +231,7 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int format, in
     p.groups = d.groups;
     p.ksegs = d.ksegs;
     p.a_part = d.a.part;
+    p.a_seg = d.a.k > 0 ? d.K / F4_BK : 0;
     p.b_part = d.b.part;
     const long long mt = (static_cast<long long>(d.M) + 255) / 256;
     const long long nt = (static_cast<long long>(d.N) + 255) / 256;
@@ -221,7 +254,7 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int format, in
 // Quantises an activation or gradient: token chunks of one matrix [T, cols], or `parts`
 // matrices.  calibrated: *scale is given; else (nv) it is computed here.  Neither by rows nor by
 // columns: only that.
-tpmlp_status quantize(const void* const* src, int parts, bool gather, long long rows, long long cols,
+tpmlp_status quantize(const DeviceInfo* dev, const void* const* src, int parts, bool gather, long long rows, long long cols,
                       int format, void* scale, bool calibrated, const Packed* by_rows,
                       const Packed* by_cols, float* sums, long long sums_ld, cudaStream_t st) {
     Fp4QuantParams p;
@@ -232,9 +265,13 @@ tpmlp_status quantize(const void* const* src, int parts, bool gather, long long 
     p.cols = cols;
     p.scale = static_cast<const float*>(scale);
     p.sums_ld = sums_ld;
+    p.err = dev->err;
+    p.timeout_ns = g_timeout_ns;
+    p.stall = g_stall;
     const int outs = gather ? 1 : parts;
     for (int i = 0; i < parts; ++i) p.src[i] = src[i];
     for (int i = 0; i < outs; ++i) {
+        if (by_rows) p.rows_k = by_rows->k;
         if (by_rows) p.q_rows[i] = by_rows->q[i], p.s_rows[i] = by_rows->s[i];
         if (by_cols) p.q_cols[i] = by_cols->q[i], p.s_cols[i] = by_cols->s[i];
         if (sums) p.sums[i] = sums + i * cols;
@@ -287,7 +324,7 @@ tpmlp_status forward(Split k, const tpmlp_linear_dims* dims, int format, const v
     if (s.T == 0) return TPMLP_OK;
     const int K = col ? s.in : s.shard;
     uint8_t* at = static_cast<uint8_t*>(workspace);
-    const Packed rows = place(at, nq, s.T, K, format);
+    const Packed rows = place_segments(at, nq, s.T, K, format);
     Packed cols = {};
     for (int i = 0; save && i < nq; ++i) {
         cols.q[i] = static_cast<uint8_t*>(Xq[i]);
@@ -302,11 +339,12 @@ tpmlp_status forward(Split k, const tpmlp_linear_dims* dims, int format, const v
     // up to 16 tokens the product quantises them itself, for one launch less (one token, 4096 ->
     // 12288 features)
     p.x = s.T <= FP4_QUANT_ROWS && !save ? X : nullptr;
-    TPMLP_TRY(quantize(X, nx, col, col ? s.Tc : s.T, K, format, x_scale, x_calibrated != 0,
+    TPMLP_TRY(quantize(dev, X, nx, col, col ? s.Tc : s.T, K, format, x_scale, x_calibrated != 0,
                        p.x ? nullptr : &rows, save ? &cols : nullptr, nullptr, 0, st));
     p.a = Operand{reinterpret_cast<const void* const*>(rows.q), reinterpret_cast<const void* const*>(rows.s),
-                  nq, col ? F4_SINGLE : F4_KSEG, x_scale};
-    p.b = Operand{Wq, Ws, s.t, col ? F4_GROUP : F4_KSEG, w_scale};
+                  rows.k > 0 ? 1 : nq, rows.k > 0 || col ? F4_SINGLE : F4_KSEG, x_scale, rows.k};
+    if (p.x) p.a = Operand{nullptr, nullptr, nq, col ? F4_SINGLE : F4_KSEG, x_scale, 0};
+    p.b = Operand{Wq, Ws, s.t, col ? F4_GROUP : F4_KSEG, w_scale, 0};
     p.bias = b;
     p.f32 = false;
     p.out = Y;
@@ -343,11 +381,11 @@ tpmlp_status backward(Split k, const tpmlp_linear_dims* dims, int format, const 
     if (s.T == 0) return zero_grads(s, k, dW, db, st);
     const int width = s.out / ng;  // columns of a gradient
     uint8_t* at = static_cast<uint8_t*>(workspace);
-    const Packed rows = place(at, ng, s.T, width, format), cols = place(at, ng, width, s.T, format);
+    const Packed rows = place_segments(at, ng, s.T, width, format), cols = place(at, ng, width, s.T, format);
     float* sums = reinterpret_cast<float*>(at);
     at += align256(static_cast<size_t>(up128(s.T)) * s.out * sizeof(float));
     void* dy_scale = format == FP4_NV ? at : nullptr;
-    TPMLP_TRY(quantize(dY, ndy, !col, col ? s.T : s.Tc, width, format, dy_scale, false, &rows, &cols, sums,
+    TPMLP_TRY(quantize(dev, dY, ndy, !col, col ? s.T : s.Tc, width, format, dy_scale, false, &rows, &cols, sums,
                        s.out, st));
     TPMLP_CUDA(timed(TPMLP_KERNEL_BIAS_GRAD, 1, st, [&] {
         return launch_colsum_f32(sums, up128(s.T), s.out, s.out, static_cast<float*>(db), st);
@@ -361,8 +399,9 @@ tpmlp_status backward(Split k, const tpmlp_linear_dims* dims, int format, const 
         p.groups = col ? 1 : s.t;
         p.ksegs = col ? s.t : 1;
         p.a = Operand{reinterpret_cast<const void* const*>(rows.q),
-                      reinterpret_cast<const void* const*>(rows.s), ng, col ? F4_KSEG : F4_SINGLE, dy_scale};
-        p.b = Operand{Wq, Ws, s.t, col ? F4_KSEG : F4_GROUP, w_scale};
+                      reinterpret_cast<const void* const*>(rows.s), rows.k > 0 ? 1 : ng,
+                      col && rows.k == 0 ? F4_KSEG : F4_SINGLE, dy_scale, rows.k};
+        p.b = Operand{Wq, Ws, s.t, col ? F4_KSEG : F4_GROUP, w_scale, 0};
         p.bias = nullptr;
         p.f32 = false;
         p.out = dX;
@@ -379,9 +418,9 @@ tpmlp_status backward(Split k, const tpmlp_linear_dims* dims, int format, const 
         p.K = s.T;
         p.groups = s.t;
         p.ksegs = 1;
-        p.a = Operand{Xq, Xs, nx, col ? F4_SINGLE : F4_GROUP, x_scale};
+        p.a = Operand{Xq, Xs, nx, col ? F4_SINGLE : F4_GROUP, x_scale, 0};
         p.b = Operand{reinterpret_cast<const void* const*>(cols.q),
-                      reinterpret_cast<const void* const*>(cols.s), ng, col ? F4_GROUP : F4_SINGLE, dy_scale};
+                      reinterpret_cast<const void* const*>(cols.s), ng, col ? F4_GROUP : F4_SINGLE, dy_scale, 0};
         p.bias = nullptr;
         p.f32 = true;
         p.out = dW;
@@ -473,6 +512,9 @@ TPMLP_API tpmlp_status tpmlp_fp4_quantize(const tpmlp_fp4_quant* d, const void* 
         if (cols) p.q_cols[i] = static_cast<uint8_t*>(q_cols[i]), p.s_cols[i] = static_cast<uint8_t*>(s_cols[i]);
     }
     p.scale = static_cast<const float*>(scale);
+    p.err = dev->err;
+    p.timeout_ns = g_timeout_ns;
+    p.stall = g_stall;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int mode = (rows ? FP4_Q_ROWS : 0) | (cols ? FP4_Q_COLS : 0);
     TPMLP_CUDA(timed(TPMLP_KERNEL_SP_COPY, 1, st, [&] { return launch_fp4_quant(p, d->format, mode, st); }));

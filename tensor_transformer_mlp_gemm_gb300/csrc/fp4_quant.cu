@@ -5,14 +5,18 @@
 // element and grouping.  So both groupings of a matrix, and the column sums of a gradient
 // (the bias gradient), come from one read.
 //
-// A CTA takes a 128 x 128 tile: whole groups, and whole blocks of scales, both ways.  For
-// the rows a thread holds 8 rows x 8 columns as eight 16-byte loads, all in flight before
-// the first use.  For the columns the tile goes through shared memory, and a thread takes
-// 32 rows of two columns, which is 16 bytes of each column's output.
+// A CTA takes 128 x 128 tiles, whole groups and whole blocks of scales both ways, and copies the
+// next into shared memory under the arithmetic of one.  A thread takes 32 columns of two rows,
+// then 32 rows of two columns: whole groups, 16 bytes of each output.  (Tiles loaded into
+// registers, 8 rows x 8 columns a thread, had every lane of a group work out its scale and
+// nothing on the way meanwhile: both groupings of 16384 x 4096 43 us, now 40, with the sums 46,
+// now 42; threads of 16 rows or columns, 512 in a CTA, took 45 us.)  It issues in two thirds of
+// the cycles: two instructions a value and grouping for the conversion alone, 2.5 of nv.
 #include <cuda_fp16.h>
 
 #include "fp4_cvt.cuh"
 #include "fp4_quant.cuh"
+#include "fp8_mma.cuh"
 #include "ptx.cuh"
 
 namespace tpmlp {
@@ -35,28 +39,107 @@ __device__ __forceinline__ uint32_t scale_at(uint32_t r, uint32_t j) {
     return (j >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (j & 3);
 }
 
-constexpr int per_sm(int mode) { return mode & FP4_Q_COLS ? 3 : 4; }
+constexpr int Q_PER_SM = 3;
+// A row of a tile in shared memory takes 17 times 16 bytes, and every 32 rows 32 bytes more: the
+// eight rows that a quarter of a warp reads 16 bytes of, and the four runs of 32 rows that a
+// warp reads words of, meet different banks.
+constexpr int Q_PITCH = 272;
+constexpr int Q_STAGE = 35072;
+__device__ __forceinline__ uint32_t row_at(int r) { return r * Q_PITCH + (r >> 5) * 32; }
+static_assert(127 * Q_PITCH + 3 * 32 + 256 <= Q_STAGE && Q_STAGE % 128 == 0, "a tile's rows");
+constexpr int Q_SMEM = 2 * Q_STAGE;
+static_assert(Q_PER_SM * (Q_SMEM + 4 * 1024 + 1024) <= 228 * 1024, "shared memory of an SM");
+
+// The pair of largest magnitudes among 8 values.
+__device__ __forceinline__ uint32_t largest2(const uint4& v) {
+    return larger(larger(v.x, v.y), larger(v.z, v.w));
+}
+
+// Copies `bytes` (a multiple of 16) to shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
 
 template <int FMT, int MODE>
-__global__ void __launch_bounds__(QT, per_sm(MODE))
-    fp4_quant_kernel(const __grid_constant__ Fp4QuantParams p, int col_tiles) {
+__global__ void __launch_bounds__(QT, Q_PER_SM)
+    fp4_quant_kernel(const __grid_constant__ Fp4QuantParams p, unsigned row_tiles, unsigned col_tiles,
+                     unsigned tiles) {
     constexpr bool ROWS = MODE & FP4_Q_ROWS, COLS = MODE & FP4_Q_COLS, SUMS = MODE & FP4_Q_SUMS;
     constexpr int SB = fp4_scale_step(FMT) / 2;  // bytes of a tile's scales
     constexpr int PER = FMT == FP4_NV ? 2 : 1;   // groups of 32 elements
-    __shared__ uint4 s_tile[COLS ? TILE * TILE / 8 : 1];  // [row][column / 8], columns as below
-    __shared__ alignas(16) uint8_t s_rows[ROWS ? SB : 16];
-    __shared__ alignas(16) uint8_t s_cols[COLS ? SB : 16];
+    extern __shared__ __align__(128) uint8_t s_tiles[];
+    __shared__ alignas(16) uint8_t s_rows[2][ROWS ? SB : 16];
+    __shared__ alignas(16) uint8_t s_cols[2][COLS ? SB : 16];
+    __shared__ alignas(8) uint64_t s_bar[2];
+    __shared__ volatile int s_abort;
 
-    const int part = p.gather ? 0 : blockIdx.y;
-    const long long rt = blockIdx.x / col_tiles, ct = blockIdx.x % col_tiles;
-    const long long r0 = rt * TILE, c0 = ct * TILE;
     const long long total = p.gather ? p.rows * p.parts : p.rows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cv = lane & 15;                 // this thread's 8 columns
-    const int slot = warp * 2 + (lane >> 4);  // its rows: slot + 16 i
-    const long long c = c0 + cv * 8;
-    const bool col_in = c < p.cols;
+    const uint32_t tile0 = ptx::smem_u32(s_tiles), bar0 = ptx::smem_u32(s_bar);
 
+    // Tiles part by part, row by row, each CTA every gridDim.x-th; stepped, not divided out.
+    struct Tile {
+        unsigned part, rt, ct;
+    };
+    const unsigned each = row_tiles * col_tiles;
+    auto tile_of = [&](unsigned t) { return Tile{t / each, t % each / col_tiles, t % col_tiles}; };
+    const Tile step = tile_of(gridDim.x);
+    auto next_of = [&](Tile x) {
+        x.ct += step.ct;
+        x.rt += step.rt;
+        x.part += step.part;
+        if (x.ct >= col_tiles) {
+            x.ct -= col_tiles;
+            ++x.rt;
+        }
+        if (x.rt >= row_tiles) {
+            x.rt -= row_tiles;
+            ++x.part;
+        }
+        return x;
+    };
+    // Starts a tile's way into buffer b: thread r copies row r, and zeroes what the matrix does
+    // not have of it.
+    int loads = 0;
+    auto load = [&](const Tile& x, int b) {
+        if (blockIdx.x == gridDim.x - 1 && loads == p.stall) return;
+        ++loads;
+        const long long r0 = static_cast<long long>(x.rt) * TILE, c0 = static_cast<long long>(x.ct) * TILE;
+        const int rows = total - r0 < TILE ? static_cast<int>(max(0LL, total - r0)) : TILE;
+        const int bytes = 2 * (p.cols - c0 < TILE ? static_cast<int>(max(0LL, p.cols - c0)) : TILE);
+        if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bar0 + 8 * b, rows * bytes);
+        if (threadIdx.x < TILE) {
+            const int r = threadIdx.x;
+            const int here = r < rows ? bytes : 0;
+            if (here > 0) {
+                unsigned from = x.part;
+                long long row = r0 + r;
+                if (p.gather && p.parts > 1) {  // (chunks of whole tiles)
+                    const unsigned chunk = static_cast<unsigned>(p.rows / TILE);
+                    from = x.rt / chunk;
+                    row -= static_cast<long long>(from) * p.rows;
+                }
+                bulk_load(tile0 + b * Q_STAGE + row_at(r),
+                          static_cast<const uint16_t*>(p.src[from]) + row * p.cols + c0, here, bar0 + 8 * b);
+            }
+            if (here < 2 * TILE) {
+                uint4* to = reinterpret_cast<uint4*>(s_tiles + b * Q_STAGE + row_at(r));
+                for (int i = here / 16; i < TILE / 8; ++i) to[i] = make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(bar0, 1);
+        ptx::mbar_init(bar0 + 8, 1);
+        s_abort = 0;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    __syncthreads();
     // The dependent launch after the wait: what came before this grid has ended when it starts,
     // so that it may read weights before this grid ends.
     ptx::griddep_wait();
@@ -64,150 +147,174 @@ __global__ void __launch_bounds__(QT, per_sm(MODE))
 
     float inv_g = 0.0f;
     if constexpr (FMT == FP4_NV) inv_g = inverse_of(p.scale);
-    int from = part;
-    long long before = 0;  // rows of the parts before this one
-    if (p.gather && r0 < total) {
-        from = static_cast<int>(r0 / p.rows);
-        before = from * p.rows;
-    }
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.src[from]) + c);
-    const long long vstep = p.cols / 8;
-    uint4 v[8];
+    int b = 0;
+    uint32_t phase = 0;
+    Tile x = tile_of(blockIdx.x);
+    load(x, 0);
+    __syncthreads();  // (zeroes)
+    int done = 0;
+    for (unsigned t = blockIdx.x; t < tiles; t += gridDim.x, ++done) {
+        const Tile next = next_of(x);
+        if (t + gridDim.x < tiles) load(next, b ^ 1);
+        const bool ok = f8::wait(bar0 + 8 * b, phase, &s_abort, p.timeout_ns, p.err, ERR_EPILOGUE);
+        const long long r0 = static_cast<long long>(x.rt) * TILE, c0 = static_cast<long long>(x.ct) * TILE;
+        const uint8_t* tile = s_tiles + b * Q_STAGE;
+        if (ROWS && ok) {
+            const int run = lane >> 3;  // a thread takes 32 columns of two rows
+            const long long c = c0 + run * 32;
+            uint8_t* q = p.q_rows[x.part];
+            const long long ld = fp4_ld(p.rows_k);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const long long r = r0 + slot + 16 * i;
-        v[i] = (col_in && r < total) ? __ldg(src + (r - before) * vstep) : make_uint4(0, 0, 0, 0);
-    }
-
-    if constexpr (COLS) {
-        // 16-byte vector cv of a row lies at cv ^ 2 (row / 32), so that a warp's reads below
-        // meet 32 banks
+            for (int i = 0; i < 2; ++i) {
+                const int r = warp * 16 + (lane & 7) + 8 * i;
+                const uint4* src = reinterpret_cast<const uint4*>(tile + row_at(r) + run * 64);
+                const uint4 v[4] = {src[0], src[1], src[2], src[3]};
+                uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = slot + 16 * i;
-            s_tile[r * 16 + (cv ^ ((r >> 5) << 1))] = v[i];
-        }
-    }
-    if constexpr (ROWS) {
-        // largest magnitudes of each row's groups, two rows in a word
-        uint32_t rm[4];
+                for (int h = 0; h < PER; ++h) {
+                    uint32_t m = larger(largest2(v[h * 2]), largest2(v[h * 2 + 1]));
+                    if constexpr (PER == 1) m = larger(m, larger(largest2(v[2]), largest2(v[3])));
+                    const Scale4 sc = scale_of<FMT>(fold(m), inv_g);
+                    s_rows[b][scale_at(r, run * PER + h)] = static_cast<uint8_t>(sc.byte);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rm[i] = largest(v[2 * i]) | largest(v[2 * i + 1]) << 16;
+                    for (int j = h * (4 / PER); j < (h + 1) * (4 / PER); ++j) {
+                        float2 f[4];
 #pragma unroll
-        for (int o = 1; o < 4 / PER; o <<= 1)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rm[i] = larger(rm[i], __shfl_xor_sync(0xffffffffu, rm[i], o));
-        const uint32_t group = PER == 2 ? cv >> 1 : cv >> 2;
-        uint8_t* q = p.q_rows[part];
-        const long long ld = fp4_ld(p.cols);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const Scale4 sc = scale_of<FMT>((i & 1 ? rm[i / 2] >> 16 : rm[i / 2]) & 0x7FFFu, inv_g);
-            const int r = slot + 16 * i;
-            if (cv % (4 / PER) == 0) s_rows[scale_at(r, group)] = static_cast<uint8_t>(sc.byte);
-            if (col_in && r0 + r < total) {
-                float2 f[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t w = word(v[i], j);
-                    f[j] = scaled<FMT>(make_float2(lo_f(w), hi_f(w)), sc.inv);
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t w = word(v[j], e);
+                            f[e] = scaled<FMT>(make_float2(lo_f(w), hi_f(w)), sc.inv);
+                        }
+                        o[j] = cvt8(f[0], f[1], f[2], f[3]);
+                        if (!(sc.inv > 0.0f)) o[j] = 0;
+                    }
                 }
-                const uint32_t u = cvt8(f[0], f[1], f[2], f[3]);
-                *reinterpret_cast<uint32_t*>(q + (r0 + r) * ld + c / 2) = sc.inv > 0.0f ? u : 0u;
+                if (c < p.cols && r0 + r < total)
+                    *reinterpret_cast<uint4*>(q + (r0 + r) * ld + c / 2) = make_uint4(o[0], o[1], o[2], o[3]);
             }
         }
-    }
-    __syncthreads();
-
-    if constexpr (COLS) {
-        const int g = lane & 3, cp = warp * 8 + (lane >> 2);  // 32 rows, two columns
-        const uint32_t* tile = reinterpret_cast<const uint32_t*>(s_tile) + g * 32 * 64 + (cp ^ (g << 3));
-        uint32_t w[32];
+        if (COLS && ok) {
+            const int g = lane & 3, cp = warp * 8 + (lane >> 2);  // 32 rows, two columns
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(tile + row_at(32 * g)) + cp;
+            uint32_t w[32];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) w[k] = tile[k * 64];
-        const long long cc = c0 + 2 * cp;
-        if constexpr (SUMS) {
-            // 32 rows in order, then the four groups of them
-            float2 t = make_float2(lo_f(w[0]), hi_f(w[0]));
-#pragma unroll
-            for (int k = 1; k < 32; ++k) t = __fadd2_rn(t, make_float2(lo_f(w[k]), hi_f(w[k])));
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
-                t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
-            }
-            if (g == 0 && cc < p.cols && r0 < total)
-                *reinterpret_cast<float2*>(p.sums[part] + rt * p.sums_ld + cc) = t;
-        }
-        const long long ld = fp4_ld(total);
-        const bool in = cc < p.cols && r0 + 32 * g < total;
-        uint8_t* q = p.q_cols[part] + cc * ld + r0 / 2 + g * 16;
-        uint32_t m[PER];
-#pragma unroll
-        for (int h = 0; h < PER; ++h) {
-            m[h] = w[h * (32 / PER)];
-#pragma unroll
-            for (int k = 1; k < 32 / PER; ++k) m[h] = larger(m[h], w[h * (32 / PER) + k]);
-        }
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {  // the even column, the odd one
-            uint32_t o[4];
-            Scale4 sc[PER];
+            for (int k = 0; k < 32; ++k) w[k] = src[k * (Q_PITCH / 4)];
+            const long long cc = c0 + 2 * cp;
+            const long long ld = fp4_ld(total);
+            const bool in = cc < p.cols && r0 + 32 * g < total;
+            uint8_t* q = p.q_cols[x.part] + cc * ld + r0 / 2 + g * 16;
+            uint32_t m[PER];
 #pragma unroll
             for (int h = 0; h < PER; ++h) {
-                sc[h] = scale_of<FMT>((side ? m[h] >> 16 : m[h]) & 0x7FFFu, inv_g);
-                s_cols[scale_at(2 * cp + side, g * PER + h)] = static_cast<uint8_t>(sc[h].byte);
+                m[h] = w[h * (32 / PER)];
+#pragma unroll
+                for (int k = 1; k < 32 / PER; ++k) m[h] = larger(m[h], w[h * (32 / PER) + k]);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const Scale4& s = sc[j * PER / 4];
-                float2 f[4];
+            for (int side = 0; side < 2; ++side) {  // the even column, the odd one
+                uint32_t o[4];
+                Scale4 sc[PER];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t a = w[8 * j + 2 * i], b = w[8 * j + 2 * i + 1];
-                    f[i] = scaled<FMT>(side ? make_float2(hi_f(a), hi_f(b)) : make_float2(lo_f(a), lo_f(b)),
-                                       s.inv);
+                for (int h = 0; h < PER; ++h) {
+                    sc[h] = scale_of<FMT>((side ? m[h] >> 16 : m[h]) & 0x7FFFu, inv_g);
+                    s_cols[b][scale_at(2 * cp + side, g * PER + h)] = static_cast<uint8_t>(sc[h].byte);
                 }
-                o[j] = cvt8(f[0], f[1], f[2], f[3]);
-                if (!(s.inv > 0.0f)) o[j] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const Scale4& s = sc[j * PER / 4];
+                    float2 f[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t u = w[8 * j + 2 * i], y = w[8 * j + 2 * i + 1];
+                        f[i] = scaled<FMT>(side ? make_float2(hi_f(u), hi_f(y)) : make_float2(lo_f(u), lo_f(y)),
+                                           s.inv);
+                    }
+                    o[j] = cvt8(f[0], f[1], f[2], f[3]);
+                    if (!(s.inv > 0.0f)) o[j] = 0;
+                }
+                if (in) *reinterpret_cast<uint4*>(q + side * ld) = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            if (in) *reinterpret_cast<uint4*>(q + side * ld) = make_uint4(o[0], o[1], o[2], o[3]);
+            if constexpr (SUMS) {
+                // 32 rows in order, then the four groups of them; read again, which takes fewer
+                // registers than they have until here
+                asm volatile("" ::: "memory");
+                float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll 8
+                for (int k = 0; k < 32; ++k) {
+                    const uint32_t u = src[k * (Q_PITCH / 4)];
+                    s = __fadd2_rn(s, make_float2(lo_f(u), hi_f(u)));
+                }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+                    s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+                }
+                if (g == 0 && cc < p.cols && r0 < total)
+                    *reinterpret_cast<float2*>(p.sums[x.part] + x.rt * p.sums_ld + cc) = s;
+            }
         }
-        __syncthreads();
-    }
-
-    // the tile's scales, as they lie
-    if (threadIdx.x < SB / 16) {
-        const int i = threadIdx.x * 16;
-        if (ROWS && r0 < total) {
-            uint8_t* s = p.s_rows[part] + rt * ((p.cols + 255) / 256) * (2 * SB) + ct * SB + i;
-            *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(s_rows + i);
+        // the buffer has been read and the scales are there; who gave up takes the others along
+        ptx::fence_proxy_async_smem();
+        if (__syncthreads_or(!ok)) {
+            // what is still on its way lands before the CTA leaves
+            if (threadIdx.x == 0) {
+                if (loads > done) f8::drain(bar0 + 8 * b, phase, p.timeout_ns, p.err);
+                if (loads > done + 1) f8::drain(bar0 + 8 * (b ^ 1), phase ^ b, p.timeout_ns, p.err);
+            }
+            return;
         }
-        if (COLS && c0 < p.cols) {
-            uint8_t* s = p.s_cols[part] + ct * ((total + 255) / 256) * (2 * SB) + rt * SB + i;
-            *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(s_cols + i);
+        if (threadIdx.x < SB / 16) {
+            const int i = threadIdx.x * 16;
+            if (ROWS && r0 < total) {
+                uint8_t* s = p.s_rows[x.part] + x.rt * ((p.rows_k + 255) / 256) * (2 * SB) + x.ct * SB + i;
+                *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(&s_rows[b][i]);
+            }
+            if (COLS && c0 < p.cols) {
+                uint8_t* s = p.s_cols[x.part] + x.ct * ((total + 255) / 256) * (2 * SB) + x.rt * SB + i;
+                *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(&s_cols[b][i]);
+            }
         }
+        phase ^= b;
+        b ^= 1;
+        x = next;
     }
 }
 
 template <int FMT, int MODE>
 cudaError_t launch(const Fp4QuantParams& p, cudaStream_t st) {
+    constexpr int kDevices = 64;
+    static int sms[kDevices] = {};  // asked once a device, with the kernel's attribute
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    int n = __atomic_load_n(&sms[dev], __ATOMIC_ACQUIRE);
+    if (n == 0) {
+        e = cudaFuncSetAttribute(fp4_quant_kernel<FMT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q_SMEM);
+        if (e != cudaSuccess) return e;
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&sms[dev], n, __ATOMIC_RELEASE);
+    }
     const long long total = p.gather ? p.rows * p.parts : p.rows;
     long long rt = (total + TILE - 1) / TILE, ct = (p.cols + TILE - 1) / TILE;
     // scales are filled up to 256 along the grouped axis
     if (MODE & FP4_Q_ROWS) ct += ct & 1;
     if (MODE & FP4_Q_COLS) rt += rt & 1;
-    if (ct > 0x7FFFFFFFLL || rt > 0x7FFFFFFFLL / ct) return cudaErrorInvalidValue;
+    const long long parts = p.gather ? 1 : p.parts;
+    if (rt > 0x7FFFFFFFLL / ct / parts) return cudaErrorInvalidValue;
+    const long long tiles = rt * ct * parts, most = static_cast<long long>(n) * Q_PER_SM;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(rt * ct), static_cast<unsigned>(p.gather ? 1 : p.parts), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles < most ? tiles : most), 1, 1);
     cfg.blockDim = dim3(QT, 1, 1);
+    cfg.dynamicSmemBytes = Q_SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fp4_quant_kernel<FMT, MODE>, p, static_cast<int>(ct));
+    return cudaLaunchKernelEx(&cfg, fp4_quant_kernel<FMT, MODE>, p, static_cast<unsigned>(rt),
+                              static_cast<unsigned>(ct), static_cast<unsigned>(tiles));
 }
 
 template <int FMT>
@@ -340,7 +447,9 @@ __global__ void __launch_bounds__(DT, 4)
 
 }  // namespace
 
-cudaError_t launch_fp4_quant(const Fp4QuantParams& p, int fmt, int mode, cudaStream_t st) {
+cudaError_t launch_fp4_quant(const Fp4QuantParams& params, int fmt, int mode, cudaStream_t st) {
+    Fp4QuantParams p = params;
+    if (p.rows_k == 0) p.rows_k = p.cols;
     return fmt == FP4_NV ? launch_mode<FP4_NV>(p, mode, st) : launch_mode<FP4_MX>(p, mode, st);
 }
 

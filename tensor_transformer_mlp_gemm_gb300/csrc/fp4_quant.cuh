@@ -55,7 +55,11 @@ struct Fp4QuantParams {
     float* sums[FP4_MAX_PARTS];       // column sums of each 128 rows, [ceil(R/128)][sums_ld]
     const float* scale;               // g (nv)
     long long rows, cols, sums_ld;
+    long long rows_k;                 // K of q_rows and s_rows, of which a part is `cols`; 0: cols
     int parts, gather;
+    unsigned int* err;                // the device error word and the limit of any one wait
+    unsigned long long timeout_ns;
+    int stall;                        // failure-detection self-test: the last CTA loads this many tiles; < 0: all
 };
 
 enum Fp4QuantMode : int { FP4_Q_ROWS = 1, FP4_Q_COLS = 2, FP4_Q_SUMS = 4 };  // SUMS with both

@@ -137,12 +137,13 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
             // B's part of stage `stage`; scales of 128 rows lie next to each other along K
             constexpr uint32_t X_BYTES = QUANT ? TN * 128 + C::kScales : 0;  // written here, not copied
             const long long along = static_cast<long long>(kblocks) * C::kScales;
+            const long long along_a = p.a_seg ? along * p.ksegs : along;
             auto load_b = [&](int st, int seg, int block) {
                 const uint32_t sw = base + st * C::kStageBytes, full = bar_full + 8 * st;
                 const int wi = f4::pick(p.b_part, g, seg);
                 ptx::mbar_arrive_expect_tx(full, C::kStageBytes - X_BYTES);
                 // (a byte holds two of K)
-                ptx::tma_load_2d(sw, p.b_map + wi, block * 128, f0, full);
+                ptx::tma_load_3d(sw, p.b_map + (p.b_z ? 0 : wi), block * 128, f0, p.b_z ? wi : 0, full);
                 bulk_load(sw + F4_BOX_BYTES + TN * 128, p.sb[wi] + (f0 >> 7) * along + block * C::kScales,
                           C::kScales, full);
             };
@@ -166,13 +167,14 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
                 if constexpr (!QUANT) {
                     const uint32_t sw = base + stage * C::kStageBytes, full = bar_full + 8 * stage;
                     const int xi = f4::pick(p.a_part, g, s);
-                    ptx::tma_load_2d(sw + F4_BOX_BYTES, p.a_map + xi, kb * 128, t0, full);
+                    const int ka = s * p.a_seg + kb;
+                    ptx::tma_load_3d(sw + F4_BOX_BYTES, p.a_map + (p.a_z ? 0 : xi), ka * 128, t0, p.a_z ? xi : 0, full);
 #pragma unroll
                     for (int i = 0; i < C::kTiles; ++i) {
                         // (behind the last token any: nobody reads those sums)
                         const int at = t0 + 128 * i < p.M ? (t0 >> 7) + i : 0;
                         bulk_load(sw + F4_BOX_BYTES + TN * 128 + (1 + i) * C::kScales,
-                                  p.sa[xi] + at * along + kb * C::kScales, C::kScales, full);
+                                  p.sa[xi] + at * along_a + ka * C::kScales, C::kScales, full);
                     }
                 }
                 ++fills;

@@ -395,3 +395,53 @@ def test_forward_between_keeps_what_was_saved():
     lay.backward(dY)
     _sync()
     _check_backward(lay, X, dY)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("split,T,din,dout,t", [
+    ("column", 1, 4096, 1056, 1), ("column", 7, 288, 416, 1), ("row", 1, 256, 256, 2), ("row", 16, 1088, 416, 2),
+    ("row", 9, 4096, 1024, 8), ("column", 16, 32, 32, 1), ("column", 13, 9248, 2048, 2),
+    ("row", 17, 1024, 416, 2), ("row", 40, 1088, 416, 2)])
+@pytest.mark.parametrize("calibrated", [False, True])
+def test_forward_alone(split, T, din, dout, t, fmt, calibrated):
+    """Without keeping X, where few tokens are quantised on the way; the same result as with."""
+    if calibrated and fmt == "mxfp4":
+        pytest.skip("mxfp4 has no scale to calibrate")
+    w = custom_linear(T, din, dout, t, split)
+    lay, X, dY = _layer(w, T + din, fmt, x_scale=torch.full((1,), 2.0 ** -9, device="cuda") if calibrated else None)
+    X[0][0, 3] = 40.0
+    g = GuardBands()
+    g.guard(lay, ["Y", "ws"])
+    lay.forward(X)
+    _sync()
+    g.check()
+    _check_forward(lay, X)
+    alone = [y.clone() for y in lay.Y]
+    lay.forward(X, save=True)
+    _sync()
+    assert all(torch.equal(a, b) for a, b in zip(alone, lay.Y))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_forward_alone_not_finite(fmt):
+    w = custom_linear(5, 1024, 288, 2, "row")
+    lay, X, _ = _layer(w, 3, fmt)
+    X[1][3, 77] = float("nan")
+    lay.forward(X)
+    _sync()
+    nan = torch.isnan(lay.Y[0])
+    assert nan[3].all() and int(nan.sum()) == 288
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("split,T,din,dout,t", [("row", 300, 2048, 416, 4), ("column", 300, 416, 2048, 8),
+                                                ("row", 1100, 1024, 2048, 2), ("column", 60, 288, 1024, 4)])
+def test_segments_of_whole_stages(split, T, din, dout, t, fmt):
+    """Shards that are multiples of 256, whose 4-bit segments lie in one matrix."""
+    w = custom_linear(T, din, dout, t, split)
+    lay, X, dY = _layer(w, T + din, fmt)
+    lay.forward(X, save=True)
+    lay.backward(dY)
+    _sync()
+    _check_forward(lay, X)
+    _check_backward(lay, X, dY)
