@@ -59,11 +59,13 @@ cudaError_t launch_fp4_gemm(const Fp4GemmParams& p, int fmt, bool f32, cudaStrea
 
 // The same (bf16 output) for few rows of A: tiles of 128 columns by `rows` rows of A, which
 // is also the box of A's maps, with K cut over up to 8 CTAs of a cluster.
-// A comes in 4 bits, or up to FP4_QUANT_ROWS rows of it in bf16 (quantise).
-constexpr int FP4_QUANT_ROWS = 16;
+// A comes in 4 bits, or (quantise: up to FP4_QUANT_ROWS rows) in bf16.
+constexpr int FP4_QUANT_ROWS = 32;
 cudaError_t launch_fp4_small(const Fp4GemmParams& p, int fmt, int rows, bool quantise, cudaStream_t st);
 // Those rows for a product of this shape on the current device; 0: it has rows and
 // columns enough for the pairs.
 cudaError_t fp4_small_rows(int M, int N, int groups, int fmt, int& rows);
+// Whether few rows are quantised faster by the product itself than by a launch ahead of it.
+cudaError_t fp4_small_quantises(int M, int N, int K, int groups, int ksegs, bool& quantises);
 
 }  // namespace tpmlp

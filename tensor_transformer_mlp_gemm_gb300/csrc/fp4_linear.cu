@@ -106,7 +106,7 @@ Packed place(uint8_t*& at, int n, long long R, long long K, int format) {
 
 // The same for segments of K that a product sums: where each is whole stages of K, as one
 // matrix [R, n K] (one tensor map in the place of n, and rows that lie further apart: forward
-// of 16384 x 4096 x 4096 in eight segments JOINEDUS).
+// of 16384 x 4096 x 4096 in eight segments in one map).
 Packed place_segments(uint8_t*& at, int n, long long R, long long K, int format) {
     if (n == 1 || K % F4_BK != 0) return place(at, n, R, K, format);
     Packed o = place(at, 1, R, n * K, format);
@@ -336,9 +336,10 @@ tpmlp_status forward(Split k, const tpmlp_linear_dims* dims, int format, const v
     p.K = K;
     p.groups = col ? s.t : 1;
     p.ksegs = col ? 1 : s.t;
-    // up to 16 tokens the product quantises them itself, for one launch less (one token, 4096 ->
-    // 12288 features)
-    p.x = s.T <= FP4_QUANT_ROWS && !save ? X : nullptr;
+    // (to keep X by columns takes the launch anyway)
+    bool quantises = false;
+    if (!save) TPMLP_CUDA(fp4_small_quantises(p.M, p.N, p.K, p.groups, p.ksegs, quantises));
+    p.x = quantises ? X : nullptr;
     TPMLP_TRY(quantize(dev, X, nx, col, col ? s.Tc : s.T, K, format, x_scale, x_calibrated != 0,
                        p.x ? nullptr : &rows, save ? &cols : nullptr, nullptr, 0, st));
     p.a = Operand{reinterpret_cast<const void* const*>(rows.q), reinterpret_cast<const void* const*>(rows.s),

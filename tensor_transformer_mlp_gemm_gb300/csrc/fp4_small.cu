@@ -47,6 +47,7 @@ struct Small {
                                      : kSums + kStages * kSlot <= 256 ? 256
                                                                       : 512;
     static constexpr int kPerSm = PER_SM;
+    static constexpr int kSharing = TN <= 16 ? 1 : 2;    // warps that quantise a stage
     static_assert(kStages >= 3 && kStageBytes % 1024 == 0, "stages");
     static_assert(kSums + kStages * kSlot <= 512 / kPerSm, "tensor memory");
     static_assert(TN * 128 * 4 <= kStages * kStageBytes, "the sums fit where the operands were");
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, QUANT ? 1 + S_WARPS : 1);
+            ptx::mbar_init(bar_full + 8 * s, QUANT ? 1 + C::kSharing : 1);
             ptx::mbar_init(bar_empty + 8 * s, 1);
         }
         ptx::mbar_init(bar_done, 1);
@@ -234,92 +235,104 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
         ptx::griddep_wait();
         if constexpr (QUANT) {
-            // A: a thread takes 32 of a row of each stage, 16 bytes of its 128-byte swizzle row
-            static_assert(TN == 16 && C::kTiles == 1, "eight threads a row");
+            // A: a warp takes 16 rows of every stage that is its own, each lane 32 of every fourth
+            // of them, 16 bytes of a 128-byte swizzle row.  What lies behind the last token is
+            // left: nobody reads those sums.  (With all four warps at each stage a stage took
+            // 1.2 us from one wait to the next: 12288 -> 36864 features, 48 stages a CTA, 8 tokens
+            // 63 us, now 42.)
             constexpr int PER = FMT == FP4_NV ? 2 : 1;  // groups of 32
-            const int i = q * 32 + lane, row = i >> 3, run = i & 7;
+            constexpr int N = 4;                        // rows of a lane
+            constexpr int SHARE = C::kSharing, TURN = S_WARPS / SHARE;
+            const int row0 = (q % SHARE) * 16 + (lane >> 3), run = lane & 7;
             float inv_g = 0.0f;
             if constexpr (FMT == FP4_NV) inv_g = q4::inverse_of(p.ga);
-            int s = first / kblocks, kb = first - s * kblocks;
-            auto fetch = [&](uint4 (&v)[4]) {
+            auto fetch = [&](int stage_k, uint4 (&v)[N][4]) {
+                const int s = stage_k / kblocks, kb = stage_k - s * kblocks;
                 const int k = kb * F4_BK + run * 32;
-                const bool in = row < p.M && k < p.K;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(p.x[f4::pick(p.a_part, g, s)]) +
-                    (in ? static_cast<long long>(row) * p.K + k : 0));
+                const uint16_t* src = static_cast<const uint16_t*>(p.x[f4::pick(p.a_part, g, s)]) + k;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = in ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-                if (++kb == kblocks) {
-                    kb = 0;
-                    ++s;
+                for (int n = 0; n < N; ++n) {
+                    const int row = row0 + 4 * n;
+                    const bool in = row < p.M && k < p.K;
+                    const uint4* at = reinterpret_cast<const uint4*>(src + static_cast<long long>(row) * p.K);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[n][j] = in ? __ldg(at + j) : make_uint4(0, 0, 0, 0);
                 }
             };
-            uint8_t* to = gbase + F4_BOX_BYTES + row * 128 + ((run ^ (row & 7)) << 4);
-            uint8_t* scales = gbase + F4_BOX_BYTES + TN * 128 + C::kScales + row * 16;
-            uint4 next[4];
-            if (first < last) fetch(next);
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int k = first; k < last; ++k) {
-                uint4 v[4] = {next[0], next[1], next[2], next[3]};
-                if (k + 1 < last) fetch(next);
-                uint32_t o[4];
-                uint32_t byte[PER];
+            uint4 next[N][4];
+            int k = first + q / SHARE;
+            if (k < last) fetch(k, next);
+            for (; k < last; k += TURN) {
+                uint4 o[N];
+                uint32_t byte[N][PER];
 #pragma unroll
-                for (int h = 0; h < PER; ++h) {
-                    uint32_t m = q4::larger(q4::largest(v[2 * h]), q4::largest(v[2 * h + 1]));
-                    if constexpr (PER == 1)
-                        m = q4::larger(m, q4::larger(q4::largest(v[2]), q4::largest(v[3])));
-                    const q4::Scale4 sc = q4::scale_of<FMT>(m & 0x7FFFu, inv_g);
-                    byte[h] = sc.byte;
+                for (int n = 0; n < N; ++n) {
+                    const uint4* v = next[n];
+                    uint32_t w4[4];
 #pragma unroll
-                    for (int j = h * (4 / PER); j < (h + 1) * (4 / PER); ++j) {
-                        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-                        float2 f[4];
+                    for (int h = 0; h < PER; ++h) {
+                        uint32_t m = q4::larger(q4::largest(v[2 * h]), q4::largest(v[2 * h + 1]));
+                        if constexpr (PER == 1)
+                            m = q4::larger(m, q4::larger(q4::largest(v[2]), q4::largest(v[3])));
+                        const q4::Scale4 sc = q4::scale_of<FMT>(m & 0x7FFFu, inv_g);
+                        byte[n][h] = sc.byte;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            f[e] = q4::scaled<FMT>(make_float2(q8::lo_f(w[e]), q8::hi_f(w[e])), sc.inv);
-                        o[j] = sc.inv > 0.0f ? q4::cvt8(f[0], f[1], f[2], f[3]) : 0u;
+                        for (int j = h * (4 / PER); j < (h + 1) * (4 / PER); ++j) {
+                            const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                            float2 f[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                f[e] = q4::scaled<FMT>(make_float2(q8::lo_f(w[e]), q8::hi_f(w[e])), sc.inv);
+                            w4[j] = sc.inv > 0.0f ? q4::cvt8(f[0], f[1], f[2], f[3]) : 0u;
+                        }
                     }
+                    o[n] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                    if ((q % SHARE) * 16 + 4 * (n + 1) >= p.M) break;  // (the rest behind the last token)
                 }
+                if (k + TURN < last) fetch(k + TURN, next);
+                const int stage = (k - first) % NST;
+                const uint32_t phase = static_cast<uint32_t>((k - first) / NST) & 1u;
                 const bool ok = __all_sync(0xffffffffu, wait(bar_empty + 8 * stage, phase ^ 1u, abort_flag,
                                                              p.timeout_ns, p.err, ERR_PRODUCER));
                 if (!ok) {
                     if (lane == 0) quantised[q] = k - first;
                     break;
                 }
-                const int at = stage * C::kStageBytes;
-                *reinterpret_cast<uint4*>(to + at) = make_uint4(o[0], o[1], o[2], o[3]);
+                uint8_t* to = gbase + stage * C::kStageBytes + F4_BOX_BYTES;
+                uint8_t* scales = to + TN * 128 + C::kScales;
 #pragma unroll
-                for (int h = 0; h < PER; ++h) {
-                    const int j = run * PER + h;  // the stage's group
-                    scales[at + (j >> 2) * 512 + (j & 3)] = static_cast<uint8_t>(byte[h]);
+                for (int n = 0; n < N; ++n) {
+                    const int row = row0 + 4 * n;
+                    if (row >= p.M) break;
+                    *reinterpret_cast<uint4*>(to + row * 128 + ((run ^ (row & 7)) << 4)) = o[n];
+#pragma unroll
+                    for (int h = 0; h < PER; ++h) {
+                        const int j = run * PER + h;  // the stage's group
+                        scales[row * 16 + (j >> 2) * 512 + (j & 3)] = static_cast<uint8_t>(byte[n][h]);
+                    }
                 }
                 // for the tensor cores, which read shared memory another way
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar_full + 8 * stage);
-                if (++stage == NST) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
             }
         }
         // this CTA's sums, feature by feature of each token, where the operands were
         // (not of a CTA that has given up: copies and MMAs may still be under way there)
         if (__all_sync(0xffffffffu, wait(bar_done, 0, abort_flag, p.timeout_ns, p.err, ERR_EPILOGUE))) {
             ptx::tc_fence_after();
-            float* sums = reinterpret_cast<float*>(gbase);
-            const int f = q * 32 + lane;
+            float* sums = reinterpret_cast<float*>(gbase) + q * 32 + lane;  // a feature, token by token
+            constexpr int AT = TN < 64 ? TN : TN > 128 ? 16 : 64;  // columns on the way at a time
 #pragma unroll
-            for (int c = 0; c < TN / 16; ++c) {
-                float x[16];
-                load_cols16(lanes + c * 16, x);
+            for (int c = 0; c < TN; c += AT) {
+                float x[AT];
+#pragma unroll
+                for (int i = 0; i < AT; i += 16) load_cols16(lanes + c + i, x + i);
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < AT; ++i) {
                     asm volatile("" : "+f"(x[i]));  // used after the wait
-                    sums[(c * 16 + i) * 128 + f] = x[i];
+                    sums[(c + i) * 128] = x[i];
                 }
             }
             ptx::tc_fence_before();
@@ -337,7 +350,7 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
         for (int k = max(0, n - NST); k < n; ++k) {
             const uint32_t full = bar_full + 8 * (k % NST);
             for (int w = 0; QUANT && w < S_WARPS; ++w)
-                if (quantised[w] <= k) arrive_relaxed(full);
+                if (w / C::kSharing == k % (S_WARPS / C::kSharing) && quantised[w] <= k) arrive_relaxed(full);
             drain(full, static_cast<uint32_t>((k / NST) & 1), p.timeout_ns, p.err);
         }
         drain(bar_done, 0, p.timeout_ns, p.err);
@@ -357,13 +370,20 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
         const int here = min(TN, p.M - t0);
         for (int t = rank + warp * splits; t < here; t += (S_THREADS / 32) * splits) {
             const uint32_t at = base + (t * 128 + lane * 4) * 4;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int r = 0; r < splits; ++r) {
-                const float4 x = load_cluster(ptx::mapa_shared(at, static_cast<uint32_t>(r)));
-                s.x += x.x;
-                s.y += x.y;
-                s.z += x.z;
-                s.w += x.w;
+            // (all parts on the way before the first is added)
+            float4 x[S_MAX_SPLIT];
+#pragma unroll
+            for (int r = 0; r < S_MAX_SPLIT; ++r)
+                if (r < splits) x[r] = load_cluster(ptx::mapa_shared(at, static_cast<uint32_t>(r)));
+            float4 s = x[0];
+#pragma unroll
+            for (int r = 1; r < S_MAX_SPLIT; ++r) {
+                if (r < splits) {
+                    s.x += x[r].x;
+                    s.y += x[r].y;
+                    s.z += x[r].z;
+                    s.w += x[r].w;
+                }
             }
             if constexpr (FMT == FP4_NV) {
                 s.x = s.x * alpha.first * alpha.second;
@@ -484,12 +504,27 @@ cudaError_t fp4_small_rows(int M, int N, int groups, int fmt, int& rows) {
     return cudaSuccess;
 }
 
+cudaError_t fp4_small_quantises(int M, int N, int K, int groups, int ksegs, bool& quantises) {
+    // Every CTA quantises what it takes of the tokens.  Up to 16 that is less than a launch; up
+    // to 32 where a CTA has four stages or fewer (24 tokens, 4096 -> 4096 features 6.9 us, 8.3
+    // with a launch ahead; 32 tokens, 12288 -> 12288, sixteen stages, 26.7 and 23.4).
+    quantises = M <= 16;
+    if (M <= 16 || M > FP4_QUANT_ROWS) return cudaSuccess;
+    const int* clusters = nullptr;
+    const cudaError_t e = resident<FP4_MX, 32, 2, true>(clusters);
+    if (e != cudaSuccess) return e;
+    const long long tiles = static_cast<long long>((N + 127) / 128) * groups;
+    const long long nk = static_cast<long long>((K + F4_BK - 1) / F4_BK) * ksegs;
+    quantises = tiles * nk <= 4LL * clusters[1];
+    return cudaSuccess;
+}
+
 template <int FMT>
 static cudaError_t launch_rows(const Fp4GemmParams& p, int rows, bool quantise, cudaStream_t st) {
-    if (quantise && rows != FP4_QUANT_ROWS) return cudaErrorInvalidValue;
+    if (quantise && p.M > FP4_QUANT_ROWS) return cudaErrorInvalidValue;
     switch (rows) {
         case 16: return quantise ? launch<FMT, 16, 2, true>(p, st) : launch<FMT, 16, 2, false>(p, st);
-        case 32: return launch<FMT, 32, 2, false>(p, st);
+        case 32: return quantise ? launch<FMT, 32, 2, true>(p, st) : launch<FMT, 32, 2, false>(p, st);
         case 64: return launch<FMT, 64, 2, false>(p, st);
         case 128: {
             const int* clusters = nullptr;

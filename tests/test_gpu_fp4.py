@@ -401,7 +401,8 @@ def test_forward_between_keeps_what_was_saved():
 @pytest.mark.parametrize("split,T,din,dout,t", [
     ("column", 1, 4096, 1056, 1), ("column", 7, 288, 416, 1), ("row", 1, 256, 256, 2), ("row", 16, 1088, 416, 2),
     ("row", 9, 4096, 1024, 8), ("column", 16, 32, 32, 1), ("column", 13, 9248, 2048, 2),
-    ("row", 17, 1024, 416, 2), ("row", 40, 1088, 416, 2)])
+    ("row", 17, 1024, 416, 2), ("row", 40, 1088, 416, 2), ("column", 64, 288, 800, 1),
+    ("column", 33, 4096, 1056, 1), ("row", 48, 4096, 1024, 8), ("row", 65, 4096, 1024, 8)])
 @pytest.mark.parametrize("calibrated", [False, True])
 def test_forward_alone(split, T, din, dout, t, fmt, calibrated):
     """Without keeping X, where few tokens are quantised on the way; the same result as with."""
