@@ -160,7 +160,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     ptx::cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    ptx::griddep_wait();
+    // (B may be there before the grids ahead have ended)
+    if (warp != 2 || !p.early) ptx::griddep_wait();
 
     const int kblocks = (p.K + F4_BK - 1) / F4_BK;
     const int nk = kblocks * p.ksegs;

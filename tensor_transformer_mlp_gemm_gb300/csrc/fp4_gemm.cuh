@@ -64,7 +64,7 @@ constexpr int FP4_QUANT_ROWS = 32;
 cudaError_t launch_fp4_small(const Fp4GemmParams& p, int fmt, int rows, bool quantise, cudaStream_t st);
 // Those rows for a product of this shape on the current device; 0: it has rows and
 // columns enough for the pairs.
-cudaError_t fp4_small_rows(int M, int N, int groups, int fmt, int& rows);
+cudaError_t fp4_small_rows(int M, int N, int K, int groups, int ksegs, int fmt, int& rows);
 // Whether few rows are quantised faster by the product itself than by a launch ahead of it.
 cudaError_t fp4_small_quantises(int M, int N, int K, int groups, int ksegs, bool& quantises);
 

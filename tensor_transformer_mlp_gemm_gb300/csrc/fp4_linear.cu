@@ -208,7 +208,7 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int format, in
     Fp4GemmParams p;
     std::memset(&p, 0, sizeof(p));
     int few = 0;  // rows of a tile of the few-rows kernel
-    if (!d.f32) TPMLP_CUDA(fp4_small_rows(d.M, d.N, d.groups, format, few));
+    if (!d.f32) TPMLP_CUDA(fp4_small_rows(d.M, d.N, d.K, d.groups, d.ksegs, format, few));
     if ((!d.x && !encode_operand(p.a_map, p.as_map, d.a, d.a.k > 0 ? static_cast<int>(d.a.k) : d.K, d.M,
                                few ? few : 128, format, few ? 0 : 1, &p.a_z)) ||
         !encode_operand(p.b_map, p.bs_map, d.b, d.K, d.N, 128, format, few ? 0 : 2, &p.b_z))

@@ -317,10 +317,80 @@ cudaError_t launch(const Fp4QuantParams& p, cudaStream_t st) {
                               static_cast<unsigned>(ct), static_cast<unsigned>(tiles));
 }
 
+// ---- few rows, by rows alone -------------------------------------------------------
+// A thread takes 32 columns of a row, straight from and to global memory.  For up to FEW values:
+// the product waits for this launch, and without shared memory in use its CTAs find room beside
+// these (whole calls with this and with the tiles: 48 tokens, 12288 -> 12288 features in eight
+// row shards 20.7 us, 24.3; 256 x 4096 tokens 11.0, 12.5; but 777 x 2080 19.0, 17.1).
+
+constexpr long long FEW = 1 << 20;
+constexpr int RT = 128;
+
+template <int FMT>
+__global__ void __launch_bounds__(RT)
+    fp4_quant_few_kernel(const __grid_constant__ Fp4QuantParams p, int row_tiles, int runs) {
+    constexpr int PER = FMT == FP4_NV ? 2 : 1;  // groups of 32
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const long long i = static_cast<long long>(blockIdx.x) * RT + threadIdx.x;
+    const long long row = i / runs;
+    const int run = static_cast<int>(i - row * runs), part = blockIdx.y;
+    if (row >= row_tiles * 128LL) return;
+    float inv_g = 0.0f;
+    if constexpr (FMT == FP4_NV) inv_g = inverse_of(p.scale);
+    const bool in = row < p.rows && run * 32LL < p.cols;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.src[part]) +
+                                                      (in ? row * p.cols + run * 32LL : 0));
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = in ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+    uint8_t* scales = p.s_rows[part] + (row >> 7) * ((p.rows_k + 255) / 256) * fp4_scale_step(FMT);
+    uint32_t o[4];
+#pragma unroll
+    for (int h = 0; h < PER; ++h) {
+        uint32_t m = larger(largest2(v[h * 2]), largest2(v[h * 2 + 1]));
+        if constexpr (PER == 1) m = larger(m, larger(largest2(v[2]), largest2(v[3])));
+        const Scale4 sc = scale_of<FMT>(fold(m), inv_g);
+        const int group = run * PER + h;
+        scales[(group >> 2) * 512LL + scale_at(row & 127, group & 3)] = static_cast<uint8_t>(sc.byte);
+#pragma unroll
+        for (int j = h * (4 / PER); j < (h + 1) * (4 / PER); ++j) {
+            float2 f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t w = word(v[j], e);
+                f[e] = scaled<FMT>(make_float2(lo_f(w), hi_f(w)), sc.inv);
+            }
+            o[j] = cvt8(f[0], f[1], f[2], f[3]);
+            if (!(sc.inv > 0.0f)) o[j] = 0;
+        }
+    }
+    if (in)
+        *reinterpret_cast<uint4*>(p.q_rows[part] + row * fp4_ld(p.rows_k) + run * 16LL) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int FMT>
+cudaError_t launch_few(const Fp4QuantParams& p, cudaStream_t st) {
+    const long long rt = (p.rows + 127) / 128, runs = (p.cols + 255) / 256 * 8;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rt * runs), static_cast<unsigned>(p.parts), 1);  // 128 rows each
+    cfg.blockDim = dim3(RT, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fp4_quant_few_kernel<FMT>, p, static_cast<int>(rt), static_cast<int>(runs));
+}
+
 template <int FMT>
 cudaError_t launch_mode(const Fp4QuantParams& p, int mode, cudaStream_t st) {
     switch (mode) {
-        case FP4_Q_ROWS: return launch<FMT, FP4_Q_ROWS>(p, st);
+        case FP4_Q_ROWS:
+            return p.rows * p.cols * p.parts <= FEW && (!p.gather || p.parts == 1) ? launch_few<FMT>(p, st)
+                                                                     : launch<FMT, FP4_Q_ROWS>(p, st);
         case FP4_Q_COLS: return launch<FMT, FP4_Q_COLS>(p, st);
         case FP4_Q_ROWS | FP4_Q_COLS: return launch<FMT, FP4_Q_ROWS | FP4_Q_COLS>(p, st);
         case FP4_Q_ROWS | FP4_Q_COLS | FP4_Q_SUMS:

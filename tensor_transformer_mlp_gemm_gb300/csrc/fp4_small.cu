@@ -492,15 +492,23 @@ cudaError_t launch(const Fp4GemmParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t fp4_small_rows(int M, int N, int groups, int fmt, int& rows) {
+cudaError_t fp4_small_rows(int M, int N, int K, int groups, int ksegs, int fmt, int& rows) {
     rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     if (M <= 128) return cudaSuccess;
     const int* clusters = nullptr;
     const cudaError_t e = fmt == FP4_NV ? resident<FP4_NV, 256, 1, false>(clusters) : resident<FP4_MX, 256, 1, false>(clusters);
     if (e != cudaSuccess) return e;
-    // Pairs on 256 x 256 tiles are faster unless so few tiles that K can be cut in four here.
+    // Pairs on 256 x 256 tiles are faster unless so few tiles that K can be cut in four here,
+    // and above 256 tokens unless K is long too (us here, on pairs: 333 tokens, 1056 -> 2080
+    // features 11.8, 9.9; 4096 -> 1024 11.5, 12.6; 512 tokens, 8192 -> 2048 15.5, 18.3).
     const long long tiles = static_cast<long long>((N + 127) / 128) * groups;
-    rows = tiles * ((M + 255LL) / 256) <= clusters[4] ? 256 : 0;
+    const long long nk = static_cast<long long>((K + F4_BK - 1) / F4_BK) * ksegs;
+    rows = tiles * ((M + 255LL) / 256) <= clusters[4] && (M <= 256 || nk >= 16) ? 256 : 0;
+    // Up to 256 tokens tiles of 128 read weights twice, but from L2, and have half the sums to
+    // hand on: faster where K is cut in as many or is short (256 tokens, by 128 and by 256:
+    // 1024 -> 1024 8.0, 10.1; 8192 -> 2048 12.6, 13.9; 4096 -> 4096 12.0, 12.9; but 12288 -> 4096
+    // 19.4, 17.9).
+    if (rows == 256 && M <= 256 && (2 * tiles <= clusters[4] || nk <= 16)) rows = 128;
     return cudaSuccess;
 }
 
@@ -530,7 +538,8 @@ static cudaError_t launch_rows(const Fp4GemmParams& p, int rows, bool quantise, 
             const int* clusters = nullptr;
             const cudaError_t e = resident<FMT, 128, 1, false>(clusters);
             if (e != cudaSuccess) return e;
-            const long long tiles = static_cast<long long>((p.N + 127) / 128) * p.groups;
+            const long long tiles =
+                static_cast<long long>((p.N + 127) / 128) * p.groups * ((p.M + 127LL) / 128);
             return tiles <= clusters[2] ? launch<FMT, 128, 1, false>(p, st) : launch<FMT, 128, 2, false>(p, st);
         }
         case 256: return launch<FMT, 256, 1, false>(p, st);

@@ -446,3 +446,17 @@ def test_segments_of_whole_stages(split, T, din, dout, t, fmt):
     _sync()
     _check_forward(lay, X)
     _check_backward(lay, X, dY)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,C", [(1024, 1024), (1025, 1024), (511, 2080), (130, 8224), (1, 32), (300, 288)])
+def test_quantize_rows_alone(T, C, fmt):
+    """By rows alone, on both sides of the number of values that takes another kernel; what
+    fills up is written."""
+    from tensor_transformer_mlp_gemm_gb300 import fp4
+    x = _values(T, C, _gen(T + C))
+    got = fp4.quantize_tokens(x, fmt).rows
+    both = fp4.quantize_tokens(x, fmt, cols=True).rows
+    _sync()
+    _check(got, x, fmt, 1, None if fmt == "mxfp4" else plain.tensor_scale([x]))
+    assert torch.equal(got.q, both.q) and torch.equal(got.s, both.s)
