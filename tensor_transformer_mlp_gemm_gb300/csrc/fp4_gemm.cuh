@@ -38,7 +38,7 @@ struct Fp4GemmParams {
     const void* x[F4_MAX_MAPS];          // few rows only: A in bf16 [M, K], quantised on the way
     const float* ga;                     // the tensors' scales (nv)
     const float* gb;
-    int early;                           // B is there before the grids ahead have ended
+    int early;                           // B may be read before the grids ahead have ended
     int M, N, K;                         // per group; K per segment
     int groups, ksegs;
     int a_part, b_part;

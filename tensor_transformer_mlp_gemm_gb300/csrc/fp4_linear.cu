@@ -181,6 +181,10 @@ struct Product {
     int nout;          // outputs: one per group, or one per token chunk
     int chunk_rows;    // > 0: rows per token chunk
     const void* const* x;  // A in bf16, for the few-rows kernel to quantise, or null
+    // B was there before this call: it may be read before the grids ahead have ended, which
+    // wait for what came before the call and only then let others start.  (Not where they write
+    // B, as of a weight gradient, nor without one ahead.)
+    bool early;
 };
 
 // The maps of an operand's values, and (box_tiles > 0) of its scales, that many times 128 rows a
@@ -219,8 +223,7 @@ tpmlp_status run_product(const DeviceInfo* dev, const Product& d, int format, in
         else
             p.sa[i] = static_cast<const uint8_t*>(d.a.s[i]);
     }
-    // A was quantised by this call, after what came before had ended: B may be read already
-    p.early = !d.x;
+    p.early = d.early;
     for (int i = 0; i < d.b.n; ++i) p.sb[i] = static_cast<const uint8_t*>(d.b.s[i]);
     for (int i = 0; i < d.nout; ++i) p.out[i] = d.out[i];
     p.ga = static_cast<const float*>(d.a.scale);
@@ -340,6 +343,7 @@ tpmlp_status forward(Split k, const tpmlp_linear_dims* dims, int format, const v
     bool quantises = false;
     if (!save) TPMLP_CUDA(fp4_small_quantises(p.M, p.N, p.K, p.groups, p.ksegs, quantises));
     p.x = quantises ? X : nullptr;
+    p.early = !p.x;
     TPMLP_TRY(quantize(dev, X, nx, col, col ? s.Tc : s.T, K, format, x_scale, x_calibrated != 0,
                        p.x ? nullptr : &rows, save ? &cols : nullptr, nullptr, 0, st));
     p.a = Operand{reinterpret_cast<const void* const*>(rows.q), reinterpret_cast<const void* const*>(rows.s),
@@ -409,6 +413,7 @@ tpmlp_status backward(Split k, const tpmlp_linear_dims* dims, int format, const 
         p.nout = ndx;
         p.chunk_rows = col ? s.Tc : 0;
         p.x = nullptr;
+        p.early = true;
         TPMLP_TRY(run_product(dev, p, format, TPMLP_KERNEL_LINEAR_DGRAD, st));
     }
     {
@@ -428,6 +433,7 @@ tpmlp_status backward(Split k, const tpmlp_linear_dims* dims, int format, const 
         p.nout = s.t;
         p.chunk_rows = 0;
         p.x = nullptr;
+        p.early = false;
         TPMLP_TRY(run_product(dev, p, format, TPMLP_KERNEL_LINEAR_WGRAD, st));
     }
     return TPMLP_OK;
@@ -524,18 +530,18 @@ TPMLP_API tpmlp_status tpmlp_fp4_quantize(const tpmlp_fp4_quant* d, const void* 
 
 TPMLP_API tpmlp_status tpmlp_fp4_dequantize(int64_t rows, int64_t k, int format, const void* q,
                                             const void* s, const void* scale, void* out, void* stream) {
-    if (rows < 0 || k <= 0 || !format_ok(format)) return TPMLP_ERR_INVALID_ARG;
+    if (rows < 0 || k < 0 || !format_ok(format)) return TPMLP_ERR_INVALID_ARG;
     const int64_t lim = (int64_t(1) << 31) - 1;
     if (rows > lim || k > lim) return TPMLP_ERR_UNSUPPORTED;
     TPMLP_TRY(check_tensor_scale(scale, format));
-    if (rows > 0) {
+    if (rows > 0 && k > 0) {
         TPMLP_TRY(check_ptr(q));
         TPMLP_TRY(check_ptr(s));
         TPMLP_TRY(check_ptr(out));
     }
     DeviceInfo* dev = nullptr;
     TPMLP_TRY(device_info(&dev));
-    if (rows == 0) return TPMLP_OK;
+    if (rows == 0 || k == 0) return TPMLP_OK;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     TPMLP_CUDA(timed(TPMLP_KERNEL_SP_COPY, 1, st, [&] {
         return launch_fp4_dequant(rows, k, format, q, s, static_cast<const float*>(scale), out, st);

@@ -109,8 +109,8 @@ class _Space:
         self.q_ptrs, self.s_ptrs = _strided(base, self.q, n), _strided(base + self.at, self.s, n)
 
     def matrix(self, i: int, scale) -> Fp4Matrix:
-        R = self.shape[0]
-        q = self.buf[i * self.q:(i + 1) * self.q].view(R, self.q // max(R, 1))
+        R, K = self.shape
+        q = self.buf[i * self.q:(i + 1) * self.q].view(R, -(-K // 32) * 16)
         s = self.buf[self.at + i * self.s:self.at + (i + 1) * self.s]
         m = Fp4Matrix.__new__(Fp4Matrix)
         m.q, m.s, m.scale, m.shape, m.fmt = q, s, scale, self.shape, self.fmt
