@@ -80,7 +80,9 @@ __global__ void __launch_bounds__(QT, Q_PER_SM)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t tile0 = ptx::smem_u32(s_tiles), bar0 = ptx::smem_u32(s_bar);
 
-    // Tiles part by part, row by row, each CTA every gridDim.x-th; stepped, not divided out.
+    // Tiles part by part, row by row from the last on (which whoever wrote or read the matrix left
+    // in L2: a weight of 12288 x 4608 behind its tensor's scale 2 us), each CTA every
+    // gridDim.x-th; stepped, not divided out.
     struct Tile {
         unsigned part, rt, ct;
     };
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(QT, Q_PER_SM)
     auto load = [&](const Tile& x, int b) {
         if (blockIdx.x == gridDim.x - 1 && loads == p.stall) return;
         ++loads;
-        const long long r0 = static_cast<long long>(x.rt) * TILE, c0 = static_cast<long long>(x.ct) * TILE;
+        const long long r0 = static_cast<long long>(row_tiles - 1 - x.rt) * TILE, c0 = static_cast<long long>(x.ct) * TILE;
         const int rows = total - r0 < TILE ? static_cast<int>(max(0LL, total - r0)) : TILE;
         const int bytes = 2 * (p.cols - c0 < TILE ? static_cast<int>(max(0LL, p.cols - c0)) : TILE);
         if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bar0 + 8 * b, rows * bytes);
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(QT, Q_PER_SM)
                 long long row = r0 + r;
                 if (p.gather && p.parts > 1) {  // (chunks of whole tiles)
                     const unsigned chunk = static_cast<unsigned>(p.rows / TILE);
-                    from = x.rt / chunk;
+                    from = (row_tiles - 1 - x.rt) / chunk;
                     row -= static_cast<long long>(from) * p.rows;
                 }
                 bulk_load(tile0 + b * Q_STAGE + row_at(r),
@@ -157,7 +159,8 @@ __global__ void __launch_bounds__(QT, Q_PER_SM)
         const Tile next = next_of(x);
         if (t + gridDim.x < tiles) load(next, b ^ 1);
         const bool ok = f8::wait(bar0 + 8 * b, phase, &s_abort, p.timeout_ns, p.err, ERR_EPILOGUE);
-        const long long r0 = static_cast<long long>(x.rt) * TILE, c0 = static_cast<long long>(x.ct) * TILE;
+        const unsigned rt = row_tiles - 1 - x.rt;
+        const long long r0 = static_cast<long long>(rt) * TILE, c0 = static_cast<long long>(x.ct) * TILE;
         const uint8_t* tile = s_tiles + b * Q_STAGE;
         if (ROWS && ok) {
             const int run = lane >> 3;  // a thread takes 32 columns of two rows
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(QT, Q_PER_SM)
                     s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
                 }
                 if (g == 0 && cc < p.cols && r0 < total)
-                    *reinterpret_cast<float2*>(p.sums[x.part] + x.rt * p.sums_ld + cc) = s;
+                    *reinterpret_cast<float2*>(p.sums[x.part] + rt * p.sums_ld + cc) = s;
             }
         }
         // the buffer has been read and the scales are there; who gave up takes the others along
@@ -265,11 +268,11 @@ __global__ void __launch_bounds__(QT, Q_PER_SM)
         if (threadIdx.x < SB / 16) {
             const int i = threadIdx.x * 16;
             if (ROWS && r0 < total) {
-                uint8_t* s = p.s_rows[x.part] + x.rt * ((p.rows_k + 255) / 256) * (2 * SB) + x.ct * SB + i;
+                uint8_t* s = p.s_rows[x.part] + rt * ((p.rows_k + 255) / 256) * (2 * SB) + x.ct * SB + i;
                 *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(&s_rows[b][i]);
             }
             if (COLS && c0 < p.cols) {
-                uint8_t* s = p.s_cols[x.part] + x.ct * ((total + 255) / 256) * (2 * SB) + x.rt * SB + i;
+                uint8_t* s = p.s_cols[x.part] + x.ct * ((total + 255) / 256) * (2 * SB) + rt * SB + i;
                 *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(&s_cols[b][i]);
             }
         }
@@ -403,8 +406,16 @@ cudaError_t launch_mode(const Fp4QuantParams& p, int mode, cudaStream_t st) {
 
 constexpr int MT = 512, M_PER_SM = 3, M_UNROLL = 4;
 
+// *scale = 0, by a kernel: behind a memset the next kernel would start only when it has ended.
+__global__ void fp4_zero_kernel(unsigned* scale) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    *scale = 0;
+}
+
 // g grows with the largest magnitude, and positive floats compare as integers: each CTA
-// raises *scale, which starts at 0, to that of its own values.
+// raises *scale, which starts at 0, to that of its own values.  What came before has ended when
+// this starts (fp4_zero_kernel lets it), so only *scale is waited for.
 __global__ void __launch_bounds__(MT, M_PER_SM)
     fp4_tensor_scale_kernel(const __grid_constant__ Fp4QuantParams p, long long vecs, unsigned* scale) {
     __shared__ uint32_t s_max[MT / 32];
@@ -412,7 +423,6 @@ __global__ void __launch_bounds__(MT, M_PER_SM)
     const long long step = static_cast<long long>(gridDim.x) * MT;
     uint32_t m = 0;
     ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
     for (long long i = static_cast<long long>(blockIdx.x) * MT + threadIdx.x; i < vecs; i += M_UNROLL * step) {
         uint4 v[M_UNROLL];
 #pragma unroll
@@ -441,6 +451,7 @@ __global__ void __launch_bounds__(MT, M_PER_SM)
         // 6 * 448 = 1.3125 * 2^11
         const int e = static_cast<int>(m >> 7), f = static_cast<int>(m & 0x7Fu);
         const int k = max(e - 127 - 11 + (f > 40 ? 1 : 0), -110);
+        ptx::griddep_wait();
         atomicMax(scale, static_cast<unsigned>(k + 127) << 23);
     }
 }
@@ -524,8 +535,7 @@ cudaError_t launch_fp4_quant(const Fp4QuantParams& params, int fmt, int mode, cu
 }
 
 cudaError_t launch_fp4_tensor_scale(const Fp4QuantParams& p, float* scale, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(scale, 0, sizeof(float), st);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     const long long vecs = p.rows * p.cols / 8;
     int sms = 0, dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -533,9 +543,18 @@ cudaError_t launch_fp4_tensor_scale(const Fp4QuantParams& p, float* scale, cudaS
     const long long most = max(1LL, static_cast<long long>(sms) * M_PER_SM / p.parts);
     const long long ctas = min((vecs + MT * M_UNROLL - 1) / (MT * M_UNROLL), most);
     cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, 1, 1);
+    cfg.blockDim = dim3(1, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, fp4_zero_kernel, reinterpret_cast<unsigned*>(scale));
+    if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(max(ctas, 1LL)), static_cast<unsigned>(p.parts), 1);
     cfg.blockDim = dim3(MT, 1, 1);
-    cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, fp4_tensor_scale_kernel, p, vecs, reinterpret_cast<unsigned*>(scale));
 }
 
