@@ -11,6 +11,7 @@ bit; groups along the axis that a product sums over share a scale (include/tpmlp
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -33,6 +34,15 @@ def _check_scale(scale, fmt: str, device, what: str) -> None:
         _check_like(scale, (1,), torch.float32, device, what)
 
 
+def _ld(k: int) -> int:
+    """Bytes of a row of k values."""
+    return -(-k // 32) * 16
+
+
+def _scale_bytes(rows: int, k: int, code: int) -> int:
+    return -(-rows // 128) * -(-k // 256) * (2048 if code else 1024)
+
+
 class Fp4Matrix:
     """A matrix [rows, k] in 4 bits, summed over k: ``q`` uint8 [rows, ceil(k/32) * 16], two
     values a byte; ``s`` uint8, the scales as the tensor cores take them; ``scale`` fp32 [1]
@@ -42,28 +52,56 @@ class Fp4Matrix:
                  fmt: str):
         code = _format(fmt)
         rows, k = shape
-        _check_like(q, (rows, -(-k // 32) * 16), torch.uint8, q.device, "q")
-        _check_like(s, (binding.tpmlp_fp4_scale_bytes(rows, k, code),), torch.uint8, q.device, "s")
+        if not q.is_cuda:
+            raise ValueError(f"q must be a CUDA tensor, got one on {q.device}")
+        _check_like(q, (rows, _ld(k)), torch.uint8, q.device, "q")
+        _check_like(s, (_scale_bytes(rows, k, code),), torch.uint8, q.device, "s")
         _check_scale(scale, fmt, q.device, "scale")
         if fmt == "nvfp4" and scale is None:
             raise ValueError("nvfp4 needs the tensor's scale")
-        self.q, self.s, self.scale, self.shape, self.fmt = q, s, scale, (rows, k), fmt
+        self._q, self._s, self._scale = q, s, scale
+        self._ptrs = (q.data_ptr(), s.data_ptr(), None if scale is None else scale.data_ptr())
+        self.shape, self.fmt, self.device = (rows, k), fmt, q.device
+
+    @classmethod
+    def _of(cls, space: "_Space", i: int, scale) -> "Fp4Matrix":
+        """Matrix i of a space, whose tensors are made when asked for."""
+        m = cls.__new__(cls)
+        m._q = m._s = None
+        m._scale, m._space, m._i = scale, space, i
+        m._ptrs = (space.q_ptrs[i], space.s_ptrs[i], space.scale_ptr)
+        m.shape, m.fmt, m.device = space.shape, space.fmt, space.device
+        return m
 
     @property
-    def device(self):
-        return self.q.device
+    def q(self) -> torch.Tensor:
+        if self._q is None:
+            self._q = self._space.bytes(self._ptrs[0], self._space.q).view(self.shape[0], _ld(self.shape[1]))
+        return self._q
+
+    @property
+    def s(self) -> torch.Tensor:
+        if self._s is None:
+            self._s = self._space.bytes(self._ptrs[1], self._space.s)
+        return self._s
+
+    @property
+    def scale(self) -> torch.Tensor | None:
+        if self._scale is None and self.fmt == "nvfp4":
+            self._scale = self._space.bytes(self._ptrs[2], 4).view(torch.float32)
+        return self._scale
 
     def values(self, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The values that it stands for, bf16 [rows, k] (exact)."""
-        dev = self.q.device
+        dev = self.device
         if out is None:
             with binding.allocate_on(dev, stream):
                 out = torch.empty(self.shape, dtype=torch.bfloat16, device=dev)
         else:
             _check_like(out, self.shape, torch.bfloat16, dev, "out")
         with binding.on_device(dev):
-            binding.tpmlp_fp4_dequantize(*self.shape, binding.FP4_FORMATS[self.fmt], self.q, self.s,
-                                         self.scale, out, binding.stream_on(dev, stream))
+            _dequantize(*self.shape, binding.FP4_FORMATS[self.fmt], *self._ptrs, out.data_ptr(),
+                        binding.stream_on(dev, stream))
         return out
 
 
@@ -84,37 +122,43 @@ class Fp4Weights:
         both = self.forward + (self.backward or [])
         if not both:
             raise ValueError("no shards")
-        self.fmt, self.scale = both[0].fmt, both[0].scale
+        first = both[0]
+        self.fmt = first.fmt
         if self.backward is not None and len(self.backward) != len(self.forward):
             raise ValueError("as many shards are needed forward and backward")
         for m in both:
             # one scale for all: the shards of a row-parallel layer are summed before it is applied
-            if m.fmt != self.fmt or m.device != both[0].device or (
-                    m.scale is not None and m.scale.data_ptr() != self.scale.data_ptr()):
+            if m.fmt != first.fmt or m.device != first.device or m._ptrs[2] != first._ptrs[2]:
                 raise ValueError("the shards of a weight have one format, device and scale")
+
+    scale = property(lambda self: self.forward[0].scale)
 
 
 class _Space:
-    """Room for n matrices [R, K] in 4 bits and their scales, in one buffer."""
+    """Room for n matrices [R, K] in 4 bits and their scales in a buffer, from byte `at` on."""
 
-    def __init__(self, n: int, R: int, K: int, fmt: str, device, stream=None):
-        code = binding.FP4_FORMATS[fmt]
+    def __init__(self, n: int, R: int, K: int, fmt: str):
         self.n, self.shape, self.fmt = n, (R, K), fmt
-        self.q = binding.tpmlp_fp4_packed_bytes(R, K)
-        self.s = binding.tpmlp_fp4_scale_bytes(R, K, code)
-        self.at = _up256(n * self.q)
-        with binding.allocate_on(device, stream):
-            self.buf = torch.empty(max(self.at + n * self.s, 256), dtype=torch.uint8, device=device)
-        base = self.buf.data_ptr()
-        self.q_ptrs, self.s_ptrs = _strided(base, self.q, n), _strided(base + self.at, self.s, n)
+        self.q, self.s = R * _ld(K), _scale_bytes(R, K, binding.FP4_FORMATS[fmt])
+        self.size = _up256(n * self.q) + _up256(n * self.s)
+        self.scale_ptr = None
 
-    def matrix(self, i: int, scale) -> Fp4Matrix:
-        R, K = self.shape
-        q = self.buf[i * self.q:(i + 1) * self.q].view(R, -(-K // 32) * 16)
-        s = self.buf[self.at + i * self.s:self.at + (i + 1) * self.s]
-        m = Fp4Matrix.__new__(Fp4Matrix)
-        m.q, m.s, m.scale, m.shape, m.fmt = q, s, scale, self.shape, self.fmt
-        return m
+    def place(self, buf: torch.Tensor, at: int) -> "_Space":
+        self.buf, self.device, self.start = buf, buf.device, buf.data_ptr()
+        base = self.start + at
+        self.q_ptrs = _strided(base, self.q, self.n)
+        self.s_ptrs = _strided(base + _up256(self.n * self.q), self.s, self.n)
+        return self
+
+    def bytes(self, ptr: int, size: int) -> torch.Tensor:
+        return self.buf[ptr - self.start:ptr - self.start + size]
+
+
+_dequantize = binding.prepared("tpmlp_fp4_dequantize")
+_quantize_call = binding.prepared("tpmlp_fp4_quantize")
+_tensor_scale_call = binding.prepared("tpmlp_fp4_tensor_scale")
+# (R, C, parts, gather, format) -> a call's description
+_quant = functools.lru_cache(maxsize=256)(lambda *a: ctypes.byref(binding.make_fp4_quant(*a)))
 
 
 def tensor_scale(parts, stream=None) -> torch.Tensor:
@@ -125,29 +169,44 @@ def tensor_scale(parts, stream=None) -> torch.Tensor:
     with binding.allocate_on(dev, stream):
         scale = torch.empty(1, dtype=torch.float32, device=dev)
     with binding.on_device(dev):
-        binding.tpmlp_fp4_tensor_scale(binding.make_fp4_quant(*parts[0].shape, len(parts), False, 1),
-                                       _pointers(parts), scale, binding.stream_on(dev, stream))
+        _tensor_scale_call(_quant(*parts[0].shape, len(parts), False, 1), _pointers(parts), scale.data_ptr(),
+                           binding.stream_on(dev, stream))
     return scale
 
 
 def _quantize(parts, fmt: str, gather: bool, rows: bool, cols: bool, scale, stream):
-    """(space by rows or None, space by columns or None, the scale used)."""
+    """(matrices by rows or None, matrices by columns or None), in one buffer with the scale
+    where that is computed here (an allocation costs more host time than a launch)."""
     code, dev, n = _format(fmt), parts[0].device, len(parts)
     if not (rows or cols):
         raise ValueError("choose rows, cols or both")
     _check_scale(scale, fmt, dev, "scale")
-    if fmt == "nvfp4" and scale is None:
-        scale = tensor_scale(parts, stream)
     R, C = parts[0].shape
     outs, T = (1, R * n) if gather else (n, R)
-    by_rows = _Space(outs, T, C, fmt, dev, stream) if rows else None
-    by_cols = _Space(outs, C, T, fmt, dev, stream) if cols else None
+    spaces = [_Space(outs, *shape, fmt) if wanted else None
+              for wanted, shape in ((rows, (T, C)), (cols, (C, T)))]
+    at = 256 if fmt == "nvfp4" else 0
+    with binding.allocate_on(dev, stream):
+        buf = torch.empty(max(at + sum(x.size for x in spaces if x), 256), dtype=torch.uint8, device=dev)
+    for x in spaces:
+        if x is not None:
+            x.place(buf, at)
+            at += x.size
+    scale_ptr = None
+    if fmt == "nvfp4":
+        scale_ptr = buf.data_ptr() if scale is None else scale.data_ptr()
+    ptrs = _pointers(parts)
+    r, c = spaces
     with binding.on_device(dev):
-        binding.tpmlp_fp4_quantize(
-            binding.make_fp4_quant(R, C, n, gather, code), _pointers(parts), scale,
-            by_rows and by_rows.q_ptrs, by_rows and by_rows.s_ptrs, by_cols and by_cols.q_ptrs,
-            by_cols and by_cols.s_ptrs, binding.stream_on(dev, stream))
-    return by_rows, by_cols, scale
+        raw = binding.stream_on(dev, stream)
+        if fmt == "nvfp4" and scale is None:
+            _tensor_scale_call(_quant(R, C, n, False, 1), ptrs, scale_ptr, raw)
+        _quantize_call(_quant(R, C, n, gather, code), ptrs, scale_ptr, r and r.q_ptrs, r and r.s_ptrs,
+                       c and c.q_ptrs, c and c.s_ptrs, raw)
+    for x in spaces:
+        if x is not None:
+            x.scale_ptr = scale_ptr
+    return tuple(x and [Fp4Matrix._of(x, i, scale) for i in range(outs)] for x in spaces)
 
 
 def quantize_tokens(X, fmt: str = "mxfp4", rows: bool = True, cols: bool = False,
@@ -159,8 +218,8 @@ def quantize_tokens(X, fmt: str = "mxfp4", rows: bool = True, cols: bool = False
     _check_parts(chunks, "token chunk")
     if len(chunks) > 1 and chunks[0].shape[0] % 128:
         raise ValueError("token chunks must be a multiple of 128 tokens")
-    r, c, scale = _quantize(chunks, fmt, True, rows, cols, scale, stream)
-    return Fp4Tokens(r and r.matrix(0, scale), c and c.matrix(0, scale))
+    r, c = _quantize(chunks, fmt, True, rows, cols, scale, stream)
+    return Fp4Tokens(r and r[0], c and c[0])
 
 
 def quantize_weight(W, fmt: str = "mxfp4", backward: bool = False, scale: torch.Tensor | None = None,
@@ -169,9 +228,8 @@ def quantize_weight(W, fmt: str = "mxfp4", backward: bool = False, scale: torch.
     the form for the backward pass too, in the same read."""
     shards = [W] if isinstance(W, torch.Tensor) else list(W)
     _check_parts(shards, "weight shard")
-    r, c, scale = _quantize(shards, fmt, False, backward, True, scale, stream)
-    return Fp4Weights([c.matrix(i, scale) for i in range(len(shards))],
-                      [r.matrix(i, scale) for i in range(len(shards))] if backward else None)
+    r, c = _quantize(shards, fmt, False, backward, True, scale, stream)
+    return Fp4Weights(c, r)
 
 
 class DeviceFp4Linear:
@@ -227,10 +285,11 @@ class DeviceFp4Linear:
         self._call_back = binding.prepared(f"tpmlp_fp4_{split}_linear_backward")
         self._dims = ctypes.byref(self.dims)
         self._b = b.data_ptr()
-        self._w_scale = None if weights.scale is None else weights.scale.data_ptr()
-        self._forward = (_pointers([m.q for m in weights.forward]), _pointers([m.s for m in weights.forward]))
-        self._backward = weights.backward and (_pointers([m.q for m in weights.backward]),
-                                               _pointers([m.s for m in weights.backward]))
+        self._w_scale = weights.forward[0]._ptrs[2]
+        def pointers(ms):
+            return tuple(_ARRAYS[t](*[m._ptrs[k] for m in ms]) for k in (0, 1))
+        self._forward = pointers(weights.forward)
+        self._backward = weights.backward and pointers(weights.backward)
         # where a forward call without a calibration writes the scale: one that keeps nothing, and
         # one that keeps X for the backward pass
         self._scales = torch.empty(2, 1, dtype=torch.float32, device=dev) if self.fmt == "nvfp4" else None
@@ -297,7 +356,10 @@ class DeviceFp4Linear:
         """Room for X by columns, kept by the layer from its first saving call on."""
         if self._saved is None:
             n, C = (1, self.w.in_features) if self.column else (self.w.t, self.w.shard)
-            self._saved = _Space(n, C, self.w.tokens, self.fmt, self.device, stream)
+            space = _Space(n, C, self.w.tokens, self.fmt)
+            with binding.allocate_on(self.device, stream):
+                buf = torch.empty(max(space.size, 256), dtype=torch.uint8, device=self.device)
+            self._saved = space.place(buf, 0)
         return self._saved
 
     def _list(self, xs, spec, what):
