@@ -494,15 +494,23 @@ cudaError_t launch(const Fp4GemmParams& p, cudaStream_t st) {
 
 cudaError_t fp4_small_rows(int M, int N, int K, int groups, int ksegs, int fmt, int& rows) {
     rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    if (M <= 128) return cudaSuccess;
-    const int* clusters = nullptr;
+    if (M <= 64) return cudaSuccess;
+    const int* clusters = nullptr;  // (of one CTA on an SM)
     const cudaError_t e = fmt == FP4_NV ? resident<FP4_NV, 256, 1, false>(clusters) : resident<FP4_MX, 256, 1, false>(clusters);
     if (e != cudaSuccess) return e;
-    // Pairs on 256 x 256 tiles are faster unless so few tiles that K can be cut in four here,
-    // and above 256 tokens unless K is long too (us here, on pairs: 333 tokens, 1056 -> 2080
-    // features 11.8, 9.9; 4096 -> 1024 11.5, 12.6; 512 tokens, 8192 -> 2048 15.5, 18.3).
     const long long tiles = static_cast<long long>((N + 127) / 128) * groups;
     const long long nk = static_cast<long long>((K + F4_BK - 1) / F4_BK) * ksegs;
+    if (M <= 128) {
+        // Pairs on 256 x 256 tiles where K is short and cannot be cut in two, but the tiles are
+        // one for each pair (us here, on pairs: 128 tokens, 4096 -> 12288 features 15.0, 13.4;
+        // 6144 -> 12288 16.6, 16.1; but 2080 -> 8224 10.4, 11.5, 4096 -> 24576 20.7, 24.8,
+        // 12288 -> 36864 51.1, 53.2).
+        if (tiles > clusters[2] && tiles <= 2 * clusters[2] && nk <= 24) rows = 0;
+        return cudaSuccess;
+    }
+    // Pairs are faster unless so few tiles that K can be cut in four here, and above 256
+    // tokens unless K is long too (us here, on pairs: 333 tokens, 1056 -> 2080 features 11.8, 9.9;
+    // 4096 -> 1024 11.5, 12.6; 512 tokens, 8192 -> 2048 15.5, 18.3).
     rows = tiles * ((M + 255LL) / 256) <= clusters[4] && (M <= 256 || nk >= 16) ? 256 : 0;
     // Up to 256 tokens tiles of 128 read weights twice, but from L2, and have half the sums to
     // hand on: faster where K is cut in as many or is short (256 tokens, by 128 and by 256:
