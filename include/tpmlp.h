@@ -711,7 +711,8 @@ tpmlp_status tpmlp_set_wait_timeout_ns(uint64_t ns);
 tpmlp_status tpmlp_selftest_stalled_gemm(const void* a, const void* b, void* c,
                                          uint64_t timeout_ns, void* stream);
 
-/* The same for the products of the 8-bit and 4-bit linear layers and the norms around a block:
+/* The same for the products of the 8-bit and 4-bit linear layers, the quantisation to 4 bits in
+ * tiles and the norms around a block:
  * after this call, those that the calling thread launches stop loading in the last
  * CTA of each cluster after `copies` (>= 0) steps (K blocks, or rows), so that what
  * waits for the rest gives up at the limit

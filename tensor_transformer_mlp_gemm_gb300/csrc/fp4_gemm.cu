@@ -9,9 +9,15 @@
 //                stages: forward of 16384 x 4096 x 4096 in eight segments 101 us, now 90.)
 //   warp 1       owns the tensor memory; in the even CTA copies the pair's scales into it and
 //                issues the MMAs, four K slices of 64 for each stage
+//   warp 3       waits for the grid ahead where the product need not; adds up column sums
 //   warps 4..11  output: warp w reads lanes 32 (w % 4) .. of the accumulator and columns
 //                128 ((w - 4) / 4) .. into registers, frees the accumulator for the next
 //                tile's MMAs, and writes from there
+// What bounds it: the tensor cores, at 256 x 256 x 256 33.5 MFLOP for 64 KB of operands and 6 to
+// 12 KB of scales from L2.  Measured: 2048 tokens, 12288 -> 36864 features nv 260 us, 7.1 PFLOP/s;
+// 16384 x 4096 x 4096 mx 86 us, 6.4 PFLOP/s, where a tile has 16 stages: of these the scales'
+// copies take 3 (nv 6), and the accumulator's hand-over and the outputs beside the loads 10 each.
+//
 // Tensor memory: 256 columns of sums, then a slot of scales for each stage (24 columns of mx,
 // 48 of nv): a stage that is free has a slot that no MMA reads.
 //
@@ -160,8 +166,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     ptx::cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // (B may be there before the grids ahead have ended)
-    if (warp != 2 || !p.early) ptx::griddep_wait();
+    // (B may be there before the grids ahead have ended, or everything)
+    if (warp == 3 || !(p.apart || (p.early && warp == 2))) ptx::griddep_wait();
 
     const int kblocks = (p.K + F4_BK - 1) / F4_BK;
     const int nk = kblocks * p.ksegs;
@@ -188,7 +194,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             long long fills = 0;
             bool ok = true;
             for (int tile = cluster; ok && tile < p.total_tiles; tile += nclusters) {
-                if (tile + nclusters >= p.total_tiles) ptx::griddep_launch_dependents();
+                if (!p.apart && !of_b && tile + nclusters >= p.total_tiles) ptx::griddep_launch_dependents();
                 int g, m0, n0;
                 decode(p, tile, g, m0, n0);
                 const int row = (of_b ? n0 : m0) + rank * 128, srow = (of_b ? n0 : row) >> 7;
@@ -225,6 +231,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             }
             if (!ok)
                 store_cluster64(ptx::mapa_shared(stages_done + 8 * (F_COPIED + 2 * rank + of_b), 0), fills);
+        } else if (warp == 3) {
+            if (p.apart) ptx::griddep_launch_dependents();  // (the grid ahead has ended)
+            if (p.sums) f4::column_sums(p, blockIdx.x, gridDim.x, lane);
         } else if (warp == 1 && rank == 0) {
             // ---------------- MMA issuer ----------------
             // The whole warp walks the loop and one lane issues, so the descriptors

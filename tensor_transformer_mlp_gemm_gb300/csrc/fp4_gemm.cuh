@@ -47,6 +47,12 @@ struct Fp4GemmParams {
     int mtiles, ntiles, total_tiles, band;
     int chunk_rows;                      // > 0: output i holds rows [i * chunk_rows, ...), else output g
     const void* bias;                    // bf16 [groups * N] or null
+    const float* sums;                   // rows of partial column sums [sum_rows, sum_cols] that are
+    float* db;                           // added up into db on the way, or null
+    long long sum_rows;
+    int sum_cols;
+    int apart;                           // takes nothing from the grid ahead and runs beside it, but
+                                         // ends after it (pairs only)
     unsigned int* err;                   // the device error word and the limit of any one wait
     unsigned long long timeout_ns;
     int stall;                           // failure-detection self-test: the loader of a cluster's last

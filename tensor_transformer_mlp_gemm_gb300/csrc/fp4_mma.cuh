@@ -16,6 +16,7 @@
 
 #include "fp4_gemm.cuh"
 #include "fp8_mma.cuh"
+#include "two_sum.cuh"
 
 namespace tpmlp {
 namespace f4 {
@@ -91,6 +92,25 @@ __device__ __forceinline__ Alpha alpha_of(const float* ga, const float* gb) {
         r.second = __uint_as_float(static_cast<uint32_t>(e - h + 127) << 23);
     }
     return r;
+}
+
+// Column sums from their partial rows, in order: a warp of each CTA takes 32 columns at a time.
+__device__ __forceinline__ void column_sums(const Fp4GemmParams& p, int cta, int ctas, int lane) {
+    for (int c = cta * 32 + lane; c < p.sum_cols; c += ctas * 32) {
+        const float* from = p.sums + c;
+        Sum s = {0.0f, 0.0f};
+        long long r = 0;
+        for (; r + 8 <= p.sum_rows; r += 8) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __ldg(from + (r + i) * p.sum_cols);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s.add(x[i]);
+        }
+        for (; r < p.sum_rows; ++r) s.add(__ldg(from + r * p.sum_cols));
+        // (of infinities the second part is NaN)
+        p.db[c] = isfinite(s.hi) ? s.hi + s.lo : s.hi;
+    }
 }
 
 __device__ __forceinline__ int pick(int part, int g, int s) {

@@ -374,6 +374,8 @@ class DeviceFp4Linear:
         """Pointers of the bf16 tensors xs, which are looked over."""
         if isinstance(xs, torch.Tensor):
             xs = (xs,)
+        elif not isinstance(xs, (list, tuple)):
+            xs = list(xs)
         shape, n = spec
         dev, bf = self.device, torch.bfloat16
         if len(xs) != n:

@@ -457,3 +457,37 @@ def test_quantize_rows_alone(T, C, fmt):
     _sync()
     _check(got, x, fmt, 1, None if fmt == "mxfp4" else plain.tensor_scale([x]))
     assert torch.equal(got.q, both.q) and torch.equal(got.s, both.s)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("split,T,din,dout,t", [
+    # tiles of 256 tokens: K long, features few, up to 256 tokens and more
+    ("column", 333, 4128, 1056, 1), ("row", 300, 8192, 512, 2), ("column", 250, 8224, 4096, 1),
+    # pairs of CTAs for 65 to 128 tokens: one tile each
+    ("column", 66, 544, 12288, 1), ("column", 127, 288, 10400, 1), ("row", 100, 768, 12064, 3)])
+def test_linear_by_other_tiles(split, T, din, dout, t, fmt):
+    w = custom_linear(T, din, dout, t, split)
+    lay, X, dY = _layer(w, T + din + dout, fmt)
+    g = GuardBands()
+    g.guard(lay, ["Y", "dX", "ws"])
+    lay.forward(X, save=True)
+    lay.backward(dY)
+    _sync()
+    g.check()
+    _check_forward(lay, X)
+    _check_backward(lay, X, dY)
+
+
+@pytest.mark.parametrize("T", [40, 300, 1100])
+def test_bias_gradient_not_finite(T):
+    """Sums of infinities are what adding them gives."""
+    w = custom_linear(T, 288, 416, 1, "column")
+    lay, X, dY = _layer(w, 22, "mxfp4")
+    inf = float("inf")
+    dY[0][1, 3], dY[0][T - 1, 4], dY[0][2, 5], dY[0][T - 2, 5], dY[0][0, 6] = inf, -inf, inf, -inf, float("nan")
+    lay.forward(X, save=True)
+    lay.backward(dY)
+    _sync()
+    assert lay.db[3] == inf and lay.db[4] == -inf
+    assert torch.isnan(lay.db[5]) and torch.isnan(lay.db[6])
+    assert int(torch.isfinite(lay.db).sum()) == 416 - 4

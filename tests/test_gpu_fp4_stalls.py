@@ -67,3 +67,18 @@ def test_quantisation(copies, fmt):
     f4._sync()
     f4._check(got.rows, x, fmt, 1, None if g is None else float(g))
     f4._check(got.cols, x, fmt, 0, None if g is None else float(g))
+
+
+@pytest.mark.parametrize("fmt", f4.FORMATS)
+@pytest.mark.parametrize("copies", [0, 1, 3, 6])
+@pytest.mark.parametrize("split,T,din,dout,t", [
+    ("column", 333, 16384, 512, 1), ("row", 256, 16384, 4096, 2), ("column", 100, 2304, 12288, 1)])
+def test_other_tiles(split, T, din, dout, t, copies, fmt):
+    """Tiles of 256 tokens; pairs for 65 to 128 tokens."""
+    w = custom_linear(T, din, dout, t, split)
+    lay, X, _ = f4._layer(w, 5, fmt, backward=False)
+    with stalled(copies):
+        gives_up(lambda: lay.forward(X), 2)
+    lay.forward(X)
+    f4._sync()
+    f4._check_forward(lay, X)

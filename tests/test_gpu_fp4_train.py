@@ -388,3 +388,35 @@ def test_gradients_beyond_32_bits():
     assert abs(float(d.norm) - norm) <= tg.NORM * norm
     tg._check_out([out[-4:].clone(), out[:2].clone()], [x[-4:], x[:2]], norm, 1.0)
     assert int((out == 9.0).sum()) == 0
+
+
+@pytest.mark.parametrize("fmt", f4.FORMATS)
+@pytest.mark.parametrize("T,din,mid,dout", [
+    (24, 288, 416, 96), (100, 512, 2080, 416), (300, 1056, 2080, 288), (2300, 1024, 2080, 1056)])
+def test_two_layers_without_a_pause(T, din, mid, dout, fmt):
+    """Two layers forward, back and clipped, with new tokens each time and nothing that waits in
+    between: every step's results are those of the same calls one at a time."""
+    from tensor_transformer_mlp_gemm_gb300.grad import DeviceGradients
+    one, X, _ = f4._layer(custom_linear(T, din, mid, 1, "column"), 3, fmt)
+    two, _, dY = f4._layer(custom_linear(T, mid, dout, 1, "row"), 4, fmt)
+    clip = DeviceGradients(one.dW + [one.db] + two.dW + [two.db])
+    gen = f4._gen(5)
+    data = [(f4._randn(gen, T, din), f4._randn(gen, *dY[0].shape)) for _ in range(6)]
+    layers = (one, two)
+
+    def run(between):
+        seen = []
+        for x, dy in data:
+            one.forward([x], save=True), between()
+            two.forward(one.Y, save=True), between()
+            two.backward([dy]), between()
+            one.backward(two.dX), between()
+            clip.clip(0.05), between()
+            seen.append([v.clone() for lay in layers for v in lay.Y + lay.dX + lay.dW + [lay.db]])
+        f4._sync()
+        return seen
+
+    apart = run(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, b in zip(apart, run(lambda: None)):
+            assert _equal(a, b)
