@@ -490,7 +490,8 @@ size_t tpmlp_fp4_linear_workspace_bytes(const tpmlp_linear_dims* dims, int forma
  *   db = column sums of the bf16 dY (fp32)
  *   Xq, Xs, x_scale  as the forward call left them
  *   Wq, Ws     [t] shards W_i by rows ([in, oi])
- * With T = 0 the forward does nothing and the backward zeroes dW and db. */
+ * With T = 0 the forward does nothing and the backward zeroes dW and db.  Y may lie over X, and
+ * dX over dY; nothing else that is written over anything else of the call. */
 tpmlp_status tpmlp_fp4_column_linear_forward(const tpmlp_linear_dims* dims, int format,
                                              const void* const* X, void* x_scale, int x_calibrated,
                                              void* Xq, void* Xs, const void* const* Wq_shards,

@@ -304,6 +304,18 @@ tpmlp_status zero_grads(const Lin& s, Split k, void* const* dW, void* db, cudaSt
     return TPMLP_OK;
 }
 
+// Whether one of m buffers lies over one of n.
+bool any_overlap(const void* const* a, int m, int64_t abytes, void* const* b, int n, int64_t bbytes) {
+    for (int i = 0; i < m; ++i) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a[i]);
+        for (int j = 0; j < n; ++j) {
+            const uintptr_t y = reinterpret_cast<uintptr_t>(b[j]);
+            if (x < y + bbytes && y < x + abytes) return true;
+        }
+    }
+    return false;
+}
+
 inline const void* const* as_const(void* const* p) { return reinterpret_cast<const void* const*>(p); }
 
 tpmlp_status forward(Split k, const tpmlp_linear_dims* dims, int format, const void* const* X,
@@ -347,9 +359,11 @@ tpmlp_status forward(Split k, const tpmlp_linear_dims* dims, int format, const v
     p.K = K;
     p.groups = col ? s.t : 1;
     p.ksegs = col ? 1 : s.t;
-    // (to keep X by columns takes the launch anyway)
+    // (to keep X by columns takes the launch anyway; and CTAs that quantise X read it while others
+    // write Y)
     bool quantises = false;
-    if (!save) TPMLP_CUDA(fp4_small_quantises(p.M, p.N, p.K, p.groups, p.ksegs, quantises));
+    if (!save && !any_overlap(X, nx, 2LL * (col ? s.Tc : s.T) * K, Y, ny, 2LL * (col ? s.T : s.Tc) * p.N))
+        TPMLP_CUDA(fp4_small_quantises(p.M, p.N, p.K, p.groups, p.ksegs, quantises));
     p.x = quantises ? X : nullptr;
     p.early = !p.x;
     TPMLP_TRY(quantize(dev, X, nx, col, col ? s.Tc : s.T, K, format, x_scale, x_calibrated != 0,

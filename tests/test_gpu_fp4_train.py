@@ -420,3 +420,29 @@ def test_two_layers_without_a_pause(T, din, mid, dout, fmt):
     for _ in range(3):
         for a, b in zip(apart, run(lambda: None)):
             assert _equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", f4.FORMATS)
+@pytest.mark.parametrize("split,T,n,t", [
+    ("column", 1, 4096, 1), ("row", 8, 512, 1), ("column", 24, 512, 1), ("row", 100, 512, 1), ("column", 600, 1056, 1)])
+def test_results_over_inputs(split, T, n, t, fmt):
+    """Y where X lies, or a little behind it, and dX where dY lies."""
+    lay, X, dY = f4._layer(custom_linear(T, n, n, t, split), 8, fmt)
+    lay.forward(X, save=True)
+    lay.backward(dY)
+    want = [x[0].clone() for x in (lay.Y, lay.dX)]
+    for shift in (0, 8, -8, 64, n * (T // 2)):
+        # (buffers with room on both sides)
+        room = torch.zeros((T + 2) * n + 2 * abs(shift), dtype=torch.bfloat16, device="cuda")
+        at = n + abs(shift)
+        x, y = (room[k:k + T * n].view(T, n) for k in (at, at + shift))
+        for save in (False, True):
+            for _ in range(3):
+                x.copy_(X[0])
+                lay.forward([x], save=save, Y=[y])
+                f4._sync()
+                assert torch.equal(y, want[0])
+        x.copy_(dY[0])
+        lay.backward([x], dX=[y])
+        f4._sync()
+        assert torch.equal(y, want[1])
