@@ -288,7 +288,7 @@ tpmlp_status quantize(const DeviceInfo* dev, const void* const* src, int parts, 
         if (sums) p.sums[i] = sums + i * cols;
     }
     if (format == FP4_NV && !calibrated)
-        TPMLP_CUDA(timed(TPMLP_KERNEL_SP_COPY, 2, st,
+        TPMLP_CUDA(timed(TPMLP_KERNEL_SP_COPY, fp4_tensor_scale_kernels(p), st,
                          [&] { return launch_fp4_tensor_scale(p, static_cast<float*>(scale), st); }));
     if (!by_rows && !by_cols) return TPMLP_OK;
     const int mode = (by_rows ? FP4_Q_ROWS : 0) | (by_cols ? FP4_Q_COLS : 0) | (sums ? FP4_Q_SUMS : 0);
@@ -507,7 +507,7 @@ TPMLP_API tpmlp_status tpmlp_fp4_tensor_scale(const tpmlp_fp4_quant* d, const vo
     TPMLP_TRY(device_info(&dev));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const Fp4QuantParams p = quant_params(*d, src);
-    TPMLP_CUDA(timed(TPMLP_KERNEL_SP_COPY, 2, st,
+    TPMLP_CUDA(timed(TPMLP_KERNEL_SP_COPY, fp4_tensor_scale_kernels(p), st,
                      [&] { return launch_fp4_tensor_scale(p, static_cast<float*>(scale), st); }));
     return TPMLP_OK;
 }

@@ -66,7 +66,9 @@ enum Fp4QuantMode : int { FP4_Q_ROWS = 1, FP4_Q_COLS = 2, FP4_Q_SUMS = 4 };  // 
 
 // cudaErrorInvalidValue for a mode that is not built or a grid past the limit.
 cudaError_t launch_fp4_quant(const Fp4QuantParams& p, int fmt, int mode, cudaStream_t st);
-// g of all parts together into *scale (src, rows, cols and parts of p are read).
+// g of all parts together into *scale (src, rows, cols and parts of p are read), by one kernel or
+// two.
+int fp4_tensor_scale_kernels(const Fp4QuantParams& p);
 cudaError_t launch_fp4_tensor_scale(const Fp4QuantParams& p, float* scale, cudaStream_t st);
 // The values of a 4-bit matrix [R, K] (K-major) in bf16 [R, K].
 cudaError_t launch_fp4_dequant(long long R, long long K, int fmt, const void* q, const void* s,

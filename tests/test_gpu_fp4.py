@@ -491,3 +491,25 @@ def test_bias_gradient_not_finite(T):
     assert lay.db[3] == inf and lay.db[4] == -inf
     assert torch.isnan(lay.db[5]) and torch.isnan(lay.db[6])
     assert int(torch.isfinite(lay.db).sum()) == 416 - 4
+
+
+@pytest.mark.parametrize("T,C,n", [(1, 32, 1), (1, 4096, 8), (3, 288, 5), (16, 16384, 1), (16, 2048, 8),
+                                   (16, 2080, 8), (17, 16384, 1), (129, 2080, 3), (0, 96, 2)])
+def test_tensor_scale_of_parts(T, C, n):
+    """The largest anywhere, also the last of the last part, counts; what is not finite does not."""
+    from tensor_transformer_mlp_gemm_gb300 import fp4
+    g = _gen(T + C + n)
+    parts = [_randn(g, T, C) for _ in range(n)]
+    if T:
+        parts[0][0, 3], parts[n // 2][T - 1, 5] = float("inf"), float("nan")
+    for i in (0, n // 2, n - 1):
+        for r, c in ((0, 0), (T - 1, C - 1), (T // 2, C // 3)) if T else ():
+            kept = parts[i][r, c].clone()
+            parts[i][r, c] = -1000.0
+            got = fp4.tensor_scale(parts)
+            _sync()
+            assert float(got) == 2.0 ** -1   # the smallest power of two >= 1000 / 2688
+            parts[i][r, c] = kept
+    got = fp4.tensor_scale(parts)
+    _sync()
+    assert float(got) == (float(plain.tensor_scale(parts)) if T else 2.0 ** -110)
