@@ -682,7 +682,7 @@ GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 def make_grad_tensors(tensors):
     """An array of (grad, out, count, type): pointers or tensors, a number, a code."""
     return (tpmlp_grad_tensor * max(len(tensors), 1))(
-        *[tpmlp_grad_tensor(_ptr(g), _ptr(o), int(n), int(code)) for g, o, n, code in tensors])
+        *[(_ptr(g), _ptr(o), int(n), int(code)) for g, o, n, code in tensors])
 
 
 def tpmlp_grad_workspace_bytes(tensors: int) -> int:

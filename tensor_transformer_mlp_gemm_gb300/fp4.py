@@ -293,6 +293,7 @@ class DeviceFp4Linear:
         # where a forward call without a calibration writes the scale: one that keeps nothing, and
         # one that keeps X for the backward pass
         self._scales = torch.empty(2, 1, dtype=torch.float32, device=dev) if self.fmt == "nvfp4" else None
+        self._scale_ptrs = self._scales is not None and tuple(x.data_ptr() for x in self._scales)
 
     weights = property(lambda self: self._weights)
     b = property(lambda self: self._bias)
@@ -393,6 +394,7 @@ class DeviceFp4Linear:
         X = self._ptrs(X, self._x, "X")
         Y = self._y_ptrs if Y is None else self._ptrs(Y, self._y, "Y")
         q = s = scale = None
+        save = bool(save)
         if save:
             if self._backward is None:
                 raise ValueError("the weights have no form for the backward pass")
@@ -401,8 +403,8 @@ class DeviceFp4Linear:
         calibrated = self._x_scale is not None
         if calibrated:
             scale = self._x_scale.data_ptr()
-        elif self._scales is not None:
-            scale = self._scales[int(save)].data_ptr()
+        elif self._scale_ptrs:
+            scale = self._scale_ptrs[save]
         dev = self.device
         with binding.on_device(dev):
             self._call(self._dims, self._code, X, scale, calibrated, q, s, *self._forward, self._w_scale,

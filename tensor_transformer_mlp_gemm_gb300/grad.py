@@ -13,21 +13,13 @@ import torch
 from . import binding
 
 
-def _flat(x: torch.Tensor, what: str):
-    if x.dtype not in binding.GRAD_TYPES or not x.is_contiguous() or not x.is_cuda:
-        raise ValueError(f"{what} must be contiguous fp32, bf16 or fp16 CUDA tensors, got {x.dtype} "
-                         f"{tuple(x.shape)} {'' if x.is_contiguous() else 'not contiguous '}on {x.device}")
+def _refuse(x: torch.Tensor, what: str, device):
+    raise ValueError(f"{what} must be contiguous fp32, bf16 or fp16 tensors on {device}, got {x.dtype} "
+                     f"{tuple(x.shape)} {'' if x.is_contiguous() else 'not contiguous '}on {x.device}")
 
 
-def _check_apart(grads, outs) -> None:
+def _check_apart(spans) -> None:
     """Nothing is written over what another entry reads or writes."""
-    spans = []
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        if g.numel():
-            n = g.numel() * g.element_size()
-            spans.append((g.data_ptr(), g.data_ptr() + n, i))
-            if o.data_ptr() != g.data_ptr():
-                spans.append((o.data_ptr(), o.data_ptr() + n, i))
     spans.sort()
     for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
         if start < end:
@@ -48,15 +40,29 @@ class DeviceGradients:
         if len(self.out) != len(self.grads):
             raise ValueError(f"{len(self.grads)} outputs are needed, got {len(self.out)}")
         self.device = dev = self.grads[0].device
-        for g, o in zip(self.grads, self.out):
-            _flat(g, "gradients")
+        if dev.type != "cuda":
+            _refuse(self.grads[0], "gradients", "a CUDA device")
+        # (one pass: a list has hundreds of tensors)
+        entries, spans = [], []
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            dtype, count, at = g.dtype, g.numel(), g.data_ptr()
+            code = binding.GRAD_TYPES.get(dtype)
+            if code is None or not g.is_contiguous() or g.device != dev:
+                _refuse(g, "gradients", dev)
+            end, to = at + count * g.element_size(), at
             if o is not g:
-                _flat(o, "outputs")
-            if g.device != dev or o.device != dev or o.dtype != g.dtype or o.shape != g.shape:
-                raise ValueError(f"gradients lie on one device, outputs have their shape and type: got "
-                                 f"{g.dtype} {tuple(g.shape)} on {g.device}, {o.dtype} {tuple(o.shape)} on "
-                                 f"{o.device}")
-        _check_apart(self.grads, self.out)
+                if not o.is_contiguous() or o.device != dev:
+                    _refuse(o, "outputs", dev)
+                if o.dtype != dtype or o.shape != g.shape:
+                    raise ValueError(f"outputs have their gradients' shape and type: got {dtype} "
+                                     f"{tuple(g.shape)} and {o.dtype} {tuple(o.shape)}")
+                to = o.data_ptr()
+            if count:
+                spans.append((at, end, i))
+                if to != at:
+                    spans.append((to, to + end - at, i))
+            entries.append((at, to, count, code))
+        _check_apart(spans)
         n = len(self.grads)
         need = binding.tpmlp_grad_workspace_bytes(n)
         if need == 0:
@@ -64,8 +70,7 @@ class DeviceGradients:
         self._measure = binding.prepared("tpmlp_grad_norm")
         self._clip = binding.prepared("tpmlp_grad_clip")
         # (marshalled once, so the object keeps the tensors)
-        self._tensors = binding.make_grad_tensors(
-            [(g, o, g.numel(), binding.GRAD_TYPES[g.dtype]) for g, o in zip(self.grads, self.out)])
+        self._tensors = binding.make_grad_tensors(entries)
         self.norm = torch.empty(1, dtype=torch.float32, device=dev)
         self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
 
