@@ -603,9 +603,9 @@ tpmlp_status tpmlp_norm_backward(const tpmlp_norm_params* params, const void* co
  * for each of them, in the gradient's own type (the product in fp32, rounded once).  out may
  * be grad itself; it may not lie over any other tensor of the list, nor may a tensor be in
  * the list twice.  Tensors are contiguous, of any size (0 too, and then any pointer), and start
- * on a multiple of their element's size.  Squares are summed in fp32 over at most 64 elements
- * and in 64 bits from there (in 64 bits at once where fp32 would overflow or lose them), in an
- * order that depends on sizes and alignment alone.  A NaN makes the norm and everything clipped
+ * on a multiple of their element's size.  Squares are summed in fp32 over at most 64 elements,
+ * from there in two fp32 parts and in 64 bits (in 64 bits at once where fp32 would overflow or
+ * lose them), in an order that depends on sizes and alignment alone.  A NaN makes the norm and everything clipped
  * NaN; an infinity makes the norm infinite and what is clipped 0 (infinities NaN).  In place,
  * gradients whose factor is 1 are not written.
  *   norm       fp32 [1] on the device (output; infinite where the norm is past fp32's range,
@@ -780,7 +780,7 @@ enum {
     TPMLP_KERNEL_WGRAD_A = 5,     /* dA_i = X^T.dY_i */
     TPMLP_KERNEL_BIAS_GRAD = 6,   /* db1, db2, linear db column sums; gradient norm and clipping (all launches) */
     TPMLP_KERNEL_LINEAR_FWD = 7,  /* linear layers (bf16, 8-bit, 4-bit): Y_i = X.W_i + b, Z = sum_i X_i.W_i + b */
-    TPMLP_KERNEL_LINEAR_DGRAD = 8,  /* linear layers (bf16, 8-bit, 4-bit): dX = sum_i dY_i.W_i^T, dX_i = dZ.W_i^T */
+    TPMLP_KERNEL_LINEAR_DGRAD = 8,  /* linear layers (bf16, 8-bit, 4-bit): dX = sum_i dY_i.W_i^T, dX_i = dZ.W_i^T (4-bit: and db) */
     TPMLP_KERNEL_LINEAR_WGRAD = 9,  /* linear layers (bf16, 8-bit, 4-bit): dW_i */
     TPMLP_KERNEL_LAYERNORM_FWD = 10,  /* sequence-parallel sublayer: LN(X) and row statistics; tpmlp_norm_forward */
     TPMLP_KERNEL_LAYERNORM_BWD = 11,  /* sequence-parallel sublayer: dX, dgamma, dbeta (2 launches; 3 for h > 4096); tpmlp_norm_backward (2; 1 with no norm and no gate to add up) */
