@@ -96,7 +96,9 @@ __device__ __forceinline__ Alpha alpha_of(const float* ga, const float* gb) {
 
 // Column sums from their partial rows, in order: a warp of each CTA takes 32 columns at a time.
 __device__ __forceinline__ void column_sums(const Fp4GemmParams& p, int cta, int ctas, int lane) {
-    for (int c = cta * 32 + lane; c < p.sum_cols; c += ctas * 32) {
+    // (unsigned: a step may pass 2^31)
+    const unsigned cols = p.sum_cols, step = ctas * 32;
+    for (unsigned c = cta * 32 + lane; c < cols; c += step) {
         const float* from = p.sums + c;
         Sum s = {0.0f, 0.0f};
         long long r = 0;
