@@ -479,6 +479,8 @@ constexpr unsigned ONE = C_CTAS * CT * M_UNROLL;
 __global__ void __cluster_dims__(C_CTAS, 1, 1) __launch_bounds__(CT, 1)
     fp4_small_scale_kernel(const __grid_constant__ Fp4QuantParams p, unsigned vecs, unsigned* scale) {
     __shared__ uint32_t s_all[C_CTAS];
+    // (the first CTA's shared memory is there once it has started: all have by the wait below)
+    ptx::cluster_arrive_relaxed();
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const unsigned all = vecs * p.parts;
@@ -493,6 +495,8 @@ __global__ void __cluster_dims__(C_CTAS, 1, 1) __launch_bounds__(CT, 1)
 #pragma unroll
     for (int u = 0; u < M_UNROLL; ++u) m = largest_finite(v[u], m);
     m = largest_of_cta<CT>(m);
+    __syncwarp();
+    ptx::cluster_wait();
     if (threadIdx.x == 0)
         f8::store_cluster(ptx::mapa_shared(ptx::smem_u32(&s_all[blockIdx.x]), 0), static_cast<int>(m));
     __syncwarp();
