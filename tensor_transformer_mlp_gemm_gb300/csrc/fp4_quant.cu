@@ -267,12 +267,13 @@ __global__ void __launch_bounds__(QT, Q_PER_SM)
         }
         if (threadIdx.x < SB / 16) {
             const int i = threadIdx.x * 16;
+            // (tiles times bytes pass 2^32 from 2^29 of K on)
             if (ROWS && r0 < total) {
-                uint8_t* s = p.s_rows[x.part] + rt * ((p.rows_k + 255) / 256) * (2 * SB) + x.ct * SB + i;
+                uint8_t* s = p.s_rows[x.part] + rt * ((p.rows_k + 255) / 256) * (2 * SB) + static_cast<long long>(x.ct) * SB + i;
                 *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(&s_rows[b][i]);
             }
             if (COLS && c0 < p.cols) {
-                uint8_t* s = p.s_cols[x.part] + x.ct * ((total + 255) / 256) * (2 * SB) + rt * SB + i;
+                uint8_t* s = p.s_cols[x.part] + x.ct * ((total + 255) / 256) * (2 * SB) + static_cast<long long>(rt) * SB + i;
                 *reinterpret_cast<uint4*>(s) = *reinterpret_cast<const uint4*>(&s_cols[b][i]);
             }
         }
