@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
             const int stop = p.stall >= 0 && rank == splits - 1 ? min(last, first + p.stall) : last;
             // B's part of stage `stage`; scales of 128 rows lie next to each other along K
             constexpr uint32_t X_BYTES = QUANT ? TN * 128 + C::kScales : 0;  // written here, not copied
+            // (of long K their offsets pass 2^31)
             const long long along = static_cast<long long>(kblocks) * C::kScales;
             const long long along_a = p.a_seg ? along * p.ksegs : along;
             auto load_b = [&](int st, int seg, int block) {
@@ -149,8 +150,8 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
                 ptx::mbar_arrive_expect_tx(full, C::kStageBytes - X_BYTES);
                 // (a byte holds two of K)
                 ptx::tma_load_3d(sw, p.b_map + (p.b_z ? 0 : wi), block * 128, f0, p.b_z ? wi : 0, full);
-                bulk_load(sw + F4_BOX_BYTES + TN * 128, p.sb[wi] + (f0 >> 7) * along + block * C::kScales,
-                          C::kScales, full);
+                bulk_load(sw + F4_BOX_BYTES + TN * 128,
+                          p.sb[wi] + (f0 >> 7) * along + static_cast<long long>(block) * C::kScales, C::kScales, full);
             };
             // what the ring takes of B, if that may be read already
             int ahead = 0;
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(S_THREADS, Small<FMT, TN, PER_SM>::kPerSm)
                         // (behind the last token any: nobody reads those sums)
                         const int at = t0 + 128 * i < p.M ? (t0 >> 7) + i : 0;
                         bulk_load(sw + F4_BOX_BYTES + TN * 128 + (1 + i) * C::kScales,
-                                  p.sa[xi] + at * along_a + ka * C::kScales, C::kScales, full);
+                                  p.sa[xi] + at * along_a + static_cast<long long>(ka) * C::kScales, C::kScales, full);
                     }
                 }
                 ++fills;

@@ -4,7 +4,9 @@ import gc
 import pytest
 import torch
 
+import plain_fp4 as plain
 import test_gpu_fp4 as f4
+from tensor_transformer_mlp_gemm_gb300.inputs import custom_linear
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +74,45 @@ def test_quantise_columns(fmt):
     got = fp4.quantize_tokens(x, fmt, rows=False, cols=True, scale=scale).cols
     f4._sync()
     _periodic(got, one)
+
+
+# features in whose scales' bytes of 128 rows pass 2^31
+LONG = {"mxfp4": (1 << 29) + 1024, "nvfp4": (1 << 28) + 1024}
+END = 4096
+
+
+@pytest.mark.parametrize("fmt", f4.FORMATS)
+@pytest.mark.parametrize("split,T,t", [("column", 1, 1), ("row", 20, 1), ("row", 40, 2)])
+def test_few_tokens(split, T, t, fmt):
+    """A layer of so many features in that the scales of its last ones lie past 2^31 bytes: X is zero
+    but for the first and the last of each shard, whose products are those of 8192 of K."""
+    from tensor_transformer_mlp_gemm_gb300 import fp4
+    din, dout = LONG[fmt], 32
+    n = din // t
+    g = f4._gen(T)
+    ends = [[f4._randn(g, END, dout, std=0.05) for _ in range(2)] for _ in range(t)]
+    W = []
+    for a, b in ends:
+        w = torch.zeros(n, dout, dtype=torch.bfloat16, device="cuda")
+        w[:END], w[-END:] = a, b
+        w[END:-END].fill_(0.01)           # (scales of their own in between)
+        W.append(w)
+    weights = fp4.quantize_weight(W, fmt)
+    del W, w
+    X, kept = [], []
+    for _ in range(t):
+        x = torch.zeros(T, n, dtype=torch.bfloat16, device="cuda")
+        x[:, :END], x[:, -END:] = f4._randn(g, T, END), f4._randn(g, T, END)
+        X.append(x)
+        kept += [x[:, :END], x[:, -END:]]
+    lay = fp4.DeviceFp4Linear(custom_linear(T, din, dout, t, split), weights, f4._randn(g, dout, std=0.1))
+    lay.forward(X)
+    f4._sync()
+    gx = None if fmt == "mxfp4" else plain.tensor_scale([torch.cat(kept, 1)])
+    gw = weights.scale
+    a = torch.cat([plain.values(x, fmt, 1, gx) for x in kept], 1)
+    v = torch.cat([plain.values(w, fmt, 0, gw) for pair in ends for w in pair], 0)
+    ref = a @ v + lay.b.double()
+    # (what X is zero for adds zeros, without a rounding)
+    bound = plain.product_bound(a, v, a.shape[1] // 64) + 2 * plain.F32 * ref.abs()
+    plain.check("Y", lay.Y[0], ref, bound + plain.BF16 * (ref.abs() + bound))
