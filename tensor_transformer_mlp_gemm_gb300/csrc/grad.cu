@@ -266,8 +266,11 @@ __device__ __forceinline__ Norm norm_of(const double* partial, int n, double max
         if (threadIdx.x == 0) {
             if (x >= 1e-30 && x <= 1e30) {
                 // (roots and quotients in 64 bits take a microsecond)
-                s_norm->norm = sqrtf(static_cast<float>(x));
-                s_norm->factor = static_cast<float>(max_norm) / (s_norm->norm + static_cast<float>(G_EPS));
+                const float r = sqrtf(static_cast<float>(x));
+                const float q = static_cast<float>(max_norm) / (r + static_cast<float>(G_EPS));
+                s_norm->norm = r;
+                // (a quotient near or below fp32's smallest normal number has lost digits)
+                s_norm->factor = q >= 0x1p-100f || max_norm == 0.0 ? q : max_norm / (sqrt(x) + G_EPS);
             } else {
                 const double r = sqrt(x);
                 s_norm->norm = static_cast<float>(r);
