@@ -252,30 +252,32 @@ __global__ void __launch_bounds__(GT, G_PER_SM)
     }
 }
 
-// The norm of all partial sums, and max_norm / (norm + 1e-6), in every thread.
+// The norm of all partial sums, and min(1, max_norm / (norm + 1e-6)) as f e, in every thread.  (In
+// two factors where fp32 would lose digits: f stays normal down to quotients of 2^-266, where no
+// product is.  A NaN stays.)
 struct Norm {
-    float norm;
-    double factor;
+    float norm, f, e;
 };
-__device__ __forceinline__ Norm norm_of(const double* partial, int n, double max_norm, Norm* s_norm) {
+__device__ __forceinline__ Norm norm_of(const double* partial, int n, float max_norm, Norm* s_norm) {
     if (threadIdx.x < 32) {
         double x = 0.0;
         for (int i = threadIdx.x; i < n; i += 32) x += partial[i];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (threadIdx.x == 0) {
-            if (x >= 1e-30 && x <= 1e30) {
-                // (roots and quotients in 64 bits take a microsecond)
-                const float r = sqrtf(static_cast<float>(x));
-                const float q = static_cast<float>(max_norm) / (r + static_cast<float>(G_EPS));
-                s_norm->norm = r;
-                // (a quotient near or below fp32's smallest normal number has lost digits)
-                s_norm->factor = q >= 0x1p-100f || max_norm == 0.0 ? q : max_norm / (sqrt(x) + G_EPS);
+            // (roots and quotients in 64 bits take a microsecond)
+            const bool plain = x >= 1e-30 && x <= 1e30;
+            float r = sqrtf(static_cast<float>(x)), f = max_norm / (r + static_cast<float>(G_EPS)), e = 1.0f;
+            if (plain && (f >= 0x1p-100f || max_norm == 0.0f)) {
+                f = fminf(f, 1.0f);
             } else {
-                const double r = sqrt(x);
-                s_norm->norm = static_cast<float>(r);
-                s_norm->factor = max_norm / (r + G_EPS);
+                const double root = sqrt(x), q = max_norm / (root + G_EPS);
+                const bool tiny = q < 0x1p-100, least = q < 0x1p-200;
+                if (!plain) r = static_cast<float>(root);
+                f = q >= 1.0 ? 1.0f : static_cast<float>(least ? q * 0x1p140 : tiny ? q * 0x1p64 : q);
+                e = least ? 0x1p-140f : tiny ? 0x1p-64f : 1.0f;
             }
+            *s_norm = Norm{r, f, e};
         }
     }
     __syncthreads();
@@ -286,14 +288,14 @@ __global__ void __launch_bounds__(GT) grad_norm_kernel(const double* partial, in
     __shared__ Norm s_norm;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const Norm x = norm_of(partial, n, 0.0, &s_norm);
+    const Norm x = norm_of(partial, n, 0.0f, &s_norm);
     if (threadIdx.x == 0) *norm = x.norm;
 }
 
 template <int N>
 __global__ void __launch_bounds__(GT, G_PER_SM)
     grad_scale_kernel(const __grid_constant__ Tensors<N> p, const double* __restrict__ partial, int n,
-                      double max_norm, float* norm) {
+                      float max_norm, float* norm) {
     __shared__ Norm s_norm;
     ptx::griddep_launch_dependents();
     // the first chunk is on its way while the sums of squares end
@@ -303,10 +305,7 @@ __global__ void __launch_bounds__(GT, G_PER_SM)
     ptx::griddep_wait();
     const Norm x = norm_of(partial, n, max_norm, &s_norm);
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = x.norm;
-    const double q = x.factor;
-    // in two factors: one below fp32's normal numbers would lose digits  (NaN stays)
-    const bool tiny = q < 0x1p-100;
-    const float f = q >= 1.0 ? 1.0f : static_cast<float>(tiny ? q * 0x1p64 : q), e = tiny ? 0x1p-64f : 1.0f;
+    const float f = x.f, e = x.e;
     for (unsigned r = blockIdx.x; r < p.chunks; r += gridDim.x) {
         if (r != blockIdx.x) {
             k = chunk_of(p, p.chunks - 1 - r);
@@ -461,7 +460,7 @@ tpmlp_status run(const Plan& plan, const tpmlp_grad_tensor* t, int64_t n, bool c
         if (l < launches - 1) fill(p, t, n, &at, plan.vecs);
         const unsigned grid = p.chunks < static_cast<unsigned>(plan.ctas) ? p.chunks : plan.ctas;
         TPMLP_CUDA(timed(TPMLP_KERNEL_BIAS_GRAD, 1, st, [&] {
-            return launch(grad_scale_kernel<N>, grid, st, p, all, sums, static_cast<double>(max_norm),
+            return launch(grad_scale_kernel<N>, grid, st, p, all, sums, max_norm,
                           l == launches - 1 ? norm : static_cast<float*>(nullptr));
         }));
     }

@@ -37,3 +37,10 @@ def _clip(value, max_norm):
 def test_small_limits(value, max_norm):
     """The quotient of a limit and a norm that fp32 holds may be a number that it does not."""
     _clip(value, max_norm)
+
+
+@pytest.mark.parametrize("max_norm", [1e-10, 1e-20, 1e-30, 1e-36])
+@pytest.mark.parametrize("value", [1e20, 1e28, 1e37])
+def test_large_gradients(value, max_norm):
+    """Factors down to 1e-75: no one number of fp32, and no product of two with 2^-64 for one."""
+    _clip(value, max_norm)
