@@ -682,9 +682,9 @@ tpmlp_status tpmlp_set_wide_tiles(int mode);
  * address, element type, extents, strides, box, swizzle), so a repeated call
  * on the same buffers encodes nothing.  A buffer at a new address is a new key
  * (a stale entry is never used for another address); the operands of the 8-bit
- * and 4-bit layers share one map for each shape, and each call sets the address in its own
- * copy.  At most 4096 maps are
- * kept; when the cache is full it is emptied.  Thread-safe (one mutex).
+ * and 4-bit layers share one map for each shape (4-bit shards that lie at equal steps, of whole
+ * rows, one for each shape and step), and each call sets the address in its own copy.  At most
+ * 4096 maps are kept; when the cache is full it is emptied.  Thread-safe (one mutex).
  * tpmlp_map_cache_stats reports the hits, misses (encodings) and entries so
  * far; any pointer may be NULL.  Always TPMLP_OK. */
 tpmlp_status tpmlp_map_cache_stats(uint64_t* hits, uint64_t* misses, uint64_t* entries);

@@ -129,24 +129,25 @@ size_t backward_bytes(const tpmlp_linear_dims& d, Split k, int format) {
            align256(static_cast<size_t>(up128(d.tokens)) * d.out_features * sizeof(float)) + 256;
 }
 
-// The step between matrices that lie at equal, ascending ones (a multiple of 16 bytes that a
-// tensor map takes), else 0.
-uint64_t equal_steps(const void* const* p, int n) {
+// The step between matrices [outer, inner bytes] that lie at equal, ascending ones which a tensor
+// map takes beside its rows' (whole rows of them, of at least a matrix), else 0.
+uint64_t equal_steps(const void* const* p, int n, uint64_t inner, uint64_t outer) {
     const uint64_t first = reinterpret_cast<uint64_t>(p[0]);
     const uint64_t step = n > 1 ? reinterpret_cast<uint64_t>(p[1]) - first : 0;
     for (int i = 2; i < n; ++i)
         if (reinterpret_cast<uint64_t>(p[i]) - first != i * step) return 0;
-    return step < (uint64_t(1) << 40) && step % 16 == 0 ? step : 0;
+    return step < (uint64_t(1) << 40) && step >= inner * outer && step % inner == 0 ? step : 0;
 }
 
 // Matrices [outer, inner bytes], `n` of them `step` bytes apart, in elements of `elem` bytes and
-// boxes of box_inner elements x box_outer rows.  Kept by shape, as maps of 8-bit operands are.
+// boxes of box_inner elements x box_outer rows.  Kept by shape and step, as maps of 8-bit operands
+// are by shape.
 bool encode3(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t n, uint64_t step,
              int elem, uint32_t box_inner, uint32_t box_outer) {
     const CUtensorMapDataType type = elem == 8 ? CU_TENSOR_MAP_DATA_TYPE_INT64 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const CUtensorMapSwizzle swizzle = elem == 8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
     const cuuint64_t dims[3] = {inner / elem, outer, n};
-    const cuuint64_t strides[2] = {inner, n > 1 ? step : inner};
+    const cuuint64_t strides[2] = {inner, n > 1 ? step : inner * outer};
     const cuuint32_t box[3] = {box_inner, box_outer, 1};
     const MapKey key =
         make_map_key(type, 3, nullptr, dims, strides, box, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
@@ -195,7 +196,8 @@ struct Product {
 bool encode_operand(CUtensorMap* m, CUtensorMap* sm, const Operand& o, int K, int rows, int box,
                     int format, uint32_t box_tiles, int* z) {
     const uint64_t inner = static_cast<uint64_t>(fp4_scale_bytes(1, K, format));
-    const uint64_t step = equal_steps(o.q, o.n), sstep = equal_steps(o.s, o.n);
+    const uint64_t step = equal_steps(o.q, o.n, fp4_ld(K), rows);
+    const uint64_t sstep = equal_steps(o.s, o.n, inner, up128(rows));
     *z = o.n > 1 && step && sstep;
     const uint64_t n = *z ? o.n : 1;
     if (!encode3(m, o.q[0], fp4_ld(K), rows, n, step, 1, 128, box)) return false;
