@@ -166,8 +166,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     ptx::cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // (B may be there before the grids ahead have ended, or everything)
-    if (warp == 3 || !(p.apart || (p.early && warp == 2))) ptx::griddep_wait();
+    // (B may be there before the grids ahead have ended, or everything.  Warp 3 waits below, once its
+    // registers are free: two of the output warps need them, and waited with it.  Backward of 333
+    // tokens, 1056 -> 2080 features, in a graph 19.0 us, now 16.1; 256 tokens, 19712 -> 8192 137, now
+    // 134; but 200 tokens, 12288 -> 12288 in eight shards 146, now 148.)
+    if (warp != 3 && !(p.apart || (p.early && warp == 2))) ptx::griddep_wait();
 
     const int kblocks = (p.K + F4_BK - 1) / F4_BK;
     const int nk = kblocks * p.ksegs;
@@ -232,6 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             if (!ok)
                 store_cluster64(ptx::mapa_shared(stages_done + 8 * (F_COPIED + 2 * rank + of_b), 0), fills);
         } else if (warp == 3) {
+            ptx::griddep_wait();
             if (p.apart) ptx::griddep_launch_dependents();  // (the grid ahead has ended)
             if (p.sums) f4::column_sums(p, blockIdx.x, gridDim.x, lane);
         } else if (warp == 1 && rank == 0) {
