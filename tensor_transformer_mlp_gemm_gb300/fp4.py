@@ -115,23 +115,26 @@ class Fp4Tokens:
 
 class Fp4Weights:
     """The shards of one weight in 4 bits: ``forward`` [out_i, in_i] grouped along the inputs,
-    ``backward`` [in_i, out_i] grouped along the outputs, or None; their ``scale``."""
+    ``backward`` [in_i, out_i] grouped along the outputs, or None; their ``scale``.  They stay the
+    same: a layer holds their addresses."""
 
     def __init__(self, forward: list, backward: list | None):
-        self.forward, self.backward = list(forward), None if backward is None else list(backward)
-        both = self.forward + (self.backward or [])
+        self._forward, self._backward = tuple(forward), None if backward is None else tuple(backward)
+        both = self._forward + (self._backward or ())
         if not both:
             raise ValueError("no shards")
         first = both[0]
         self.fmt = first.fmt
-        if self.backward is not None and len(self.backward) != len(self.forward):
+        if self._backward is not None and len(self._backward) != len(self._forward):
             raise ValueError("as many shards are needed forward and backward")
         for m in both:
             # one scale for all: the shards of a row-parallel layer are summed before it is applied
             if m.fmt != first.fmt or m.device != first.device or m._ptrs[2] != first._ptrs[2]:
                 raise ValueError("the shards of a weight have one format, device and scale")
 
-    scale = property(lambda self: self.forward[0].scale)
+    forward = property(lambda self: self._forward)
+    backward = property(lambda self: self._backward)
+    scale = property(lambda self: self._forward[0].scale)
 
 
 class _Space:
@@ -261,7 +264,7 @@ class DeviceFp4Linear:
         if len(weights.forward) != t:
             raise ValueError(f"{t} weight shards are needed, got {len(weights.forward)}")
         for m, shape in ([(m, wshape[::-1]) for m in weights.forward]
-                         + [(m, wshape) for m in weights.backward or []]):
+                         + [(m, wshape) for m in weights.backward or ()]):
             if m.shape != shape or m.device != dev:
                 raise ValueError(f"a 4-bit weight shard of shape {shape} on {dev} is needed, got "
                                  f"{m.shape} on {m.device}")
