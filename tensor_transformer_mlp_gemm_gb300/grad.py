@@ -30,21 +30,22 @@ class DeviceGradients:
     """A list of gradients (fp32, bf16, fp16; any sizes) that are clipped together.
 
     out: where the clipped ones go, tensors of the same shapes and types, or None: in place.
+    Both stay the same, with the addresses that they have now: for others another list is made.
     ``norm``: fp32 [1] on the device, written by both calls."""
 
     def __init__(self, grads, out=None):
-        self.grads = tuple(grads)
-        self.out = self.grads if out is None else tuple(out)
-        if not self.grads:
+        self._grads = grads = tuple(grads)
+        self._out = out = grads if out is None else tuple(out)
+        if not grads:
             raise ValueError("at least one gradient is needed")
-        if len(self.out) != len(self.grads):
-            raise ValueError(f"{len(self.grads)} outputs are needed, got {len(self.out)}")
-        self.device = dev = self.grads[0].device
+        if len(out) != len(grads):
+            raise ValueError(f"{len(grads)} outputs are needed, got {len(out)}")
+        self.device = dev = grads[0].device
         if dev.type != "cuda":
-            _refuse(self.grads[0], "gradients", "a CUDA device")
+            _refuse(grads[0], "gradients", "a CUDA device")
         # (one pass: a list has hundreds of tensors)
         entries, spans = [], []
-        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+        for i, (g, o) in enumerate(zip(grads, out)):
             dtype, count, at = g.dtype, g.numel(), g.data_ptr()
             code = binding.GRAD_TYPES.get(dtype)
             if code is None or not g.is_contiguous() or g.device != dev:
@@ -63,7 +64,7 @@ class DeviceGradients:
                     spans.append((to, to + end - at, i))
             entries.append((at, to, count, code))
         _check_apart(spans)
-        n = len(self.grads)
+        self._n = n = len(grads)
         need = binding.tpmlp_grad_workspace_bytes(n)
         if need == 0:
             raise ValueError(f"too many gradients for a call: {n}")
@@ -74,16 +75,19 @@ class DeviceGradients:
         self.norm = torch.empty(1, dtype=torch.float32, device=dev)
         self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
 
+    grads = property(lambda self: self._grads)
+    out = property(lambda self: self._out)
+
     def measure(self, stream=None) -> torch.Tensor:
         """The norm, without clipping."""
         with binding.on_device(self.device):
-            self._measure(self._tensors, len(self.grads), self.norm.data_ptr(), self.ws.data_ptr(),
+            self._measure(self._tensors, self._n, self.norm.data_ptr(), self.ws.data_ptr(),
                           binding.stream_on(self.device, stream))
         return self.norm
 
     def clip(self, max_norm: float, stream=None) -> torch.Tensor:
         """Writes the clipped gradients; returns the norm before clipping."""
         with binding.on_device(self.device):
-            self._clip(self._tensors, len(self.grads), max_norm, self.norm.data_ptr(), self.ws.data_ptr(),
+            self._clip(self._tensors, self._n, max_norm, self.norm.data_ptr(), self.ws.data_ptr(),
                        binding.stream_on(self.device, stream))
         return self.norm

@@ -40,3 +40,25 @@ def test_weight_shards_stay():
         f4._check_forward(layer, X)
         f4._check_backward(layer, X, dY)
     assert torch.equal(other.Y[1], lay.Y[1])
+
+
+def test_gradients_stay():
+    """Neither gradients nor outputs are exchanged beneath a list (which would go on with the freed
+    ones), and a caller's own lists may change."""
+    import test_gpu_grad as tg
+    from tensor_transformer_mlp_gemm_gb300.grad import DeviceGradients
+    xs = tg._grads([3000, 70], [torch.float32, torch.bfloat16])
+    out = [torch.empty_like(x) for x in xs]
+    keep = [[x.clone() for x in xs], list(out)]
+    d = DeviceGradients(xs, out)
+    xs.clear()
+    out.clear()
+    for name in ("grads", "out"):
+        with pytest.raises(AttributeError):
+            setattr(d, name, ())
+        with pytest.raises(TypeError):
+            getattr(d, name)[0] = keep[0][0]
+    d.clip(1e-3)
+    tg._sync()
+    want = tg._check_norm(d.norm, keep[0])
+    tg._check_out(keep[1], keep[0], want, 1e-3)
