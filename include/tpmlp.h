@@ -429,6 +429,11 @@ tpmlp_status tpmlp_fp8_row_linear_backward(const tpmlp_linear_dims* dims,
  *        range becomes the largest value
  *   q  = round-to-nearest-even(x / s), of nv x / (s g)
  *
+ * Two things differ from what else goes under these names.  mx elsewhere often takes for s the
+ * power of two of max |x| over that of 4 and cuts off what lies above 6 s: bytes differ for a
+ * group whose largest is between 6 and 8 times a power of two.  nv elsewhere takes any fp32 for
+ * g: tensors quantised with one are not taken here.
+ *
  * The same on every machine: powers of two leave every comparison exact.  A group with an
  * infinity or a NaN has the scale NaN, and so have the results that take part of it.
  *

@@ -14,7 +14,7 @@
 //                128 ((w - 4) / 4) .. into registers, frees the accumulator for the next
 //                tile's MMAs, and writes from there
 // What bounds it: the tensor cores, at 256 x 256 x 256 33.5 MFLOP for 64 KB of operands and 6 to
-// 12 KB of scales from L2.  Measured: 2048 tokens, 12288 -> 36864 features nv 260 us, 7.1 PFLOP/s;
+// 12 KB of scales from L2.  Measured: 2048 tokens, 12288 -> 36864 features nv 254 us, 7.3 PFLOP/s;
 // 16384 x 4096 x 4096 mx 86 us, 6.4 PFLOP/s, where a tile has 16 stages: of these the scales'
 // copies take 3 (nv 6), and the accumulator's hand-over and the outputs beside the loads 10 each.
 //

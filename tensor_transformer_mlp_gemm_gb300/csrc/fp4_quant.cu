@@ -10,8 +10,10 @@
 // then 32 rows of two columns: whole groups, 16 bytes of each output.  (Tiles loaded into
 // registers, 8 rows x 8 columns a thread, had every lane of a group work out its scale and
 // nothing on the way meanwhile: both groupings of 16384 x 4096 43 us, now 40, with the sums 46,
-// now 42; threads of 16 rows or columns, 512 in a CTA, took 45 us.)  It issues in two thirds of
-// the cycles: two instructions a value and grouping for the conversion alone, 2.5 of nv.
+// now 42; threads of 16 rows or columns, 512 in a CTA, took 45 us.)  No unit is full: it issues in
+// 65 (mx) and 71 % (nv) of the cycles, two and 2.5 instructions a value and grouping for the
+// conversion alone, has the ALU busy for 70 % and DRAM for 55 and 44 %; with six warps for each
+// scheduler most of what waits does so for the barrier behind a tile.
 #include <cuda_fp16.h>
 
 #include "fp4_cvt.cuh"
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(MT, M_PER_SM)
 // Small tensors in one launch, by one cluster whose CTAs hand their largest to the first: as many
 // vectors in all parts as its threads have on the way at once.  (By this and by two launches, us of
 // the device one behind the other, of the host: 1 x 4096 1.65, 1.8 and 2.9, 4.6; 16 x 12288 2.3, 1.95
-// and 2.9, 4.5; but 128 x 4096 3.7, 2.2.)
+// and 2.9, 4.5; but 128 x 4096 3.7, 2.2.  The wait for the cluster's start takes 0.04 to 0.1 of it.)
 constexpr int CT = 1024, C_CTAS = 8;
 constexpr unsigned ONE = C_CTAS * CT * M_UNROLL;
 

@@ -488,9 +488,12 @@ cudaError_t launch(const Fp4GemmParams& p, cudaStream_t st) {
     const long long tiles = static_cast<long long>((p.N + 127) / 128) * p.groups;
     const long long rows = (p.M + TN - 1) / TN;
     const long long nk = static_cast<long long>((p.K + F4_BK - 1) / F4_BK) * p.ksegs;
-    // The widest split whose CTAs all run at once and still have a K block each.  128
-    // tokens, 12288 -> 4608 features (36 tiles): 4 parts 22 us, 3 or 5 parts 25 or 33;
-    // 48 tokens, 12288 -> 12288 (96 tiles): 3 parts 39 us, 2 or 4 parts 43 or 47.
+    // The widest split whose CTAs all run at once and still have a K block each.  Whole calls
+    // of mx (nv up to 4 us more): 128 tokens, 12288 -> 4608 features (36 tiles) 4 parts 14.2 us,
+    // 3 or 5 parts 14.9 or 21.0; 1 token, the same, 8 parts 8.4, 4 parts 7.7, 2 parts 10.2; 48
+    // tokens, 12288 -> 12288 in eight row shards (96 tiles) 3 parts 20.3, 2 or 4 parts 19.3 or
+    // 24.8; 4096 -> 4096 (32 tiles) 8 parts 8.4, 4 parts 7.4.  (More parts than run at once cost up
+    // to half; fewer than this rule's would save up to 12 % of the shortest calls.)
     int splits = static_cast<int>(nk < S_MAX_SPLIT ? nk : S_MAX_SPLIT);
     while (splits > 1 && tiles * rows > clusters[splits]) --splits;
     cudaLaunchConfig_t cfg = {};

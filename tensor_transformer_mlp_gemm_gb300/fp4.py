@@ -241,7 +241,8 @@ class DeviceFp4Linear:
     and quantises them on the way.
 
     x_scale (nvfp4): the activations' scale from a calibration, fp32 [1]; None computes it
-    from each input.  The backward pass needs weights with both forms."""
+    from each input.  (One that a saving forward call took keeps its value until the backward
+    call.)  The backward pass needs weights with both forms."""
 
     def __init__(self, w: LinearWorkload, weights: Fp4Weights, b: torch.Tensor,
                  x_scale: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
